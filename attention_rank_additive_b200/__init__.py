@@ -3,7 +3,8 @@
 Python binding of libflashbias (the C ABI in include/flashbias.h). The
 functions named ``fb_*`` mirror the C entry points one to one and take raw
 integers for pointers; the helpers below them (``attn``, ``attn_dense_bias``,
-``factors_sandwich``, ``factors_alibi``, ``svd_factors``) only marshal torch
+``factors_sandwich``, ``factors_alibi``, ``svd_factors``, and for serving
+``rope``, ``cache_write``, ``cache_read``, ``attn_cache``) only marshal torch
 tensors: every step of the computation runs in the library's kernels.
 
 There is no fallback: importing works without a GPU, but the first call that
@@ -26,11 +27,14 @@ __all__ = [
     "fb_svd_device_workspace_bytes", "fb_svd_factors_device", "svd_factors_device",
     "fb_attn_neural_workspace_bytes", "fb_attn_neural_fwd", "attn_neural",
     "PreparedBias", "attn_dense_bias", "factors_sandwich", "factors_alibi", "svd_factors",
-    "attn_flops",
+    "attn_flops", "FB_E4M3", "fb_rope_fwd", "fb_rope_bwd", "fb_rope_turns_host", "fb_rope_frequencies_host",
+    "fb_cache_write", "fb_cache_read", "fb_cache_bias_bytes", "fb_cache_bias_prepare",
+    "fb_attn_cache_workspace_bytes", "fb_attn_cache_fwd", "Rope", "rope", "rope_bwd", "PagedCache", "cache_write",
+    "cache_read", "CacheBias", "cache_workspace", "attn_cache",
 ]
 
 FB_OK, FB_ERR_INVALID_ARG, FB_ERR_UNSUPPORTED, FB_ERR_RANGE, FB_ERR_WORKSPACE, FB_ERR_CUDA, FB_ERR_TIMEOUT = range(7)
-FB_F32, FB_BF16, FB_F16 = 0, 1, 2
+FB_F32, FB_BF16, FB_F16, FB_E4M3 = 0, 1, 2, 3
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 lib_path = os.path.join(_HERE, "libflashbias.so")
@@ -42,7 +46,9 @@ EXPORTED = (
     "fb_selftest_wait_timeout", "fb_attn_fwd_noalloc", "fb_attn_prepare_factors", "fb_attn_fwd_prepared",
     "fb_attn_mul_bias_workspace_bytes", "fb_attn_mul_bias_fwd", "fb_svd_device_workspace_bytes",
     "fb_svd_factors_device", "fb_attn_neural_workspace_bytes", "fb_attn_neural_fwd", "fb_attn_bwd_workspace_bytes",
-    "fb_attn_bwd", "fb_attn_neural_bwd_workspace_bytes", "fb_attn_neural_bwd",
+    "fb_attn_bwd", "fb_attn_neural_bwd_workspace_bytes", "fb_attn_neural_bwd", "fb_rope_fwd", "fb_rope_bwd",
+    "fb_rope_turns_host", "fb_rope_frequencies_host", "fb_cache_write", "fb_cache_read", "fb_cache_bias_bytes",
+    "fb_cache_bias_prepare", "fb_attn_cache_workspace_bytes", "fb_attn_cache_fwd",
 )
 
 
@@ -109,6 +115,26 @@ def lib() -> ctypes.CDLL:
         L.fb_factors_alibi.argtypes, L.fb_factors_alibi.restype = [i32, i32, vp, vp, vp], i32
         L.fb_svd_factors_host.argtypes = [vp, i32, i32, i32, i32, ctypes.c_uint64, vp, vp, vp, vp]
         L.fb_svd_factors_host.restype = i32
+        rope_args = [i32, i32, i32, i32, i32, i32, vp, f32, vp, i64] + 2 * [i32, vp, i64, i64, i64, vp, i64, i64, i64]
+        L.fb_rope_fwd.argtypes, L.fb_rope_fwd.restype = rope_args + [vp], i32
+        L.fb_rope_bwd.argtypes, L.fb_rope_bwd.restype = rope_args + [vp], i32
+        L.fb_rope_turns_host.argtypes, L.fb_rope_turns_host.restype = [i32, vp, vp], i32
+        f64 = ctypes.c_double
+        L.fb_rope_frequencies_host.argtypes = [i32, f64, i32, f64, f64, f64, f64, vp, vp]
+        L.fb_rope_frequencies_host.restype = i32
+        L.fb_cache_write.argtypes = [i32, i32, i32, i32, i32, i32, vp, i64, i64, i64, vp, i64, i64, i64, vp, vp, vp, vp,
+                                     i32, i32, vp, i32, vp, vp, vp]
+        L.fb_cache_write.restype = i32
+        L.fb_cache_read.argtypes = [i32, i32, i32, i32, i32, i32, vp, vp, vp, vp, i32, i32, vp, i32, vp, vp, vp, vp, vp]
+        L.fb_cache_read.restype = i32
+        L.fb_cache_bias_bytes.argtypes, L.fb_cache_bias_bytes.restype = [i32, i32, i32, i32], sz
+        L.fb_cache_bias_prepare.argtypes = [i32, i32, i32, i32, vp, vp, vp, sz, vp]
+        L.fb_cache_bias_prepare.restype = i32
+        L.fb_attn_cache_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
+        L.fb_attn_cache_workspace_bytes.restype = sz
+        L.fb_attn_cache_fwd.argtypes = [i32, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, i32, i32, vp, i32, vp, vp, vp,
+                                        i32, vp, i32, i32, i32, i32, vp, f32, vp, vp, vp, sz, vp]
+        L.fb_attn_cache_fwd.restype = i32
         L.fb_check_device_error.argtypes, L.fb_check_device_error.restype = [vp], i32
         L.fb_selftest_wait_timeout.argtypes, L.fb_selftest_wait_timeout.restype = [i32, vp], i32
         _lib = L
@@ -336,6 +362,65 @@ def fb_svd_factors_host(bias_host, N, R, oversample, power_iters, seed, phi_q_ho
                                      rel_fro_err, energy)
 
 
+def fb_rope_fwd(dt, B, N, d, rot, interleaved, turns, factor, positions, pos_bstride, Hq, Q, q_bstride, q_hstride,
+                q_nstride, Q_out, qo_bstride, qo_hstride, qo_nstride, Hk, K, k_bstride, k_hstride, k_nstride, K_out,
+                ko_bstride, ko_hstride, ko_nstride, stream) -> int:
+    return lib().fb_rope_fwd(dt, B, N, d, rot, interleaved, turns, factor, positions, pos_bstride, Hq, Q, q_bstride,
+                             q_hstride, q_nstride, Q_out, qo_bstride, qo_hstride, qo_nstride, Hk, K, k_bstride,
+                             k_hstride, k_nstride, K_out, ko_bstride, ko_hstride, ko_nstride, stream)
+
+
+def fb_rope_bwd(dt, B, N, d, rot, interleaved, turns, factor, positions, pos_bstride, Hq, dQ_out, q_bstride, q_hstride,
+                q_nstride, dQ, qo_bstride, qo_hstride, qo_nstride, Hk, dK_out, k_bstride, k_hstride, k_nstride, dK,
+                ko_bstride, ko_hstride, ko_nstride, stream) -> int:
+    return lib().fb_rope_bwd(dt, B, N, d, rot, interleaved, turns, factor, positions, pos_bstride, Hq, dQ_out,
+                             q_bstride, q_hstride, q_nstride, dQ, qo_bstride, qo_hstride, qo_nstride, Hk, dK_out,
+                             k_bstride, k_hstride, k_nstride, dK, ko_bstride, ko_hstride, ko_nstride, stream)
+
+
+def fb_rope_turns_host(pairs, freq_host, turns_host) -> int:
+    return lib().fb_rope_turns_host(pairs, freq_host, turns_host)
+
+
+def fb_rope_frequencies_host(rot, base, scaling, factor, trained, fast, slow, freq_host, out_factor_host) -> int:
+    return lib().fb_rope_frequencies_host(rot, base, scaling, factor, trained, fast, slow, freq_host, out_factor_host)
+
+
+def fb_cache_write(dt, cache_dt, B, H, T, d, K, k_bstride, k_hstride, k_tstride, V, v_bstride, v_hstride, v_tstride,
+                   k_pages, v_pages, k_scale, v_scale, num_pages, page_size, block_table, max_pages, starts, counts,
+                   stream) -> int:
+    return lib().fb_cache_write(dt, cache_dt, B, H, T, d, K, k_bstride, k_hstride, k_tstride, V, v_bstride, v_hstride,
+                                v_tstride, k_pages, v_pages, k_scale, v_scale, num_pages, page_size, block_table,
+                                max_pages, starts, counts, stream)
+
+
+def fb_cache_read(dt, cache_dt, B, H, N, d, k_pages, v_pages, k_scale, v_scale, num_pages, page_size, block_table,
+                  max_pages, starts, counts, K, V, stream) -> int:
+    return lib().fb_cache_read(dt, cache_dt, B, H, N, d, k_pages, v_pages, k_scale, v_scale, num_pages, page_size,
+                               block_table, max_pages, starts, counts, K, V, stream)
+
+
+def fb_cache_bias_bytes(Hq, H, P, R) -> int:
+    return lib().fb_cache_bias_bytes(Hq, H, P, R)
+
+
+def fb_cache_bias_prepare(Hq, H, P, R, phi_q, phi_k, prepared, prepared_bytes, stream) -> int:
+    return lib().fb_cache_bias_prepare(Hq, H, P, R, phi_q, phi_k, prepared, prepared_bytes, stream)
+
+
+def fb_attn_cache_workspace_bytes(B, Hq, H, T, d) -> int:
+    return lib().fb_attn_cache_workspace_bytes(B, Hq, H, T, d)
+
+
+def fb_attn_cache_fwd(cache_dt, B, Hq, H, T, d, Q, k_pages, v_pages, k_scale, v_scale, num_pages, page_size,
+                      block_table, max_pages, prefix, counts, tree_mask, mask_words, depths, R, P, phi_q_heads,
+                      phi_k_heads, prepared_bias, scale, O, LSE, workspace, workspace_bytes, stream) -> int:
+    return lib().fb_attn_cache_fwd(cache_dt, B, Hq, H, T, d, Q, k_pages, v_pages, k_scale, v_scale, num_pages,
+                                   page_size, block_table, max_pages, prefix, counts, tree_mask, mask_words, depths, R,
+                                   P, phi_q_heads, phi_k_heads, prepared_bias, scale, O, LSE, workspace,
+                                   workspace_bytes, stream)
+
+
 def fb_check_device_error(stream) -> int:
     return lib().fb_check_device_error(stream)
 
@@ -536,3 +621,293 @@ def attn_flops(B: int, H: int, N: int, d: int, R: int, causal: bool) -> float:
     """Counted FLOPs: 4 N^2 d + 2 N^2 R per head, halved when causal."""
     f = float(B) * H * (4.0 * N * N * d + 2.0 * N * N * R)
     return f / 2.0 if causal else f
+
+
+# ------------------------------------------------- serving: rotary positions, paged cache, attention over it
+
+def _need(ok, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+class _On:
+    """The tensors' device as the current one while a call launches (nothing to do where it is already)."""
+
+    __slots__ = ("old", "new")
+
+    def __init__(self, device):
+        import torch
+        self.new, self.old = device.index, torch.cuda.current_device()
+
+    def __enter__(self):
+        if self.new != self.old:
+            import torch
+            torch.cuda.set_device(self.new)
+
+    def __exit__(self, *exc):
+        if self.new != self.old:
+            import torch
+            torch.cuda.set_device(self.old)
+
+
+def _ints(t, shape, device, what: str) -> int:
+    """Pointer of a contiguous int32 tensor of this shape on this device (0 for None)."""
+    import torch
+    if t is None:
+        return 0
+    _need(t.dtype == torch.int32 and t.shape == shape and t.device == device and t.is_contiguous(),
+          f"{what}: a contiguous int32 tensor {tuple(shape)} on {device}")
+    return t.data_ptr()
+
+
+class Rope:
+    """Rotary positions: the angle per position of each rotated pair.
+
+    frequencies: rot / 2 numbers; the first rot values of a head turn, pair p
+    being (2p, 2p + 1) when interleaved, else (p, p + rot / 2). factor
+    multiplies the turned values. Rope.scaled makes the usual frequencies."""
+
+    SCALINGS = ("none", "linear", "base", "yarn", "bands")
+
+    def __init__(self, frequencies, interleaved=False, factor=1.0, device="cuda"):
+        import torch
+        pairs = len(frequencies)
+        _need(pairs >= 1, "Rope: at least one pair")
+        freq = (ctypes.c_double * pairs)(*[float(w) for w in frequencies])
+        turns = (ctypes.c_uint64 * pairs)()
+        _check(fb_rope_turns_host(pairs, ctypes.addressof(freq), ctypes.addressof(turns)), "fb_rope_turns_host")
+        self.frequencies = list(freq)
+        self.rot, self.interleaved, self.factor = 2 * pairs, bool(interleaved), float(factor)
+        _need(math.isfinite(self.factor) and self.factor != 0.0, "Rope: factor finite and not 0")
+        # 2^-64 turns as two's complement: torch's uint64 has few operations
+        signed = [t - (1 << 64) if t >> 63 else t for t in turns]
+        self.turns = torch.tensor(signed, dtype=torch.int64, device=device)
+
+    @classmethod
+    def scaled(cls, rot: int, base=10000.0, scaling="none", by=1.0, trained=4096.0, fast=32.0, slow=1.0,
+               interleaved=False, factor=None, device="cuda"):
+        """base^(-2p / rot), for contexts `by` times the trained length (fb_rope_frequencies_host)."""
+        _need(scaling in cls.SCALINGS, f"Rope.scaled: scaling one of {cls.SCALINGS}")
+        freq, out = (ctypes.c_double * max(rot // 2, 1))(), ctypes.c_double()
+        _check(fb_rope_frequencies_host(rot, base, cls.SCALINGS.index(scaling), by, trained, fast, slow,
+                                        ctypes.addressof(freq), ctypes.addressof(out)), "fb_rope_frequencies_host")
+        return cls(freq, interleaved, out.value if factor is None else factor, device)
+
+
+def _rope(call, where, q, k, rope, positions, out):
+    import torch
+    _need(q.dim() == 4 and q.is_cuda and q.stride(3) == 1, f"{where}: q a CUDA tensor [B, H, N, d], d contiguous")
+    B, Hq, N, d = q.shape
+    dev, dt = q.device, _dtype_code(q)
+    _need(rope.turns.device == dev, f"{where}: the Rope is on another device")
+    qo, ko = out if out is not None else (torch.empty_like(q), None if k is None else torch.empty_like(k))
+    _need(qo.shape == q.shape and qo.dtype == q.dtype and qo.device == dev and qo.stride(3) == 1,
+          f"{where}: out like q")
+    if k is None:
+        side_k = (0, 0, 0, 0, 0, 0, 0, 0, 0)
+    else:
+        _need(k.dim() == 4 and k.shape[0] == B and k.shape[2:] == q.shape[2:] and k.dtype == q.dtype
+              and k.device == dev and k.stride(3) == 1, f"{where}: k [B, Hk, N, d] like q")
+        _need(ko.shape == k.shape and ko.dtype == k.dtype and ko.device == dev and ko.stride(3) == 1,
+              f"{where}: out like k")
+        side_k = (k.shape[1], k.data_ptr(), *k.stride()[:3], ko.data_ptr(), *ko.stride()[:3])
+    if out is not None:
+        for t in out:
+            _need(t is None or all(s > 0 or n <= 1 for s, n in zip(t.stride(), t.shape)),
+                  f"{where}: out with places of its own for every value")
+    pos, pos_bs = 0, 0
+    if positions is not None:
+        _need(positions.dtype == torch.int32 and positions.device == dev and positions.shape[-1] == N
+              and (N == 1 or positions.stride(-1) == 1)
+              and (positions.dim() == 1 or (positions.dim() == 2 and positions.shape[0] in (1, B))),
+              f"{where}: positions int32 [N], [1, N] or [B, N] on {dev}, contiguous along N")
+        pos = positions.data_ptr()
+        pos_bs = positions.stride(0) if positions.dim() == 2 and positions.shape[0] == B and B > 1 else 0
+    with _On(dev):
+        _check(call(dt, B, N, d, rope.rot, rope.interleaved, rope.turns.data_ptr(), rope.factor, pos, pos_bs, Hq,
+                    q.data_ptr(), *q.stride()[:3], qo.data_ptr(), *qo.stride()[:3], *side_k, _stream(dev)), where)
+    return qo, ko
+
+
+def rope(q, k, rope, positions=None, out=None):
+    """Queries and keys turned by their positions (fb_rope_fwd); returns (q, k).
+
+    q, k: bf16 or fp32 CUDA [B, H, N, d] in any order of the first three
+    dimensions (d contiguous); k may be None. positions: int32 [N], [1, N] or
+    [B, N], or None for 0 .. N - 1. out: (q, k) to write to, which may be the
+    inputs themselves."""
+    return _rope(lib().fb_rope_fwd, "fb_rope_fwd", q, k, rope, positions, out)
+
+
+def rope_bwd(dq, dk, rope, positions=None, out=None):
+    """Gradients of rope's inputs from those of its outputs (fb_rope_bwd); arguments as for rope."""
+    return _rope(lib().fb_rope_bwd, "fb_rope_bwd", dq, dk, rope, positions, out)
+
+
+class PagedCache:
+    """A paged key/value cache: pools k, v [pages, H, page, d], bf16 or e4m3.
+
+    An e4m3 cache has k_scale, v_scale [pages, H, page] (float8_e8m0fnu or
+    uint8, 2^(byte - 127)). The tensors are used as they are, not copied."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        import torch
+        _need(k.is_cuda and k.dim() == 4 and k.dtype in (torch.bfloat16, torch.float8_e4m3fn) and k.is_contiguous(),
+              "PagedCache: k a contiguous CUDA tensor [pages, H, page, d], bfloat16 or float8_e4m3fn")
+        _need(v.shape == k.shape and v.dtype == k.dtype and v.device == k.device and v.is_contiguous(),
+              "PagedCache: v like k")
+        self.dt = FB_E4M3 if k.dtype == torch.float8_e4m3fn else FB_BF16
+        for s in (k_scale, v_scale):
+            _need((s is None) == (self.dt == FB_BF16), "PagedCache: scales for float8_e4m3fn, none for bfloat16")
+            if s is not None:
+                _need(s.dtype in (torch.float8_e8m0fnu, torch.uint8) and s.shape == k.shape[:3] and s.device == k.device
+                      and s.is_contiguous(), "PagedCache: scales float8_e8m0fnu or uint8 [pages, H, page]")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.device = k.device
+        self.num_pages, self.heads, self.page, self.d = k.shape
+
+    @classmethod
+    def empty(cls, num_pages: int, heads: int, page: int, d: int, dtype=None, device="cuda"):
+        """A cache of its own memory, its contents undefined (dtype: bfloat16, or float8_e4m3fn)."""
+        import torch
+        dtype = torch.bfloat16 if dtype is None else dtype
+        kv = [torch.empty((num_pages, heads, page, d), dtype=dtype, device=device) for _ in range(2)]
+        if dtype != torch.float8_e4m3fn:
+            return cls(*kv)
+        return cls(*kv, *[torch.empty((num_pages, heads, page), dtype=torch.uint8, device=device).view(
+            torch.float8_e8m0fnu) for _ in range(2)])
+
+    def _pointers(self):
+        e4m3 = self.dt == FB_E4M3
+        return (self.k.data_ptr(), self.v.data_ptr(), self.k_scale.data_ptr() if e4m3 else 0,
+                self.v_scale.data_ptr() if e4m3 else 0, self.num_pages, self.page)
+
+    def _table(self, table, B):
+        import torch
+        _need(table.dtype == torch.int32 and table.dim() == 2 and table.shape[0] == B and table.device == self.device
+              and table.is_contiguous(), f"block table: a contiguous int32 tensor [{B}, pages] on {self.device}")
+        return table.data_ptr(), table.shape[1]
+
+
+def cache_write(cache: PagedCache, k, v, table, starts, counts=None):
+    """New keys and values into the cache (fb_cache_write): row n < counts[b] of
+    k, v [B, H, N, d] (bf16 or fp32, any order of the first three dimensions)
+    becomes token starts[b] + n of sequence b. table: int32 [B, max_pages];
+    starts, counts: int32 [B] (counts None: every row)."""
+    _need(k.dim() == 4 and k.device == cache.device and k.stride(3) == 1 and v.shape == k.shape and v.dtype == k.dtype
+          and v.device == k.device and v.stride(3) == 1, f"cache_write: k, v [B, H, N, d] on {cache.device}, d contiguous")
+    B, H, N, d = k.shape
+    _need(H == cache.heads and d == cache.d, f"cache_write: {cache.heads} heads of {cache.d}")
+    tab, width = cache._table(table, B)
+    kp, vp, ks, vs, pages, page = cache._pointers()
+    _need(starts is not None, "cache_write: starts")
+    with _On(cache.device):
+        _check(lib().fb_cache_write(_dtype_code(k), cache.dt, B, H, N, d, k.data_ptr(), *k.stride()[:3], v.data_ptr(),
+                                    *v.stride()[:3], kp, vp, ks, vs, pages, page, tab, width,
+                                    _ints(starts, (B,), cache.device, "starts"),
+                                    _ints(counts, (B,), cache.device, "counts"), _stream(cache.device)),
+               "fb_cache_write")
+
+
+def cache_read(cache: PagedCache, table, starts, counts, tokens: int, dtype=None, out=None):
+    """Tokens starts[b] .. starts[b] + counts[b] - 1 of each sequence as (k, v)
+    [B, H, tokens, d] (fb_cache_read), rows past counts[b] zero; dtype bfloat16
+    (the default) or float32. starts None: from 0; counts None: all tokens."""
+    import torch
+    B, dev = table.shape[0], cache.device
+    tab, width = cache._table(table, B)
+    shape = (B, cache.heads, tokens, cache.d)
+    if out is None:
+        dtype = torch.bfloat16 if dtype is None else dtype
+        k, v = torch.empty(shape, dtype=dtype, device=dev), torch.empty(shape, dtype=dtype, device=dev)
+    else:
+        k, v = out
+        _need(all(t.shape == shape and t.device == dev and t.is_contiguous() and t.dtype == k.dtype for t in (k, v))
+              and dtype in (None, k.dtype), f"cache_read: out two contiguous tensors {shape}")
+    kp, vp, ks, vs, pages, page = cache._pointers()
+    with _On(dev):
+        _check(lib().fb_cache_read(_dtype_code(k), cache.dt, B, cache.heads, tokens, cache.d, kp, vp, ks, vs, pages,
+                                   page, tab, width, _ints(starts, (B,), dev, "starts"),
+                                   _ints(counts, (B,), dev, "counts"), k.data_ptr(), v.data_ptr(), _stream(dev)),
+               "fb_cache_read")
+    return k, v
+
+
+class CacheBias:
+    """Bias factors laid out once for attn_cache (fb_cache_bias_prepare).
+
+    phi_q [Hq, P, R] and phi_k [H, P, R], or [1, P, R] or [P, R] where all heads
+    share them, fp32, over positions 0 .. P - 1. The factors are copied."""
+
+    def __init__(self, phi_q, phi_k):
+        import torch
+        phi_q, phi_k = (x[None] if x.dim() == 2 else x for x in (phi_q, phi_k))
+        for x in (phi_q, phi_k):
+            _need(x.is_cuda and x.dim() == 3 and x.dtype == torch.float32, "CacheBias: fp32 CUDA factors [heads, P, R]")
+        _need(phi_q.shape[1:] == phi_k.shape[1:] and phi_q.device == phi_k.device,
+              "CacheBias: factors of one length, rank and device")
+        phi_q, phi_k = phi_q.contiguous(), phi_k.contiguous()
+        self.device = phi_q.device
+        self.q_heads, self.P, self.R = phi_q.shape
+        self.k_heads = phi_k.shape[0]
+        nb = fb_cache_bias_bytes(self.q_heads, self.k_heads, self.P, self.R)
+        self.prepared = torch.empty(max(nb, 1), device=self.device, dtype=torch.uint8)
+        with _On(self.device):
+            _check(fb_cache_bias_prepare(self.q_heads, self.k_heads, self.P, self.R, phi_q.data_ptr(), phi_k.data_ptr(),
+                                         self.prepared.data_ptr(), nb, _stream(self.device)), "fb_cache_bias_prepare")
+
+
+def cache_workspace(B: int, Hq: int, H: int, T: int, d: int, device="cuda"):
+    """A workspace for attn_cache calls of these sizes (one per call that can run at the same time)."""
+    import torch
+    nb = fb_attn_cache_workspace_bytes(B, Hq, H, T, d)
+    _need(nb > 0, f"cache_workspace: unsupported sizes B={B} Hq={Hq} H={H} T={T} d={d}")
+    return torch.zeros(nb, device=device, dtype=torch.uint8)
+
+
+def attn_cache(q, cache: PagedCache, table, prefix, counts=None, tree_mask=None, depths=None, bias=None, scale=None,
+               workspace=None, out=None, lse=None):
+    """Attention of new tokens over the cache (fb_attn_cache_fwd); returns (O, LSE).
+
+    q: bf16 [B, Hq, T, d] contiguous, T = 1 for a decode step. table: int32
+    [B, max_pages]; prefix: int32 [B], each sequence's context, its new tokens
+    being cache tokens prefix[b] + t; counts: int32 [B], how many of the T it
+    brings (None: T). tree_mask: int32 [B, T, words], bit u of row t set where
+    new token t sees new token u (None: u <= t); depths: int32 [B, T], a new
+    token's position after the prefix (None: t). bias: a CacheBias, or None.
+    workspace: of cache_workspace (None: allocated here, at the cost of a
+    memset)."""
+    import torch
+    dev = cache.device
+    _need(q.dim() == 4 and q.dtype == torch.bfloat16 and q.device == dev and q.is_contiguous(),
+          f"attn_cache: q a contiguous bfloat16 tensor [B, Hq, T, d] on {dev}")
+    B, Hq, T, d = q.shape
+    H = cache.heads
+    _need(d == cache.d, f"attn_cache: head dim {cache.d}")
+    tab, width = cache._table(table, B)
+    words, mask = 0, 0
+    if tree_mask is not None:
+        words = tree_mask.shape[-1]
+        mask = _ints(tree_mask, (B, T, words), dev, "tree_mask")
+    R, P, fq, fk, pb = 0, 0, 0, 0, 0
+    if bias is not None:
+        _need(bias.device == dev, "attn_cache: the bias is on another device")
+        R, P, fq, fk, pb = bias.R, bias.P, bias.q_heads, bias.k_heads, bias.prepared.data_ptr()
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    o = torch.empty_like(q) if out is None else out
+    l = torch.empty((B, Hq, T), device=dev, dtype=torch.float32) if lse is None else lse
+    _need(out is None or (o.shape == q.shape and o.dtype == q.dtype and o.device == dev and o.is_contiguous()),
+          "attn_cache: out like q")
+    _need(lse is None or (l.shape == (B, Hq, T) and l.dtype == torch.float32 and l.device == dev and l.is_contiguous()),
+          "attn_cache: lse a contiguous float32 tensor [B, Hq, T]")
+    kp, vp, ks, vs, pages, page = cache._pointers()
+    with _On(dev):
+        if workspace is None:
+            workspace = torch.zeros(max(fb_attn_cache_workspace_bytes(B, Hq, H, T, d), 1), device=dev, dtype=torch.uint8)
+        _need(workspace.device == dev and workspace.is_contiguous(), "attn_cache: workspace of cache_workspace")
+        _check(lib().fb_attn_cache_fwd(cache.dt, B, Hq, H, T, d, q.data_ptr(), kp, vp, ks, vs, pages, page, tab, width,
+                                       _ints(prefix, (B,), dev, "prefix"), _ints(counts, (B,), dev, "counts"), mask,
+                                       words, _ints(depths, (B, T), dev, "depths"), R, P, fq, fk, pb, scale,
+                                       o.data_ptr(), l.data_ptr(), workspace.data_ptr(),
+                                       workspace.numel() * workspace.element_size(), _stream(dev)), "fb_attn_cache_fwd")
+    return o, l

@@ -1,0 +1,271 @@
+// fb_cache.cu -- the paged key/value cache: new rows quantised as they are
+// written, and rows read back.
+//
+// A cache is two pools of pages, [pages, heads, page, d], of bf16 or of e4m3
+// codes; an e4m3 row carries a power-of-two scale in one byte (E8M0),
+//   x ~ code 2^(s - 127),  s - 127 = ceil(log2(amax |x| / 448)), at least -126.
+// A power of two makes the division exact, so the one rounding is the code's
+// (relative 2^-4, RN), two implementations agree to the bit, and a value read
+// back has four significant bits and is exact in bf16.
+//
+// What bounds both kernels: HBM. Each row is read once and written once. A row
+// is the work of d / 8 neighbouring lanes (16 bytes of bf16 each), rounded up to
+// a power of two so that the row's maximum is a shuffle reduction; consecutive
+// groups of lanes take consecutive tokens of one head, which are neighbours in
+// a page, so a warp's stores form whole lines.
+#include <cuda_fp8.h>
+
+#include "fb_internal.h"
+#include "fb_ptx.cuh"
+
+namespace fb {
+namespace {
+
+struct CacheArgs {
+  const void *src[2];  // write: new K, V (element strides below); read: the pools
+  void *dst[2];        // write: the pools; read: K, V [B, H, N, d]
+  uint8_t *scale[2];
+  long long xb, xh, xn, yb, yh, yn;  // write: strides of new K and new V
+  int B, H, N, d, page, shift;       // N: tokens a sequence at most; page = 1 << shift
+  int num_pages, max_pages;
+  const int *table, *starts, *counts;
+  int lanes, lanes_shift;  // lanes of a row, a power of two
+  int *flags;
+};
+
+__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float *x) {
+  const uint4 u = *reinterpret_cast<const uint4 *>(p);
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void load8(const float *p, float *x) {
+  const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
+  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+}
+__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float *x) {
+  *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+                                             pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+}
+__device__ __forceinline__ void store8(float *p, const float *x) {
+  *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
+  *reinterpret_cast<float4 *>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+}
+
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+}
+
+// Row of token (b, position) in head h of the pools, or -1 (flagged) where the
+// block table does not lead to a page.
+__device__ __forceinline__ long long pool_row(const CacheArgs &a, int b, int h, long long pos) {
+  const long long i = pos >> a.shift;
+  int page = -1;
+  if (pos >= 0 && i < a.max_pages) page = a.table[(long long)b * a.max_pages + i];
+  if (page < 0 || page >= a.num_pages) {
+    atomicOr(a.flags, kFlagRange);
+    return -1;
+  }
+  return ((long long)page * a.H + h) * a.page + (pos & (a.page - 1));
+}
+
+// Which row this thread's group of lanes works on: h fastest above tokens.
+struct Row {
+  int b, h, n, lane;
+  bool ok;
+};
+__device__ __forceinline__ Row row_of(const CacheArgs &a) {
+  const long long id = blockIdx.x * (long long)blockDim.x + threadIdx.x;
+  const long long row = id >> a.lanes_shift;
+  Row r;
+  r.lane = int(id & (a.lanes - 1));
+  r.ok = row < (long long)a.B * a.H * a.N;
+  r.n = int(row % a.N);
+  const long long bh = row / a.N;
+  r.h = int(bh % a.H);
+  r.b = int(bh / a.H);
+  return r;
+}
+
+template <typename T, bool E4M3>
+__global__ void __launch_bounds__(256) cache_write_kernel(const CacheArgs a) {
+  const Row r = row_of(a);
+  griddep_wait();
+  bool live = r.ok && r.n < (a.counts ? a.counts[r.b] : a.N);
+  long long row = -1;
+  if (live) row = pool_row(a, r.b, r.h, (long long)a.starts[r.b] + r.n);
+  live = row >= 0 && r.lane * 8 < a.d;
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    float x[8];
+    if (live) {
+      const long long at = w ? r.b * a.yb + r.h * a.yh + r.n * a.yn : r.b * a.xb + r.h * a.xh + r.n * a.xn;
+      load8(static_cast<const T *>(a.src[w]) + at + r.lane * 8, x);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = 0.f;
+    }
+    if constexpr (!E4M3) {
+      if (live) store8(static_cast<__nv_bfloat16 *>(a.dst[w]) + row * a.d + r.lane * 8, x);
+    } else {
+      // the row's largest finite magnitude
+      float top = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float m = fabsf(x[i]);
+        top = fmaxf(top, m < INFINITY ? m : 0.f);
+      }
+      for (int o = a.lanes >> 1; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      // top = 1.m 2^(f - 127); the scale's exponent is f - 127 - 8, one more where 1.m > 1.75 (448 = 1.75 2^8)
+      const uint32_t bits = __float_as_uint(top);
+      int e = int(bits >> 23) - 135 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
+      e = max(e, -126);
+      const float inv = __uint_as_float(uint32_t(127 - e) << 23);
+      if (live) {
+        const uint32_t lo = e4m3x2(x[0] * inv, x[1] * inv) | (e4m3x2(x[2] * inv, x[3] * inv) << 16);
+        const uint32_t hi = e4m3x2(x[4] * inv, x[5] * inv) | (e4m3x2(x[6] * inv, x[7] * inv) << 16);
+        *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(a.dst[w]) + row * a.d + r.lane * 8) = make_uint2(lo, hi);
+        if (r.lane == 0) a.scale[w][row] = uint8_t(e + 127);
+      }
+    }
+  }
+}
+
+template <typename T, bool E4M3>
+__global__ void __launch_bounds__(256) cache_read_kernel(const CacheArgs a) {
+  const Row r = row_of(a);
+  griddep_wait();
+  if (!r.ok || r.lane * 8 >= a.d) return;
+  long long row = -1;
+  if (r.n < (a.counts ? a.counts[r.b] : a.N))
+    row = pool_row(a, r.b, r.h, (long long)(a.starts ? a.starts[r.b] : 0) + r.n);
+  const long long out = (((long long)r.b * a.H + r.h) * a.N + r.n) * a.d + r.lane * 8;
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = 0.f;
+    if (row >= 0) {
+      if constexpr (E4M3) {
+        const uint2 u = *reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(a.src[w]) + row * a.d + r.lane * 8);
+        // 2^(s - 127); s = 0 is 2^-127, a subnormal
+        const uint32_t s = a.scale[w][row];
+        const float scale = __uint_as_float(s ? s << 23 : 0x400000u);
+        const uint32_t v[2] = {u.x, u.y};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(v[i / 2] >> (16 * (i % 2))), __NV_E4M3);
+          const float2 f = __half22float2(__half2(h));
+          x[2 * i] = f.x * scale;
+          x[2 * i + 1] = f.y * scale;
+        }
+      } else {
+        load8(static_cast<const __nv_bfloat16 *>(a.src[w]) + row * a.d + r.lane * 8, x);
+      }
+    }
+    store8(static_cast<T *>(a.dst[w]) + out, x);
+  }
+}
+
+int cache_status(int cache_dt, int B, int H, int N, int d, int num_pages, int page_size, int max_pages,
+                 const void *k_pages, const void *v_pages, const void *k_scale, const void *v_scale,
+                 const int32_t *table) {
+  if (cache_dt != FB_BF16 && cache_dt != FB_E4M3) return FB_ERR_UNSUPPORTED;
+  if (B < 1 || H < 1 || N < 1 || num_pages < 1 || max_pages < 1) return FB_ERR_INVALID_ARG;
+  if (!cache_dims_ok(d, page_size)) return FB_ERR_UNSUPPORTED;
+  if (!k_pages || !v_pages || !table || (cache_dt == FB_E4M3 && (!k_scale || !v_scale))) return FB_ERR_INVALID_ARG;
+  if (((reinterpret_cast<uintptr_t>(k_pages) | reinterpret_cast<uintptr_t>(v_pages)) & 15u) != 0 ||
+      (reinterpret_cast<uintptr_t>(table) & 3u) != 0)
+    return FB_ERR_INVALID_ARG;
+  return FB_OK;
+}
+
+cudaError_t launch_rows(void (*k)(const CacheArgs), CacheArgs &a, cudaStream_t st) {
+  a.shift = 0;
+  while ((1 << a.shift) < a.page) ++a.shift;
+  a.lanes = 1, a.lanes_shift = 0;
+  while (a.lanes * 8 < a.d) a.lanes *= 2, ++a.lanes_shift;
+  const long long threads = (long long)a.B * a.H * a.N * a.lanes;
+  const long long blocks = (threads + 255) / 256;
+  if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
+  return launch_programmatic(k, dim3(unsigned(blocks)), dim3(256), 0, st, a);
+}
+
+int status_of(cudaError_t e) {
+  return e == cudaSuccess ? FB_OK : (e == cudaErrorInvalidValue ? FB_ERR_UNSUPPORTED : FB_ERR_CUDA);
+}
+
+}  // namespace
+
+bool cache_dims_ok(int d, int page_size) {
+  if (d < 16 || d > 128 || d % 16 != 0) return false;
+  return page_size == 16 || page_size == 32 || page_size == 64 || page_size == 128 || page_size == 256;
+}
+
+}  // namespace fb
+
+using namespace fb;
+
+extern "C" {
+
+int fb_cache_write(int dt, int cache_dt, int B, int H, int T, int d, const void *K, int64_t k_bstride,
+                   int64_t k_hstride, int64_t k_tstride, const void *V, int64_t v_bstride, int64_t v_hstride,
+                   int64_t v_tstride, void *k_pages, void *v_pages, uint8_t *k_scale, uint8_t *v_scale, int num_pages,
+                   int page_size, const int32_t *block_table, int max_pages, const int32_t *starts,
+                   const int32_t *counts, void *stream) {
+  if (dt != FB_BF16 && dt != FB_F32) return FB_ERR_UNSUPPORTED;
+  if (const int s = cache_status(cache_dt, B, H, T, d, num_pages, page_size, max_pages, k_pages, v_pages, k_scale,
+                                 v_scale, block_table))
+    return s;
+  if (!K || !V || !starts) return FB_ERR_INVALID_ARG;
+  const int64_t strides[6] = {k_bstride, k_hstride, k_tstride, v_bstride, v_hstride, v_tstride};
+  const int vec = dt == FB_BF16 ? 8 : 4;  // 16-byte loads
+  for (int64_t s : strides) {
+    if (s < 0) return FB_ERR_INVALID_ARG;
+    if (s % vec != 0) return FB_ERR_UNSUPPORTED;
+  }
+  if (((reinterpret_cast<uintptr_t>(K) | reinterpret_cast<uintptr_t>(V)) & 15u) != 0 ||
+      ((reinterpret_cast<uintptr_t>(starts) | reinterpret_cast<uintptr_t>(counts)) & 3u) != 0)
+    return FB_ERR_INVALID_ARG;
+  int *flags = device_flags();
+  if (!flags) return FB_ERR_CUDA;
+  CacheArgs a{};
+  a.src[0] = K, a.src[1] = V, a.dst[0] = k_pages, a.dst[1] = v_pages, a.scale[0] = k_scale, a.scale[1] = v_scale;
+  a.xb = k_bstride, a.xh = k_hstride, a.xn = k_tstride, a.yb = v_bstride, a.yh = v_hstride, a.yn = v_tstride;
+  a.B = B, a.H = H, a.N = T, a.d = d, a.page = page_size, a.num_pages = num_pages, a.max_pages = max_pages;
+  a.table = block_table, a.starts = starts, a.counts = counts, a.flags = flags;
+  void (*k)(const CacheArgs) =
+      dt == FB_BF16 ? (cache_dt == FB_E4M3 ? cache_write_kernel<__nv_bfloat16, true> : cache_write_kernel<__nv_bfloat16, false>)
+                    : (cache_dt == FB_E4M3 ? cache_write_kernel<float, true> : cache_write_kernel<float, false>);
+  return status_of(launch_rows(k, a, static_cast<cudaStream_t>(stream)));
+}
+
+int fb_cache_read(int dt, int cache_dt, int B, int H, int N, int d, const void *k_pages, const void *v_pages,
+                  const uint8_t *k_scale, const uint8_t *v_scale, int num_pages, int page_size,
+                  const int32_t *block_table, int max_pages, const int32_t *starts, const int32_t *counts, void *K,
+                  void *V, void *stream) {
+  if (dt != FB_BF16 && dt != FB_F32) return FB_ERR_UNSUPPORTED;
+  if (const int s = cache_status(cache_dt, B, H, N, d, num_pages, page_size, max_pages, k_pages, v_pages, k_scale,
+                                 v_scale, block_table))
+    return s;
+  if (!K || !V) return FB_ERR_INVALID_ARG;
+  if (((reinterpret_cast<uintptr_t>(K) | reinterpret_cast<uintptr_t>(V)) & 15u) != 0 ||
+      ((reinterpret_cast<uintptr_t>(starts) | reinterpret_cast<uintptr_t>(counts)) & 3u) != 0)
+    return FB_ERR_INVALID_ARG;
+  int *flags = device_flags();
+  if (!flags) return FB_ERR_CUDA;
+  CacheArgs a{};
+  a.src[0] = k_pages, a.src[1] = v_pages, a.dst[0] = K, a.dst[1] = V;
+  a.scale[0] = const_cast<uint8_t *>(k_scale), a.scale[1] = const_cast<uint8_t *>(v_scale);
+  a.B = B, a.H = H, a.N = N, a.d = d, a.page = page_size, a.num_pages = num_pages, a.max_pages = max_pages;
+  a.table = block_table, a.starts = starts, a.counts = counts, a.flags = flags;
+  void (*k)(const CacheArgs) =
+      dt == FB_BF16 ? (cache_dt == FB_E4M3 ? cache_read_kernel<__nv_bfloat16, true> : cache_read_kernel<__nv_bfloat16, false>)
+                    : (cache_dt == FB_E4M3 ? cache_read_kernel<float, true> : cache_read_kernel<float, false>);
+  return status_of(launch_rows(k, a, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -183,6 +183,9 @@ cudaError_t launch_programmatic(void (*kern)(KArgs...), dim3 grid, dim3 block, s
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+// Whether the cache's kernels take this head dim and page size.
+bool cache_dims_ok(int d, int page_size);
+
 // Per-device flag word (allocated once per device as a module global).
 int *device_flags();
 

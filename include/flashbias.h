@@ -55,8 +55,12 @@ typedef enum {
 } fb_status;
 
 /* Element type of Q, K, V, O (and of a dense bias). fp16 inputs are not
- * implemented: every entry point returns FB_ERR_UNSUPPORTED for FB_F16. */
-typedef enum { FB_F32 = 0, FB_BF16 = 1, FB_F16 = 2 } fb_dtype;
+ * implemented: every entry point returns FB_ERR_UNSUPPORTED for FB_F16.
+ * FB_E4M3 is a type of the key/value cache only. */
+typedef enum { FB_F32 = 0, FB_BF16 = 1, FB_F16 = 2, FB_E4M3 = 3 } fb_dtype;
+
+/* Frequencies of rotary positions (fb_rope_frequencies_host). */
+typedef enum { FB_ROPE_PLAIN = 0, FB_ROPE_LINEAR = 1, FB_ROPE_BASE = 2, FB_ROPE_YARN = 3, FB_ROPE_BANDS = 4 } fb_rope_scaling;
 
 /* Human-readable name of a status code (static string, never NULL). */
 const char *fb_status_str(int status);
@@ -421,9 +425,172 @@ int fb_svd_factors_host(const double *bias_host, int N, int R, int oversample,
                         float *phi_k_host, double *rel_fro_err, double *energy);
 
 /*
+ * Rotary positions. (The FlashBias paper has no counterpart; a model with
+ * rotary positions turns q and k before fb_attn_fwd and its cache holds turned
+ * keys.) Pair p of a token at position n turns by the angle n w_p:
+ *
+ *   y_a = f (x_a cos - x_b sin),  y_b = f (x_a sin + x_b cos),
+ *
+ * (a, b) = (2p, 2p + 1) when `interleaved`, else (p, p + rot / 2); values past
+ * the first `rot` of a head are copied, without f. fb_rope_bwd gives the
+ * gradients of x from those of y: the turn by the opposite angle, times f.
+ *
+ *  dt          FB_BF16 or FB_F32 (of q, k and the outputs). Angles, sines and
+ *              products are fp32 or better; one rounding at the end.
+ *  d, rot      head dim (1 to 4096) and rotated part, rot even, 2 <= rot <= d.
+ *  turns       [rot / 2] device: fb_rope_turns_host's form of the w_p.
+ *  factor      f, finite and not 0.
+ *  positions   int32 device, token n of batch b at b*pos_bstride + n (any value,
+ *              negative ones too), or NULL: token n is at position n.
+ *  Q, K        element (b, h, n, c) at b*bstride + h*hstride + n*nstride + c,
+ *              strides in elements and not negative; aligned to the element.
+ *              The outputs have strides of their own. An output may be its own
+ *              input (same pointer and strides), and otherwise overlaps nothing.
+ *              Hk = 0: Q alone. The widest loads need 16-byte aligned pointers
+ *              and strides that are multiples of 16 bytes.
+ */
+int fb_rope_fwd(int dt, int B, int N, int d, int rot, int interleaved,
+                const uint64_t *turns, float factor,
+                const int32_t *positions, int64_t pos_bstride,
+                int Hq, const void *Q, int64_t q_bstride, int64_t q_hstride, int64_t q_nstride,
+                void *Q_out, int64_t qo_bstride, int64_t qo_hstride, int64_t qo_nstride,
+                int Hk, const void *K, int64_t k_bstride, int64_t k_hstride, int64_t k_nstride,
+                void *K_out, int64_t ko_bstride, int64_t ko_hstride, int64_t ko_nstride,
+                void *stream);
+
+int fb_rope_bwd(int dt, int B, int N, int d, int rot, int interleaved,
+                const uint64_t *turns, float factor,
+                const int32_t *positions, int64_t pos_bstride,
+                int Hq, const void *dQ_out, int64_t q_bstride, int64_t q_hstride, int64_t q_nstride,
+                void *dQ, int64_t qo_bstride, int64_t qo_hstride, int64_t qo_nstride,
+                int Hk, const void *dK_out, int64_t k_bstride, int64_t k_hstride, int64_t k_nstride,
+                void *dK, int64_t ko_bstride, int64_t ko_hstride, int64_t ko_nstride,
+                void *stream);
+
+/* turns_host[p] = the fraction of a turn that pair p passes per position, in
+ * units of 2^-64 turns (w_p modulo a turn; exact to 2^-53 of w_p). */
+int fb_rope_turns_host(int pairs, const double *freq_host, uint64_t *turns_host);
+
+/*
+ * Frequencies of the rot / 2 pairs, w_p = base^(-2p / rot), scaled for contexts
+ * `factor` times as long as the `trained` length:
+ *   FB_ROPE_PLAIN   as they are.
+ *   FB_ROPE_LINEAR  w_p / factor.
+ *   FB_ROPE_BASE    base * factor^(rot / (rot - 2)) in place of base (rot >= 4).
+ *   FB_ROPE_YARN    pairs that make more than `fast` turns over the trained
+ *                   length stay, those below `slow` are divided by factor, the
+ *                   pair numbers between are ramped; *out_factor_host = 0.1 ln(factor) + 1.
+ *   FB_ROPE_BANDS   the same, ramped over the number of turns; out factor 1.
+ * factor >= 1; trained, fast > slow > 0 are read by the last two only.
+ */
+int fb_rope_frequencies_host(int rot, double base, int scaling, double factor,
+                             double trained, double fast, double slow,
+                             double *freq_host, double *out_factor_host);
+
+/*
+ * The paged key/value cache. (No counterpart in the FlashBias paper: the
+ * serving form of its language-model case.) Two pools of pages,
+ * [num_pages, H, page_size, d] contiguous, bf16 or e4m3; an e4m3 row has a
+ * power-of-two scale in one byte (E8M0: 2^(byte - 127)) in [num_pages, H, page_size].
+ * Token i of sequence b is row i % page_size of page block_table[b][i / page_size].
+ *
+ *  cache_dt    FB_BF16 or FB_E4M3 (scales may be NULL for FB_BF16).
+ *  d           16 to 128, a multiple of 16. page_size 16, 32, 64, 128 or 256.
+ *  pools       16-byte aligned.
+ *  block_table [B, max_pages] int32 device.
+ *  starts      [B] int32 device; counts [B] int32 device or NULL (all).
+ *
+ * fb_cache_write: rows n < counts[b] of new K, V (element (b, h, n, c) at
+ *   b*bstride + h*hstride + n*tstride + c, dt FB_BF16 or FB_F32, 16-byte
+ *   aligned, strides multiples of 16 bytes) go to tokens starts[b] + n. To
+ *   e4m3: the scale is the least power of two, 2^-126 or more, under which the
+ *   row's largest finite value is at most 448; values round to nearest even,
+ *   infinities become 448 times the scale, NaN stays. Other rows are left as
+ *   they were. Two rows of a call must not go to one place.
+ * fb_cache_read: tokens starts[b] + n (starts NULL: n) for n < counts[b] as
+ *   K, V [B, H, N, d] of dt FB_BF16 or FB_F32 (16-byte aligned); rows from
+ *   counts[b] on are 0. Exact, but for values beyond bf16's or fp32's range.
+ * A token that the table does not lead to (past max_pages, a page number
+ * outside the pool, a negative position) is skipped (read as 0) and flags
+ * FB_ERR_RANGE for fb_check_device_error().
+ */
+int fb_cache_write(int dt, int cache_dt, int B, int H, int T, int d,
+                   const void *K, int64_t k_bstride, int64_t k_hstride, int64_t k_tstride,
+                   const void *V, int64_t v_bstride, int64_t v_hstride, int64_t v_tstride,
+                   void *k_pages, void *v_pages, uint8_t *k_scale, uint8_t *v_scale,
+                   int num_pages, int page_size, const int32_t *block_table, int max_pages,
+                   const int32_t *starts, const int32_t *counts, void *stream);
+
+int fb_cache_read(int dt, int cache_dt, int B, int H, int N, int d,
+                  const void *k_pages, const void *v_pages, const uint8_t *k_scale, const uint8_t *v_scale,
+                  int num_pages, int page_size, const int32_t *block_table, int max_pages,
+                  const int32_t *starts, const int32_t *counts, void *K, void *V, void *stream);
+
+/*
+ * Bias factors laid out once for fb_attn_cache_fwd: phi_q [Hq, P, R], phi_k
+ * [H, P, R] fp32 device contiguous, over positions 0 .. P - 1 (Hq or H 1: shared
+ * by all heads). R <= 4: kept in fp32. 5 <= R <= 128: two fp16 parts (22 bits),
+ * each column balanced between q and k by a power of two; a column whose bias
+ * passes 2^30 saturates and flags FB_ERR_RANGE. `prepared`: at least
+ * fb_cache_bias_bytes(...) bytes, 256-byte aligned, written on `stream`; the
+ * factors may be freed or changed once that work has run.
+ */
+size_t fb_cache_bias_bytes(int Hq, int H, int P, int R);
+
+int fb_cache_bias_prepare(int Hq, int H, int P, int R, const float *phi_q, const float *phi_k,
+                          void *prepared, size_t prepared_bytes, void *stream);
+
+/*
+ * Attention of new tokens over the cache, with a low-rank additive bias:
+ *
+ *   O_t = sum_j p_tj v_j,  p = softmax_j(scale q_t.k_j + phi_q[pos t].phi_k[pos j]),
+ *   LSE_t = ln sum_j exp(...)
+ *
+ * Sequence b has prefix[b] tokens of context at cache tokens 0 .. prefix[b] - 1
+ * and counts[b] <= T new ones at prefix[b] + u, already written to the cache.
+ * New token t sees the context and the new tokens u < counts[b] whose bit
+ * u % 32 of word u / 32 of tree_mask[b][t] is set, or u <= t without a mask
+ * (T = 1: the decode step of one token). Its position is prefix[b] +
+ * depths[b][t], or prefix[b] + t without depths; a context token's is its index.
+ *
+ *  Q, O        [B, Hq, T, d] bf16, contiguous, 16-byte aligned. Query head h
+ *              reads key/value head h / (Hq / H); Hq a multiple of H.
+ *  cache       as above; d 16 to 128, a multiple of 16.
+ *  prefix      [B] int32 device; counts [B] int32 device or NULL (T each).
+ *  tree_mask   [B, T, mask_words] device, 32 mask_words >= T, or NULL.
+ *  depths      [B, T] int32 device, or NULL.
+ *  R, P, heads, prepared_bias   as given to fb_cache_bias_prepare, whose output
+ *              this is (the heads 1 or Hq, 1 or H); R = 0: no bias. A position
+ *              outside 0 .. P - 1 is moved to its end and flags FB_ERR_RANGE.
+ *  LSE         [B, Hq, T] fp32 device.
+ *  workspace   fb_attn_cache_workspace_bytes(...) bytes, 256-byte aligned, zero
+ *              before its first use (every call leaves the counters in it at
+ *              zero). It does not grow with B or the contexts. Calls that can
+ *              run at the same time need one each.
+ * A row that sees no key, and rows t >= counts[b], give O = 0 and LSE = -inf.
+ * Values in cache rows that a query row does not see (infinities and NaN too)
+ * do not reach it. Cache rows that the table does not lead to are not seen and
+ * flag FB_ERR_RANGE.
+ * Arithmetic: products of bf16 queries with bf16 or e4m3 keys are exact, sums
+ * and the softmax are fp32; the probabilities are rounded once, to bf16 (bf16
+ * cache) or fp16 (e4m3), for the product with V. Bitwise reproducible.
+ */
+size_t fb_attn_cache_workspace_bytes(int B, int Hq, int H, int T, int d);
+
+int fb_attn_cache_fwd(int cache_dt, int B, int Hq, int H, int T, int d, const void *Q,
+                      const void *k_pages, const void *v_pages, const uint8_t *k_scale, const uint8_t *v_scale,
+                      int num_pages, int page_size, const int32_t *block_table, int max_pages,
+                      const int32_t *prefix, const int32_t *counts,
+                      const uint32_t *tree_mask, int mask_words, const int32_t *depths,
+                      int R, int P, int phi_q_heads, int phi_k_heads, const void *prepared_bias,
+                      float scale, void *O, float *LSE,
+                      void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * Synchronises `stream`, then reads and clears the library's device flag:
  * FB_ERR_TIMEOUT if a kernel's bounded wait ran out, FB_ERR_RANGE if a factor
- * overflowed fp16 in the preparation step, FB_OK otherwise (FB_ERR_CUDA if
+ * overflowed fp16 in the preparation step or a cache call met a token, length
+ * or position outside its table, FB_OK otherwise (FB_ERR_CUDA if
  * the synchronisation itself failed). The flag is per device and shared by
  * all calls on that device.
  */

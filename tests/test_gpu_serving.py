@@ -1,0 +1,518 @@
+"""GPU parity of the serving operators (rotary positions and their gradient, the
+paged cache written and read, attention of new tokens over it) against plain
+64-bit implementations, at the sizes, strides and masks where they can go wrong."""
+import math
+import random
+
+import pytest
+
+import serving_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+import attention_rank_additive_b200 as fb  # noqa: E402
+
+F64 = torch.float64
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    from attention_rank_additive_b200 import build
+    build.build()
+    fb.lib()
+    yield
+    torch.cuda.synchronize()
+
+
+def _status():
+    return fb.fb_check_device_error(torch.cuda.current_stream().cuda_stream)
+
+
+def _randn(shape, seed, dtype=torch.float32):
+    return torch.randn(shape, generator=torch.Generator().manual_seed(seed)).to(dtype)
+
+
+# ------------------------------------------------------------------- rotary
+
+def _strided(shape, layout, seed, dtype):
+    """[B, H, N, d] on the GPU: contiguous, token-major, or a slice of a wider row at an odd offset."""
+    B, H, N, d = shape
+    if layout == "bhnd":
+        return _randn(shape, seed, dtype).cuda()
+    if layout == "bnhd":
+        return _randn((B, N, H, d), seed, dtype).cuda().transpose(1, 2)
+    wide = _randn((B, N, H, d + 7), seed, dtype).cuda()
+    return wide[..., 3:3 + d].transpose(1, 2)
+
+
+ROPE = [  # dtype, B, Hq, Hk, N, d, rot, interleaved, layout, first position
+    (torch.bfloat16, 1, 1, 1, 1, 64, 64, False, "bhnd", 0),
+    (torch.bfloat16, 2, 12, 12, 1, 64, 64, False, "bnhd", 2047),
+    (torch.bfloat16, 3, 4, 2, 37, 128, 64, True, "bnhd", 999983),
+    (torch.bfloat16, 2, 6, 1, 130, 80, 20, False, "bhnd", 7),
+    (torch.bfloat16, 1, 3, 3, 5, 96, 24, True, "odd", 100000),
+    (torch.float32, 2, 5, 5, 33, 48, 48, True, "bhnd", 0),
+    (torch.float32, 1, 8, 2, 700, 128, 32, False, "bnhd", 524288),
+    (torch.float32, 2, 3, 2, 9, 33, 22, False, "odd", 12),
+    (torch.bfloat16, 1, 2, 2, 3, 2, 2, True, "bhnd", 2 ** 31 - 60),
+    (torch.bfloat16, 1, 40, 8, 2500, 128, 128, False, "bnhd", 31),
+]
+
+
+def _rope_tol(y, x, dtype, factor):
+    """One rounding of the result; angle, sine, cosine and products within 2^-21 of the pair's size."""
+    size = x.abs().to(F64).amax(-1, keepdim=True) * abs(factor)
+    return torch.finfo(dtype).eps / 2 * y.abs() + 2.0 ** -21 * 2 * size + 1e-40
+
+
+@pytest.mark.parametrize("dtype,B,Hq,Hk,N,d,rot,inter,layout,first", ROPE)
+def test_rope_and_gradient_match_reference(dtype, B, Hq, Hk, N, d, rot, inter, layout, first):
+    r = fb.Rope.scaled(rot, scaling="yarn" if rot > 2 else "none", by=16.0, interleaved=inter)
+    q, k = _strided((B, Hq, N, d), layout, 1, dtype), _strided((B, Hk, N, d), layout, 2, dtype)
+    pos = (torch.arange(N)[None] + first + torch.arange(B)[:, None] * 3).to(torch.int32)
+    for call, sign in ((fb.rope, 1.0), (fb.rope_bwd, -1.0)):
+        out = call(q, k, r, pos.cuda())
+        torch.cuda.synchronize()
+        for x, y in zip((q, k), out):
+            assert y.shape == x.shape and y.dtype == dtype
+            want = ref.rope(x.cpu(), r.frequencies, pos, rot, inter, r.factor, sign)
+            err = (y.cpu().to(F64) - want).abs()
+            tol = _rope_tol(want, x.cpu(), dtype, r.factor)
+            assert (err <= tol).all(), (err / tol).max()
+            if rot < d:
+                assert torch.equal(y[..., rot:], x[..., rot:])
+    assert _status() == fb.FB_OK
+
+
+def test_rope_gradient_is_the_adjoint_and_the_difference():
+    """rope is linear in x: <rope(x), g> = <x, rope_bwd(g)>, and its difference along any direction is rope of it."""
+    r = fb.Rope.scaled(40, interleaved=False, factor=1.25)
+    x, g, h = (_randn((2, 3, 50, 64), s).cuda() for s in (1, 2, 3))
+    pos = torch.arange(50, dtype=torch.int32, device="cuda") * 17
+    y, _ = fb.rope(x, None, r, pos)
+    dx, _ = fb.rope_bwd(g, None, r, pos)
+    a, b = (y.double() * g.double()).sum(), (x.double() * dx.double()).sum()
+    assert abs(a - b) <= 2.0 ** -20 * (y.double().abs() * g.double().abs()).sum()
+    step = 0.5
+    y2, _ = fb.rope(x + step * h, None, r, pos)
+    dirs = ((y2.double() - y.double()) * g.double()).sum() / step
+    want = (h.double() * dx.double()).sum()
+    assert abs(dirs - want) <= 2.0 ** -18 * ((y2.double().abs() + y.double().abs()) * g.double().abs()).sum() / step
+
+
+def test_rope_in_place_default_positions_and_shared_ones():
+    r = fb.Rope.scaled(32)
+    q, k = _randn((3, 4, 9, 64), 1, torch.bfloat16).cuda(), _randn((3, 2, 9, 64), 2, torch.bfloat16).cuda()
+    want = fb.rope(q, k, r)
+    pos = torch.arange(9, dtype=torch.int32, device="cuda")
+    for p in (pos, pos[None], pos[None].repeat(3, 1), pos[None].expand(3, 9)):
+        assert all(torch.equal(a, b) for a, b in zip(want, fb.rope(q, k, r, p)))
+    q2, k2 = q.clone(), k.clone()
+    got = fb.rope(q2, k2, r, pos, out=(q2, k2))
+    assert got[0] is q2 and all(torch.equal(a, b) for a, b in zip(want, got))
+    # a prompt turned in one call and token by token agree to the bit
+    for n in range(9):
+        one = fb.rope(q[:, :, n:n + 1], k[:, :, n:n + 1], r, pos[n:n + 1])
+        assert all(torch.equal(a[:, :, n:n + 1], b) for a, b in zip(want, one))
+
+
+# -------------------------------------------------------------------- cache
+
+def _cache(pages, H, page, d, kind, seed):
+    k, v = _randn((pages, H, page, d), seed), _randn((pages, H, page, d), seed + 1)
+    if kind == "bf16":
+        return fb.PagedCache(k.to(torch.bfloat16).cuda(), v.to(torch.bfloat16).cuda())
+    (kc, ks), (vc, vs) = ref.quantise(k), ref.quantise(v * torch.exp2(_randn((pages, H, page, 1), seed + 2).round()))
+    return fb.PagedCache(kc.view(torch.float8_e4m3fn).cuda(), vc.view(torch.float8_e4m3fn).cuda(),
+                         ks.cuda(), vs.cuda())
+
+
+def _table(B, per, total, seed):
+    rng = random.Random(seed)
+    order = list(range(total))
+    rng.shuffle(order)
+    return torch.tensor(order[:B * per], dtype=torch.int32).view(B, per)
+
+
+def _bytes(t):
+    return t.view(torch.uint8 if t.element_size() == 1 else torch.int16)
+
+
+CACHE = [  # cache, dtype, B, H, N, d, page, starts, counts, layout
+    ("bf16", torch.bfloat16, 1, 1, 1, 16, 16, [0], None, "bhnd"),
+    ("bf16", torch.float32, 3, 2, 40, 48, 16, [0, 15, 33], [40, 0, 17], "bnhd"),
+    ("e4m3", torch.bfloat16, 2, 3, 1, 128, 64, [63, 64], None, "bnhd"),
+    ("e4m3", torch.float32, 2, 2, 70, 80, 32, [5, 31], [70, 1], "bhnd"),
+    ("e4m3", torch.bfloat16, 4, 8, 33, 64, 256, [0, 255, 256, 7], [33, 33, 2, 0], "bnhd"),
+    ("e4m3", torch.bfloat16, 1, 5, 300, 112, 128, [100], None, "bhnd"),
+]
+
+
+@pytest.mark.parametrize("kind,dtype,B,H,N,d,page,starts,counts,layout", CACHE)
+def test_cache_write_and_read(kind, dtype, B, H, N, d, page, starts, counts, layout):
+    per = -(-(max(starts) + N) // page)
+    cache = _cache(B * per + 2, H, page, d, kind, 5)
+    table = _table(B, per, B * per + 2, 6)
+    k, v = _strided((B, H, N, d), layout, 7, dtype), _strided((B, H, N, d), layout, 8, dtype)
+    k[0, 0, 0] = 0.0  # a row of zeros, one of tiny values, one with a single large one
+    v[-1, -1, 0] *= 2.0 ** -130 if dtype == torch.float32 else 2.0 ** -100
+    v[0, 0, 0, d // 2] = 3e38
+    n = counts if counts is not None else [N] * B
+    want = []
+    for name, new in (("k", k), ("v", v)):
+        pool = getattr(cache, name).cpu().clone()
+        scale = getattr(cache, name + "_scale")
+        scale = None if scale is None else scale.cpu().clone()
+        if kind == "e4m3":
+            codes, bytes_ = ref.quantise(new.cpu())
+            pool = pool.view(torch.uint8)
+        for b in range(B):
+            for i in range(n[b]):
+                at, place = int(table[b, (starts[b] + i) // page]), (starts[b] + i) % page
+                if kind == "e4m3":
+                    pool[at, :, place], scale[at, :, place] = codes[b, :, i], bytes_[b, :, i]
+                else:
+                    pool[at, :, place] = new[b, :, i].cpu().to(torch.bfloat16)
+        want.append((pool, scale))
+    dev = [None if x is None else torch.tensor(x, dtype=torch.int32).cuda() for x in (starts, counts)]
+    fb.cache_write(cache, k, v, table.cuda(), *dev)
+    assert _status() == fb.FB_OK
+    for (pool, scale), name in zip(want, "kv"):
+        assert torch.equal(_bytes(getattr(cache, name).cpu()), _bytes(pool)), name
+        if scale is not None:
+            assert torch.equal(getattr(cache, name + "_scale").cpu(), scale), name
+    for out in (torch.bfloat16, torch.float32):
+        got = fb.cache_read(cache, table.cuda(), *dev, N, dtype=out)
+        assert _status() == fb.FB_OK
+        for x, name in zip(got, "kv"):
+            scale = getattr(cache, name + "_scale")
+            values = ref.pool_values(getattr(cache, name).cpu(), None if scale is None else scale.cpu())
+            full = torch.zeros(B, H, N, d, dtype=F64)
+            for b in range(B):
+                full[b, :, :n[b]] = ref.rows(values, table[b], starts[b], n[b])
+            # 8-bit values have 4 significant bits, so bf16 holds them exactly while they are normal
+            assert ((x.cpu().to(F64) - full).abs() <= 2.0 ** -133).all()
+
+
+def test_cache_special_values():
+    cache = fb.PagedCache.empty(1, 1, 16, 16, torch.float8_e4m3fn)
+    x = torch.zeros(1, 1, 4, 16)
+    x[0, 0, 0, :4] = torch.tensor([math.inf, -math.inf, math.nan, 7.0])
+    x[0, 0, 1, :3] = torch.tensor([448.0, -448.0, 449.0])
+    x[0, 0, 2, :2] = torch.tensor([1e-45, -1e-45])
+    x[0, 0, 3, :2] = torch.tensor([3.4e38, -3.4e38])
+    tab = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+    zero = torch.zeros(1, dtype=torch.int32, device="cuda")
+    fb.cache_write(cache, x.cuda(), x.cuda(), tab, zero)
+    codes, scale = ref.quantise(x)
+    assert torch.equal(cache.k.view(torch.uint8)[0, :, :4].cpu(), codes[0])
+    assert torch.equal(cache.k_scale.view(torch.uint8)[0, :, :4].cpu(), scale[0])
+    k, _ = fb.cache_read(cache, tab, None, None, 4, dtype=torch.float32)
+    assert k[0, 0, 0, 0] == 448 * 2.0 ** -6 and k[0, 0, 0, 2].isnan() and k[0, 0, 0, 3] == 7.0
+    assert _status() == fb.FB_OK
+
+
+def test_cache_bad_tables_are_skipped_and_flagged():
+    cache = _cache(4, 2, 16, 64, "bf16", 1)
+    before = cache.k.clone(), cache.v.clone()
+    k = _randn((2, 2, 3, 64), 3, torch.bfloat16).cuda()
+    start = torch.tensor([0, 40], dtype=torch.int32, device="cuda")  # the second lies past the table
+    for table in ([[-1], [0]], [[4], [0]], [[2 ** 31 - 1], [0]]):
+        tab = torch.tensor(table, dtype=torch.int32, device="cuda")
+        fb.cache_write(cache, k, k, tab, start)
+        assert _status() == fb.FB_ERR_RANGE
+        assert torch.equal(cache.k, before[0]) and torch.equal(cache.v, before[1])
+        got = fb.cache_read(cache, tab, start, None, 3)
+        assert _status() == fb.FB_ERR_RANGE and all((x == 0).all() for x in got)
+        o, lse = fb.attn_cache(k, cache, tab, start)
+        assert _status() == fb.FB_ERR_RANGE and torch.isfinite(o).all()
+    neg = torch.tensor([-5, -1], dtype=torch.int32, device="cuda")
+    fb.cache_write(cache, k[:, :, :1], k[:, :, :1], torch.zeros(2, 1, dtype=torch.int32, device="cuda"), neg)
+    assert _status() == fb.FB_ERR_RANGE and torch.equal(cache.k, before[0])
+    assert _status() == fb.FB_OK
+
+
+# ---------------------------------------------------------------- attention
+
+def _tree(B, T, seed):
+    rng = random.Random(seed)
+    seen, depth = torch.zeros(B, T, T, dtype=torch.bool), torch.zeros(B, T, dtype=torch.int32)
+    for b in range(B):
+        for t in range(T):
+            p = rng.randint(max(-1, t - 5), t - 1) if t else -1
+            if p >= 0:
+                seen[b, t] = seen[b, p]
+                depth[b, t] = depth[b, p] + 1
+            seen[b, t, t] = True
+    return seen, depth
+
+
+def _words(seen):
+    B, T, _ = seen.shape
+    bits = torch.zeros(B, T, -(-T // 32) * 32, dtype=torch.int64)
+    bits[:, :, :T] = seen
+    w = (bits.view(B, T, -1, 32) << torch.arange(32)).sum(-1)
+    return torch.where(w >= 2 ** 31, w - 2 ** 32, w).to(torch.int32)
+
+
+def _bias(kind, Hq, H, P, seed):
+    if kind == "none":
+        return None, None
+    pos = torch.arange(P, dtype=F64)
+    if kind == "alibi":
+        m = 2.0 ** (-8.0 * torch.arange(1, Hq + 1, dtype=F64) / Hq)
+        return (torch.stack([-m[:, None] * pos, m[:, None].expand(Hq, P)], -1).float(),
+                torch.stack([torch.ones_like(pos), pos], -1).float()[None])
+    if kind.startswith("sandwich"):
+        R = int(kind[8:])
+        a = pos[:, None] * 10000.0 ** (-2.0 * torch.arange(1, R // 2 + 1, dtype=F64) / R)
+        phi = torch.stack([a.cos(), a.sin()], -1).reshape(1, P, R).float()
+        return phi, phi
+    R = int(kind[3:])  # "low17": factors of each head, columns of very different size
+    size = torch.exp2(torch.linspace(-12, 12, R))
+    return _randn((Hq, P, R), seed) * R ** -0.5 * size, _randn((H, P, R), seed + 1) / size
+
+
+def _case(kind, d, Hq, H, T, page, prefix, counts, bias, tree, seed=0):
+    B = len(prefix)
+    per = max(1, -(-(max(prefix) + T) // page))
+    cache = _cache(B * per + 1, H, page, d, kind, seed + 10)
+    table = _table(B, per, B * per + 1, seed + 11)
+    q = _randn((B, Hq, T, d), seed + 12, torch.bfloat16)
+    mask = depth = None
+    if tree:
+        seen, depth = _tree(B, T, seed + 13)
+        mask = _words(seen)
+    fq, fk = _bias(bias, Hq, H, per * page, seed + 14)
+    return dict(q=q, cache=cache, table=table, prefix=torch.tensor(prefix, dtype=torch.int32),
+                counts=None if counts is None else torch.tensor(counts, dtype=torch.int32), mask=mask, depth=depth,
+                fq=fq, fk=fk)
+
+
+def _call(c, **kw):
+    dev = lambda x: None if x is None else x.cuda()  # noqa: E731
+    bias = None if c["fq"] is None else fb.CacheBias(c["fq"].cuda(), c["fk"].cuda())
+    return fb.attn_cache(c["q"].cuda(), c["cache"], c["table"].cuda(), c["prefix"].cuda(), dev(c["counts"]),
+                         tree_mask=dev(c["mask"]), depths=dev(c["depth"]), bias=bias, **kw)
+
+
+def _want(c):
+    cache = c["cache"]
+    e4m3 = cache.k_scale is not None
+    kv = ref.pool_values(cache.k.cpu(), cache.k_scale.cpu() if e4m3 else None)
+    vv = ref.pool_values(cache.v.cpu(), cache.v_scale.cpu() if e4m3 else None)
+    counts = c["counts"] if c["counts"] is not None else [c["q"].shape[2]] * c["q"].shape[0]
+    return ref.attend(c["q"], kv, vv, c["table"], c["prefix"], counts, c["mask"], c["depth"], c["fq"], c["fk"],
+                      part_bits=11 if e4m3 else 8)
+
+
+def _compare(got, want):
+    (o, lse), (ro, rl, to, tl) = (x.cpu().to(F64) for x in got), want
+    assert torch.equal(lse == -math.inf, rl == -math.inf)
+    some = rl > -math.inf
+    err = (lse[some] - rl[some]).abs() / tl[some]
+    assert not some.any() or err.max() <= 1.0, f"LSE: {float(err.max()):.3g} of its bound"
+    assert torch.isfinite(o).all()
+    over = (o - ro).abs() - to
+    assert (over <= 0).all(), f"O: {float(over.max()):.3g} past its bound"
+
+
+ATTEND = [  # cache, d, Hq, H, T, page, prefix, counts, bias, tree
+    ("bf16", 64, 1, 1, 1, 16, [0], None, "none", False),
+    ("bf16", 64, 12, 12, 1, 16, [700], None, "sandwich64", False),
+    ("e4m3", 128, 16, 16, 1, 64, [1, 15, 16, 17, 127, 1023], None, "alibi", False),
+    ("bf16", 128, 32, 4, 1, 128, [5000, 63], None, "none", False),
+    ("e4m3", 16, 2, 1, 1, 16, [33, 0], None, "low3", False),
+    ("bf16", 16, 4, 2, 3, 32, [31, 32, 33], [3, 1, 2], "low17", False),
+    ("e4m3", 48, 3, 3, 24, 16, [100, 0, 511], [24, 24, 5], "alibi", True),
+    ("bf16", 80, 4, 1, 5, 256, [255, 256, 1], None, "low32", True),
+    ("e4m3", 96, 8, 2, 61, 64, [130, 64], [61, 33], "low8", True),
+    ("bf16", 112, 6, 2, 33, 16, [47], None, "sandwich32", True),
+    ("bf16", 32, 8, 8, 64, 64, [200, 3], [64, 1], "low48", True),
+    ("e4m3", 64, 16, 2, 17, 32, [77, 2000], None, "sandwich128", False),
+    ("e4m3", 128, 32, 4, 61, 64, [900, 31], [61, 60], "low32", True),
+    ("bf16", 128, 8, 8, 1, 64, [64 * k for k in range(40)], None, "alibi", False),
+    ("bf16", 64, 2, 2, 200, 16, [300, 0], [200, 150], "none", False),
+]
+
+
+@pytest.mark.parametrize("kind,d,Hq,H,T,page,prefix,counts,bias,tree", ATTEND)
+def test_attn_cache_matches_reference(kind, d, Hq, H, T, page, prefix, counts, bias, tree):
+    c = _case(kind, d, Hq, H, T, page, prefix, counts, bias, tree)
+    ws = fb.cache_workspace(len(prefix), Hq, H, T, d)
+    want = _want(c)
+    got = _call(c, workspace=ws)
+    assert _status() == fb.FB_OK
+    _compare(got, want)
+    again = _call(c, workspace=ws)  # the workspace is as it was, and the result the same to the bit
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("T", [4, 40])
+def test_rows_that_see_nothing_and_values_that_are_not_seen(kind, T):
+    """No context and an empty mask row: O = 0, LSE = -inf. Infinities and NaN in drafted rows, in the rows behind the
+    last token and in unused pages stay where they are seen."""
+    c = _case(kind, 64, 4, 2, T, 16, [0, 20], [T, T - 1], "low8", True, seed=3)
+    mask = c["mask"]
+    mask[0, 2] = 0
+    seen_1 = (mask[1, :, 0] >> 1) & 1  # rows of sequence 1 that see its drafted token 1
+    clean = _want(c)
+    at = lambda b, i: (int(c["table"][b, i // 16]), i % 16)  # noqa: E731
+    cache = c["cache"]
+    for name in "kv":
+        pool, scale = getattr(cache, name), getattr(cache, name + "_scale")
+        used = [at(0, i) for i in range(T)] + [at(1, i) for i in range(20 + T - 1)]
+        flat = torch.ones(pool.shape[0], 16, dtype=torch.bool)
+        for p, i in used:
+            flat[p, i] = False
+        p, i = at(1, 21)
+        flat[p, i] = True
+        where = flat.nonzero().cuda()
+        if kind == "bf16":
+            pool[where[:, 0], :, where[:, 1]] = math.nan
+            pool[where[:, 0], :, where[:, 1], 5] = math.inf
+        else:
+            pool.view(torch.uint8)[where[:, 0], :, where[:, 1]] = 0x7F
+            scale.view(torch.uint8)[where[:, 0], :, where[:, 1]] = 0xFF
+    o, lse = _call(c)
+    ro, rl, to, tl = clean
+    hit = torch.zeros(2, T, dtype=torch.bool)
+    hit[1] = (seen_1 == 1) & (torch.arange(T) < T - 1)
+    assert o[1].cpu()[:, hit[1]].isnan().any() if hit.any() else True
+    keep = ~hit[:, None, :].expand(2, 4, T)
+    o, lse = o.cpu().to(F64), lse.cpu().to(F64)
+    assert (lse[0, :, 2] == -math.inf).all() and (o[0, :, 2] == 0).all()
+    assert (lse[1, :, T - 1] == -math.inf).all() and (o[1, :, T - 1] == 0).all()
+    assert torch.equal(lse[keep] == -math.inf, rl[keep] == -math.inf)
+    some = keep & (rl > -math.inf)
+    assert ((lse[some] - rl[some]).abs() <= tl[some]).all()
+    assert ((o - ro).abs() <= to)[keep].all()
+
+
+def test_infinite_value_reaches_the_rows_that_see_it():
+    c = _case("bf16", 32, 1, 1, 3, 16, [4], None, "none", False)
+    p, i = int(c["table"][0, 0]), 5  # drafted token 1: rows 1 and 2 see it
+    c["cache"].v[p, 0, i, 7] = math.inf
+    o, _ = _call(c)
+    assert torch.isfinite(o[0, 0, 0]).all() and (o[0, 0, 1:, 7] == math.inf).all()
+    o = o[0, 0, :, [j for j in range(32) if j != 7]]
+    assert torch.isfinite(o).all()
+
+
+def test_bias_of_the_lowest_values():
+    """Factors that shut keys out with the type's lowest value, or all keys of a row: fp32 scores, so the softmax of a
+    row whose scores all are -3e38 is uniform, as its definition says."""
+    low = torch.finfo(torch.float32).min
+    c = _case("bf16", 64, 2, 1, 1, 16, [40], None, "none", False)
+    P = 48
+    fk = torch.zeros(1, P, 1)
+    fk[0, 10:] = 1.0
+    c["fq"], c["fk"] = torch.full((2, P, 1), low), fk
+    o, lse = _call(c)
+    v = ref.rows(c["cache"].v.cpu().to(F64), c["table"][0], 0, 41)[0]
+    c2 = _case("bf16", 64, 2, 1, 1, 16, [40], None, "none", False)
+    full = _want(dict(c, fq=None, fk=None))
+    del full, c2
+    k = ref.rows(c["cache"].k.cpu().to(F64), c["table"][0], 0, 41)[0]
+    x = (c["q"][0, :, 0].to(F64) @ k[:10].T) / 8
+    want = torch.softmax(x, -1) @ v[:10]
+    assert ((o[0, :, 0].cpu().to(F64) - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -7 * v[:10].abs().amax(0)).all()
+    assert ((lse[0, :, 0].cpu().to(F64) - torch.logsumexp(x, -1)).abs() <= 1e-4).all()
+    c["fk"] = torch.ones(1, P, 1)
+    o, lse = _call(c)
+    assert ((o[0, :, 0].cpu().to(F64) - v.mean(0)).abs() <= 2.0 ** -8 * v.abs().amax(0)).all()
+    assert (lse < -3e38).all() and torch.isfinite(lse).all()
+
+
+def test_value_rows_of_very_different_size():
+    """An e4m3 row of values 2^100 larger that carries no weight does not push the others out of fp16's range."""
+    c = _case("e4m3", 64, 2, 2, 1, 16, [60], None, "none", False)
+    c["cache"].v_scale.view(torch.uint8)[int(c["table"][0, 0]), :, 3] = 227
+    P = 64
+    fk = torch.zeros(1, P, 1)
+    fk[0, 3] = 1.0
+    c["fq"], c["fk"] = torch.full((2, P, 1), -1e4), fk
+    _compare(_call(c), _want(c))
+
+
+def test_positions_past_the_factors_are_flagged():
+    c = _case("bf16", 64, 1, 1, 1, 16, [30], None, "alibi", False)
+    c["fq"], c["fk"] = c["fq"][:, :20].contiguous(), c["fk"][:, :20].contiguous()
+    o, _ = _call(c)
+    assert _status() == fb.FB_ERR_RANGE and torch.isfinite(o).all()
+
+
+def test_captured_calls_on_another_stream():
+    """One graph of a whole step (turn, write, attend) replayed with new inputs, beside eager calls on another stream
+    with a workspace of their own."""
+    B, H, T, d = 3, 4, 1, 64
+    cache = _cache(13, H, 16, d, "e4m3", 1)
+    table = _table(B, 4, 13, 2).cuda()
+    r = fb.Rope.scaled(64)
+    q, k, v = (_randn((B, T, H, d), s, torch.bfloat16).cuda() for s in (3, 4, 5))
+    prefix = torch.tensor([5, 30, 62], dtype=torch.int32, device="cuda")
+    pos = prefix[:, None].clone()
+
+    def step(ws):
+        qr, kr = fb.rope(q.transpose(1, 2), k.transpose(1, 2), r, pos)
+        fb.cache_write(cache, kr, v.transpose(1, 2), table, prefix)
+        return fb.attn_cache(qr.contiguous(), cache, table, prefix, workspace=ws)
+
+    ws, ws2 = (fb.cache_workspace(B, H, H, T, d) for _ in range(2))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(ws)
+        side.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            out = step(ws)
+    torch.cuda.current_stream().wait_stream(side)
+    for s in range(3):
+        for x, seed in ((q, 10), (k, 20), (v, 30)):
+            x.copy_(_randn(x.shape, seed + s, torch.bfloat16))
+        if s:
+            prefix.sub_(1)
+            pos.sub_(1)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [x.clone() for x in out]
+        with torch.cuda.stream(side):
+            eager = step(ws2)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, eager))
+    assert _status() == fb.FB_OK
+
+
+def test_decode_steps_agree_with_full_attention():
+    """A run as it is used: prompt turned and written, tokens decoded one at a time with ALiBi factors, then the same
+    tokens as one drafted chain, and the framework's full causal attention over what the cache holds."""
+    B, Hq, H, N, d, steps = 2, 4, 4, 90, 64, 6
+    total = N + steps
+    r = fb.Rope.scaled(64, scaling="linear", by=4.0)
+    q, k, v = (_randn((B, H, total, d), s, torch.bfloat16).cuda() for s in (1, 2, 3))
+    qr, kr = fb.rope(q, k, r)
+    pq, pk = fb.factors_alibi(Hq, total)
+    bias = fb.CacheBias(pq, pk)
+    for dtype in (torch.bfloat16, torch.float8_e4m3fn):
+        cache = fb.PagedCache.empty(2 * 6 + 1, H, 16, d, dtype)
+        table = _table(B, 6, 13, 4).cuda()
+        at = lambda n: torch.full((B,), n, dtype=torch.int32, device="cuda")  # noqa: E731
+        fb.cache_write(cache, kr[:, :, :N], v[:, :, :N], table, at(0))
+        ones = []
+        for n in range(N, total):
+            fb.cache_write(cache, kr[:, :, n:n + 1], v[:, :, n:n + 1], table, at(n))
+            ones.append(fb.attn_cache(qr[:, :, n:n + 1].contiguous(), cache, table, at(n), bias=bias))
+        chain = fb.attn_cache(qr[:, :, N:].contiguous(), cache, table, at(N), bias=bias)
+        kc, vc = fb.cache_read(cache, table, None, None, total)
+        full = fb.attn(qr, kc, vc, pq, pk, causal=True)
+        assert _status() == fb.FB_OK
+        for i in range(steps):
+            for a, b, c in zip(ones[i], chain, full):
+                a, b, c = a[:, :, 0].double(), b[:, :, i].double(), c[:, :, N + i].double()
+                # all three round probabilities (2^-8 of weights that add up to 1, on values below 5) and O
+                assert (a - b).abs().max() <= 2.0 ** -6 and (a - c).abs().max() <= 2e-2
