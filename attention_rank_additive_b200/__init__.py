@@ -625,29 +625,34 @@ def attn_flops(B: int, H: int, N: int, d: int, R: int, causal: bool) -> float:
 
 # ------------------------------------------------- serving: rotary positions, paged cache, attention over it
 
-def _need(ok, what: str):
-    if not ok:
-        raise ValueError(what)
-
-
 class _On:
-    """The tensors' device as the current one while a call launches (nothing to do where it is already)."""
+    """The tensors' device as the current one while a call launches."""
 
     __slots__ = ("old", "new")
 
-    def __init__(self, device):
-        import torch
-        self.new, self.old = device.index, torch.cuda.current_device()
+    def __init__(self, new: int, old: int):
+        self.new, self.old = new, old
 
     def __enter__(self):
-        if self.new != self.old:
-            import torch
-            torch.cuda.set_device(self.new)
+        import torch
+        torch.cuda.set_device(self.new)
 
     def __exit__(self, *exc):
-        if self.new != self.old:
-            import torch
-            torch.cuda.set_device(self.old)
+        import torch
+        torch.cuda.set_device(self.old)
+
+
+def _launch(call, where: str, index: int, *args):
+    """call(*args, the current stream of device `index`), with that device current."""
+    import torch
+    now = torch.cuda.current_device()
+    if now == index:
+        status = call(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with _On(index, now):
+            status = call(*args, torch._C._cuda_getCurrentRawStream(index))
+    if status != FB_OK:
+        raise FlashBiasError(status, where)
 
 
 def _ints(t, shape, device, what: str) -> int:
@@ -655,8 +660,8 @@ def _ints(t, shape, device, what: str) -> int:
     import torch
     if t is None:
         return 0
-    _need(t.dtype == torch.int32 and t.shape == shape and t.device == device and t.is_contiguous(),
-          f"{what}: a contiguous int32 tensor {tuple(shape)} on {device}")
+    if t.dtype != torch.int32 or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{what}: a contiguous int32 tensor {tuple(shape)} on {device}")
     return t.data_ptr()
 
 
@@ -672,13 +677,15 @@ class Rope:
     def __init__(self, frequencies, interleaved=False, factor=1.0, device="cuda"):
         import torch
         pairs = len(frequencies)
-        _need(pairs >= 1, "Rope: at least one pair")
+        if not (pairs >= 1):
+            raise ValueError("Rope: at least one pair")
         freq = (ctypes.c_double * pairs)(*[float(w) for w in frequencies])
         turns = (ctypes.c_uint64 * pairs)()
         _check(fb_rope_turns_host(pairs, ctypes.addressof(freq), ctypes.addressof(turns)), "fb_rope_turns_host")
         self.frequencies = list(freq)
         self.rot, self.interleaved, self.factor = 2 * pairs, bool(interleaved), float(factor)
-        _need(math.isfinite(self.factor) and self.factor != 0.0, "Rope: factor finite and not 0")
+        if not (math.isfinite(self.factor) and self.factor != 0.0):
+            raise ValueError("Rope: factor finite and not 0")
         # 2^-64 turns as two's complement: torch's uint64 has few operations
         signed = [t - (1 << 64) if t >> 63 else t for t in turns]
         self.turns = torch.tensor(signed, dtype=torch.int64, device=device)
@@ -687,7 +694,8 @@ class Rope:
     def scaled(cls, rot: int, base=10000.0, scaling="none", by=1.0, trained=4096.0, fast=32.0, slow=1.0,
                interleaved=False, factor=None, device="cuda"):
         """base^(-2p / rot), for contexts `by` times the trained length (fb_rope_frequencies_host)."""
-        _need(scaling in cls.SCALINGS, f"Rope.scaled: scaling one of {cls.SCALINGS}")
+        if not (scaling in cls.SCALINGS):
+            raise ValueError(f"Rope.scaled: scaling one of {cls.SCALINGS}")
         freq, out = (ctypes.c_double * max(rot // 2, 1))(), ctypes.c_double()
         _check(fb_rope_frequencies_host(rot, base, cls.SCALINGS.index(scaling), by, trained, fast, slow,
                                         ctypes.addressof(freq), ctypes.addressof(out)), "fb_rope_frequencies_host")
@@ -696,36 +704,38 @@ class Rope:
 
 def _rope(call, where, q, k, rope, positions, out):
     import torch
-    _need(q.dim() == 4 and q.is_cuda and q.stride(3) == 1, f"{where}: q a CUDA tensor [B, H, N, d], d contiguous")
+    if not (q.dim() == 4 and q.is_cuda and q.stride(3) == 1):
+        raise ValueError(f"{where}: q a CUDA tensor [B, H, N, d], d contiguous")
     B, Hq, N, d = q.shape
     dev, dt = q.device, _dtype_code(q)
-    _need(rope.turns.device == dev, f"{where}: the Rope is on another device")
+    if not (rope.turns.device == dev):
+        raise ValueError(f"{where}: the Rope is on another device")
     qo, ko = out if out is not None else (torch.empty_like(q), None if k is None else torch.empty_like(k))
-    _need(qo.shape == q.shape and qo.dtype == q.dtype and qo.device == dev and qo.stride(3) == 1,
-          f"{where}: out like q")
+    if not (qo.shape == q.shape and qo.dtype == q.dtype and qo.device == dev and qo.stride(3) == 1):
+        raise ValueError(f"{where}: out like q")
     if k is None:
         side_k = (0, 0, 0, 0, 0, 0, 0, 0, 0)
     else:
-        _need(k.dim() == 4 and k.shape[0] == B and k.shape[2:] == q.shape[2:] and k.dtype == q.dtype
-              and k.device == dev and k.stride(3) == 1, f"{where}: k [B, Hk, N, d] like q")
-        _need(ko.shape == k.shape and ko.dtype == k.dtype and ko.device == dev and ko.stride(3) == 1,
-              f"{where}: out like k")
+        if not (k.dim() == 4 and k.shape[0] == B and k.shape[2:] == q.shape[2:]
+                and k.dtype == q.dtype and k.device == dev and k.stride(3) == 1):
+            raise ValueError(f"{where}: k [B, Hk, N, d] like q")
+        if not (ko.shape == k.shape and ko.dtype == k.dtype and ko.device == dev and ko.stride(3) == 1):
+            raise ValueError(f"{where}: out like k")
         side_k = (k.shape[1], k.data_ptr(), *k.stride()[:3], ko.data_ptr(), *ko.stride()[:3])
     if out is not None:
         for t in out:
-            _need(t is None or all(s > 0 or n <= 1 for s, n in zip(t.stride(), t.shape)),
-                  f"{where}: out with places of its own for every value")
+            if not (t is None or all(s > 0 or n <= 1 for s, n in zip(t.stride(), t.shape))):
+                raise ValueError(f"{where}: out with places of its own for every value")
     pos, pos_bs = 0, 0
     if positions is not None:
-        _need(positions.dtype == torch.int32 and positions.device == dev and positions.shape[-1] == N
-              and (N == 1 or positions.stride(-1) == 1)
-              and (positions.dim() == 1 or (positions.dim() == 2 and positions.shape[0] in (1, B))),
-              f"{where}: positions int32 [N], [1, N] or [B, N] on {dev}, contiguous along N")
+        if not (positions.dtype == torch.int32 and positions.device == dev and positions.shape[-1] == N
+                and (N == 1 or positions.stride(-1) == 1)
+                and (positions.dim() == 1 or (positions.dim() == 2 and positions.shape[0] in (1, B)))):
+            raise ValueError(f"{where}: positions int32 [N], [1, N] or [B, N] on {dev}, contiguous along N")
         pos = positions.data_ptr()
         pos_bs = positions.stride(0) if positions.dim() == 2 and positions.shape[0] == B and B > 1 else 0
-    with _On(dev):
-        _check(call(dt, B, N, d, rope.rot, rope.interleaved, rope.turns.data_ptr(), rope.factor, pos, pos_bs, Hq,
-                    q.data_ptr(), *q.stride()[:3], qo.data_ptr(), *qo.stride()[:3], *side_k, _stream(dev)), where)
+    _launch(call, where, dev.index, dt, B, N, d, rope.rot, rope.interleaved, rope.turns.data_ptr(), rope.factor, pos,
+            pos_bs, Hq, q.data_ptr(), *q.stride()[:3], qo.data_ptr(), *qo.stride()[:3], *side_k)
     return qo, ko
 
 
@@ -752,16 +762,18 @@ class PagedCache:
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
         import torch
-        _need(k.is_cuda and k.dim() == 4 and k.dtype in (torch.bfloat16, torch.float8_e4m3fn) and k.is_contiguous(),
-              "PagedCache: k a contiguous CUDA tensor [pages, H, page, d], bfloat16 or float8_e4m3fn")
-        _need(v.shape == k.shape and v.dtype == k.dtype and v.device == k.device and v.is_contiguous(),
-              "PagedCache: v like k")
+        if not (k.is_cuda and k.dim() == 4 and k.dtype in (torch.bfloat16, torch.float8_e4m3fn) and k.is_contiguous()):
+            raise ValueError("PagedCache: k a contiguous CUDA tensor [pages, H, page, d], bfloat16 or float8_e4m3fn")
+        if not (v.shape == k.shape and v.dtype == k.dtype and v.device == k.device and v.is_contiguous()):
+            raise ValueError("PagedCache: v like k")
         self.dt = FB_E4M3 if k.dtype == torch.float8_e4m3fn else FB_BF16
         for s in (k_scale, v_scale):
-            _need((s is None) == (self.dt == FB_BF16), "PagedCache: scales for float8_e4m3fn, none for bfloat16")
+            if not ((s is None) == (self.dt == FB_BF16)):
+                raise ValueError("PagedCache: scales for float8_e4m3fn, none for bfloat16")
             if s is not None:
-                _need(s.dtype in (torch.float8_e8m0fnu, torch.uint8) and s.shape == k.shape[:3] and s.device == k.device
-                      and s.is_contiguous(), "PagedCache: scales float8_e8m0fnu or uint8 [pages, H, page]")
+                if not (s.dtype in (torch.float8_e8m0fnu, torch.uint8) and s.shape == k.shape[:3]
+                        and s.device == k.device and s.is_contiguous()):
+                    raise ValueError("PagedCache: scales float8_e8m0fnu or uint8 [pages, H, page]")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.device = k.device
         self.num_pages, self.heads, self.page, self.d = k.shape
@@ -784,8 +796,9 @@ class PagedCache:
 
     def _table(self, table, B):
         import torch
-        _need(table.dtype == torch.int32 and table.dim() == 2 and table.shape[0] == B and table.device == self.device
-              and table.is_contiguous(), f"block table: a contiguous int32 tensor [{B}, pages] on {self.device}")
+        if not (table.dtype == torch.int32 and table.dim() == 2 and table.shape[0] == B
+                and table.device == self.device and table.is_contiguous()):
+            raise ValueError(f"block table: a contiguous int32 tensor [{B}, pages] on {self.device}")
         return table.data_ptr(), table.shape[1]
 
 
@@ -794,19 +807,20 @@ def cache_write(cache: PagedCache, k, v, table, starts, counts=None):
     k, v [B, H, N, d] (bf16 or fp32, any order of the first three dimensions)
     becomes token starts[b] + n of sequence b. table: int32 [B, max_pages];
     starts, counts: int32 [B] (counts None: every row)."""
-    _need(k.dim() == 4 and k.device == cache.device and k.stride(3) == 1 and v.shape == k.shape and v.dtype == k.dtype
-          and v.device == k.device and v.stride(3) == 1, f"cache_write: k, v [B, H, N, d] on {cache.device}, d contiguous")
+    if not (k.dim() == 4 and k.device == cache.device and k.stride(3) == 1 and v.shape == k.shape
+            and v.dtype == k.dtype and v.device == k.device and v.stride(3) == 1):
+        raise ValueError(f"cache_write: k, v [B, H, N, d] on {cache.device}, d contiguous")
     B, H, N, d = k.shape
-    _need(H == cache.heads and d == cache.d, f"cache_write: {cache.heads} heads of {cache.d}")
+    if not (H == cache.heads and d == cache.d):
+        raise ValueError(f"cache_write: {cache.heads} heads of {cache.d}")
     tab, width = cache._table(table, B)
     kp, vp, ks, vs, pages, page = cache._pointers()
-    _need(starts is not None, "cache_write: starts")
-    with _On(cache.device):
-        _check(lib().fb_cache_write(_dtype_code(k), cache.dt, B, H, N, d, k.data_ptr(), *k.stride()[:3], v.data_ptr(),
-                                    *v.stride()[:3], kp, vp, ks, vs, pages, page, tab, width,
-                                    _ints(starts, (B,), cache.device, "starts"),
-                                    _ints(counts, (B,), cache.device, "counts"), _stream(cache.device)),
-               "fb_cache_write")
+    if not (starts is not None):
+        raise ValueError("cache_write: starts")
+    dev = cache.device
+    _launch(lib().fb_cache_write, "fb_cache_write", dev.index, _dtype_code(k), cache.dt, B, H, N, d, k.data_ptr(),
+            *k.stride()[:3], v.data_ptr(), *v.stride()[:3], kp, vp, ks, vs, pages, page, tab, width,
+            _ints(starts, (B,), dev, "starts"), _ints(counts, (B,), dev, "counts"))
 
 
 def cache_read(cache: PagedCache, table, starts, counts, tokens: int, dtype=None, out=None):
@@ -822,14 +836,13 @@ def cache_read(cache: PagedCache, table, starts, counts, tokens: int, dtype=None
         k, v = torch.empty(shape, dtype=dtype, device=dev), torch.empty(shape, dtype=dtype, device=dev)
     else:
         k, v = out
-        _need(all(t.shape == shape and t.device == dev and t.is_contiguous() and t.dtype == k.dtype for t in (k, v))
-              and dtype in (None, k.dtype), f"cache_read: out two contiguous tensors {shape}")
+        if not (all(t.shape == shape and t.device == dev and t.is_contiguous() and t.dtype == k.dtype for t in (k, v))
+                and dtype in (None, k.dtype)):
+            raise ValueError(f"cache_read: out two contiguous tensors {shape}")
     kp, vp, ks, vs, pages, page = cache._pointers()
-    with _On(dev):
-        _check(lib().fb_cache_read(_dtype_code(k), cache.dt, B, cache.heads, tokens, cache.d, kp, vp, ks, vs, pages,
-                                   page, tab, width, _ints(starts, (B,), dev, "starts"),
-                                   _ints(counts, (B,), dev, "counts"), k.data_ptr(), v.data_ptr(), _stream(dev)),
-               "fb_cache_read")
+    _launch(lib().fb_cache_read, "fb_cache_read", dev.index, _dtype_code(k), cache.dt, B, cache.heads, tokens, cache.d,
+            kp, vp, ks, vs, pages, page, tab, width, _ints(starts, (B,), dev, "starts"),
+            _ints(counts, (B,), dev, "counts"), k.data_ptr(), v.data_ptr())
     return k, v
 
 
@@ -843,25 +856,26 @@ class CacheBias:
         import torch
         phi_q, phi_k = (x[None] if x.dim() == 2 else x for x in (phi_q, phi_k))
         for x in (phi_q, phi_k):
-            _need(x.is_cuda and x.dim() == 3 and x.dtype == torch.float32, "CacheBias: fp32 CUDA factors [heads, P, R]")
-        _need(phi_q.shape[1:] == phi_k.shape[1:] and phi_q.device == phi_k.device,
-              "CacheBias: factors of one length, rank and device")
+            if not (x.is_cuda and x.dim() == 3 and x.dtype == torch.float32):
+                raise ValueError("CacheBias: fp32 CUDA factors [heads, P, R]")
+        if not (phi_q.shape[1:] == phi_k.shape[1:] and phi_q.device == phi_k.device):
+            raise ValueError("CacheBias: factors of one length, rank and device")
         phi_q, phi_k = phi_q.contiguous(), phi_k.contiguous()
         self.device = phi_q.device
         self.q_heads, self.P, self.R = phi_q.shape
         self.k_heads = phi_k.shape[0]
         nb = fb_cache_bias_bytes(self.q_heads, self.k_heads, self.P, self.R)
         self.prepared = torch.empty(max(nb, 1), device=self.device, dtype=torch.uint8)
-        with _On(self.device):
-            _check(fb_cache_bias_prepare(self.q_heads, self.k_heads, self.P, self.R, phi_q.data_ptr(), phi_k.data_ptr(),
-                                         self.prepared.data_ptr(), nb, _stream(self.device)), "fb_cache_bias_prepare")
+        _launch(lib().fb_cache_bias_prepare, "fb_cache_bias_prepare", self.device.index, self.q_heads, self.k_heads,
+                self.P, self.R, phi_q.data_ptr(), phi_k.data_ptr(), self.prepared.data_ptr(), nb)
 
 
 def cache_workspace(B: int, Hq: int, H: int, T: int, d: int, device="cuda"):
     """A workspace for attn_cache calls of these sizes (one per call that can run at the same time)."""
     import torch
     nb = fb_attn_cache_workspace_bytes(B, Hq, H, T, d)
-    _need(nb > 0, f"cache_workspace: unsupported sizes B={B} Hq={Hq} H={H} T={T} d={d}")
+    if not (nb > 0):
+        raise ValueError(f"cache_workspace: unsupported sizes B={B} Hq={Hq} H={H} T={T} d={d}")
     return torch.zeros(nb, device=device, dtype=torch.uint8)
 
 
@@ -879,11 +893,12 @@ def attn_cache(q, cache: PagedCache, table, prefix, counts=None, tree_mask=None,
     memset)."""
     import torch
     dev = cache.device
-    _need(q.dim() == 4 and q.dtype == torch.bfloat16 and q.device == dev and q.is_contiguous(),
-          f"attn_cache: q a contiguous bfloat16 tensor [B, Hq, T, d] on {dev}")
+    if not (q.dim() == 4 and q.dtype == torch.bfloat16 and q.device == dev and q.is_contiguous()):
+        raise ValueError(f"attn_cache: q a contiguous bfloat16 tensor [B, Hq, T, d] on {dev}")
     B, Hq, T, d = q.shape
     H = cache.heads
-    _need(d == cache.d, f"attn_cache: head dim {cache.d}")
+    if not (d == cache.d):
+        raise ValueError(f"attn_cache: head dim {cache.d}")
     tab, width = cache._table(table, B)
     words, mask = 0, 0
     if tree_mask is not None:
@@ -891,23 +906,25 @@ def attn_cache(q, cache: PagedCache, table, prefix, counts=None, tree_mask=None,
         mask = _ints(tree_mask, (B, T, words), dev, "tree_mask")
     R, P, fq, fk, pb = 0, 0, 0, 0, 0
     if bias is not None:
-        _need(bias.device == dev, "attn_cache: the bias is on another device")
+        if not (bias.device == dev):
+            raise ValueError("attn_cache: the bias is on another device")
         R, P, fq, fk, pb = bias.R, bias.P, bias.q_heads, bias.k_heads, bias.prepared.data_ptr()
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
     o = torch.empty_like(q) if out is None else out
     l = torch.empty((B, Hq, T), device=dev, dtype=torch.float32) if lse is None else lse
-    _need(out is None or (o.shape == q.shape and o.dtype == q.dtype and o.device == dev and o.is_contiguous()),
-          "attn_cache: out like q")
-    _need(lse is None or (l.shape == (B, Hq, T) and l.dtype == torch.float32 and l.device == dev and l.is_contiguous()),
-          "attn_cache: lse a contiguous float32 tensor [B, Hq, T]")
+    if not (out is None or (o.shape == q.shape and o.dtype == q.dtype and o.device == dev and o.is_contiguous())):
+        raise ValueError("attn_cache: out like q")
+    if not (lse is None or (l.shape == (B, Hq, T) and l.dtype == torch.float32 and l.device == dev
+                            and l.is_contiguous())):
+        raise ValueError("attn_cache: lse a contiguous float32 tensor [B, Hq, T]")
     kp, vp, ks, vs, pages, page = cache._pointers()
-    with _On(dev):
-        if workspace is None:
-            workspace = torch.zeros(max(fb_attn_cache_workspace_bytes(B, Hq, H, T, d), 1), device=dev, dtype=torch.uint8)
-        _need(workspace.device == dev and workspace.is_contiguous(), "attn_cache: workspace of cache_workspace")
-        _check(lib().fb_attn_cache_fwd(cache.dt, B, Hq, H, T, d, q.data_ptr(), kp, vp, ks, vs, pages, page, tab, width,
-                                       _ints(prefix, (B,), dev, "prefix"), _ints(counts, (B,), dev, "counts"), mask,
-                                       words, _ints(depths, (B, T), dev, "depths"), R, P, fq, fk, pb, scale,
-                                       o.data_ptr(), l.data_ptr(), workspace.data_ptr(),
-                                       workspace.numel() * workspace.element_size(), _stream(dev)), "fb_attn_cache_fwd")
+    if workspace is None:
+        nb = fb_attn_cache_workspace_bytes(B, Hq, H, T, d)
+        workspace = torch.zeros(max(nb, 1), device=dev, dtype=torch.uint8)
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("attn_cache: workspace of cache_workspace")
+    _launch(lib().fb_attn_cache_fwd, "fb_attn_cache_fwd", dev.index, cache.dt, B, Hq, H, T, d, q.data_ptr(), kp, vp, ks,
+            vs, pages, page, tab, width, _ints(prefix, (B,), dev, "prefix"), _ints(counts, (B,), dev, "counts"), mask,
+            words, _ints(depths, (B, T), dev, "depths"), R, P, fq, fk, pb, scale, o.data_ptr(), l.data_ptr(),
+            workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return o, l

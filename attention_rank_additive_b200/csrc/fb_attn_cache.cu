@@ -12,11 +12,16 @@
 // the keys are the 16 rows of the matrix instruction and the (few) query rows
 // its 8 columns, S^T = K Q^T and O^T = V^T P^T. Both operands that come from
 // memory then take d in any order as long as the query side (or the output)
-// uses the same one, so each lane loads 16 neighbouring bytes of a row straight
-// into the registers that feed the tensor cores: no shared memory, no barrier
-// between warps, and every sector of a row is read whole by one instruction.
-// The same swap halves the idle rows for a single token (8 columns, not 16
-// rows). P^T is S^T's accumulator after one 8x8 transpose (movmatrix).
+// uses the same one, so a lane's operand registers are 16 neighbouring bytes of
+// a row, and every sector of a row is read whole by one instruction. The same
+// swap halves the idle rows for a single token (8 columns, not 16 rows). P^T is
+// S^T's accumulator after one 8x8 transpose (movmatrix).
+//
+// Each warp walks over 16-key groups of its own. A lane copies the very bytes
+// that it will use itself into a ring in shared memory with cp.async, several
+// groups ahead: the ring needs no barrier and has no bank conflicts, and the
+// loads in flight cost no registers (held in registers, 32 keys a step, the
+// 16-head ALiBi decode step took 142 us, 45 % of the copy rate).
 //
 // Work is dealt out by keys: all blocks of keys of all (sequence, head) items,
 // as the lengths on the device say, are numbered through and each CTA takes an
@@ -29,33 +34,42 @@
 #include <cmath>
 #include <cstring>
 
-#include "fb_attn_cache.h"
+#include "fb_attn_cache.cuh"
 #include "fb_internal.h"
-#include "fb_ptx.cuh"
 
 namespace fb {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kWarps = 4;
+constexpr int kBlockKeys = 16 * kWarps;  // a block: a 16-key group per warp
+
+// CTAs of 128 threads on an SM at most, by blocks of 8 query rows: the registers of O and Q allow no more.
+constexpr int cta_per_sm(int NB) { return NB == 1 ? 4 : (NB == 2 ? 3 : 2); }
 
 __device__ __forceinline__ void mma_bf16(float *c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
                "{%0,%1,%2,%3};"
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void mma_f16(float *c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+               "{%0,%1,%2,%3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_e4m3(float *c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
                "{%0,%1,%2,%3};"
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
 // Two e4m3 codes (the low or high half of w) as fp16; exact.
@@ -73,21 +87,36 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<uint32_t *>(&v);
 }
-// 2^e for an integer e, clamped to the normal range.
-__device__ __forceinline__ float pow2i(int e) { return __uint_as_float(uint32_t(min(max(e, -126), 127) + 127) << 23); }
-
-// N words (1, 2, 4 or a sum of those) from an address aligned to the widest of them.
+// Wait until at most `left` (0 to 7) of this thread's latest groups are in flight.
+__device__ __forceinline__ void copies_wait(int left) {
+  switch (left) {
+    case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+    case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+    case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+    case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+    case 4: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
+    case 5: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
+    case 6: asm volatile("cp.async.wait_group 6;" ::: "memory"); break;
+    default: asm volatile("cp.async.wait_group 7;" ::: "memory"); break;
+  }
+}
+// N words of shared memory: plain loads, which the compiler may start early and order among the products as it likes.
 template <int N>
-__device__ __forceinline__ void load_words(const void *p, uint32_t *w) {
+__device__ __forceinline__ void read_words(const uint8_t *src, uint32_t *w) {
   if constexpr (N == 4) {
-    const uint4 u = __ldg(static_cast<const uint4 *>(p));
+    const uint4 u = *reinterpret_cast<const uint4 *>(src);
     w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
   } else if constexpr (N == 2) {
-    const uint2 u = __ldg(static_cast<const uint2 *>(p));
+    const uint2 u = *reinterpret_cast<const uint2 *>(src);
     w[0] = u.x, w[1] = u.y;
   } else {
-    w[0] = __ldg(static_cast<const uint32_t *>(p));
+    w[0] = *reinterpret_cast<const uint32_t *>(src);
   }
+}
+
+__device__ __forceinline__ uint32_t e4m3_codes(const float *x) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(x[0], x[1]), __NV_SATFINITE, __NV_E4M3) |
+         uint32_t(__nv_cvt_float2_to_fp8x2(make_float2(x[2], x[3]), __NV_SATFINITE, __NV_E4M3)) << 16;
 }
 
 // How a lane's share of a row lies, for head dims padded to D (32, 64, 96, 128).
@@ -100,8 +129,9 @@ struct Lay {
   static constexpr int KL = E4M3 && D % 64 != 0 ? 2 : 4;
   // V: a piece of 64 values (of 128 for e4m3 at D = 128) is spread over eight lanes, then one of 32
   static constexpr int VL0 = D == 32 ? VW : (E4M3 ? (D == 128 ? 4 : 2) : 4);
-  // 16-key blocks per warp and step: about 8 KB of loads in flight per warp
-  static constexpr int KM = D * ES >= 192 ? 1 : (D * ES >= 96 ? 2 : 4);
+  // a stage of the ring: K pieces, V pieces, then 32 scale bytes (e4m3) and the keys' factors
+  static constexpr int KBYTES = 2 * KW * 4 * 32, VBYTES = 4 * VW * 4 * 32, SBYTES = E4M3 ? 32 : 0;
+  static constexpr int BASE = KBYTES + VBYTES + SBYTES;
   // d of value v (0 .. D/8 - 1) of lane group g
   static __device__ __forceinline__ int vd(int g, int v) {
     constexpr int per0 = VL0 * 4 / ES;  // values of a piece per lane
@@ -110,188 +140,105 @@ struct Lay {
   }
 };
 
-struct Seq {
-  int prefix, count, len;
-};
+constexpr int kMaxStages = 8;
 
-__device__ __forceinline__ Seq sequence(const CacheAttnArgs &a, int b, bool check) {
-  Seq s;
-  int p = a.prefix[b], c = a.counts ? a.counts[b] : a.T;
-  const long long room = (long long)a.max_pages << a.page_shift;
-  bool bad = p < 0 || c < 0 || c > a.T;
-  p = max(p, 0);
-  c = min(max(c, 0), a.T);
-  if ((long long)p + c > room) {  // the table does not reach that far
-    bad = true;
-    p = int(min((long long)p, room));
-    c = int(min((long long)c, room - p));
-  }
-  if (bad && check) atomicOr(a.flags, kFlagRange);
-  s.prefix = p, s.count = c, s.len = c > 0 ? p + c : 0;
-  return s;
-}
-
-__device__ __forceinline__ bool drafted_visible(const CacheAttnArgs &a, int b, int t, int u) {
-  if (!a.mask) return u <= t;
-  return (a.mask[((long long)b * a.T + t) * a.mask_words + (u >> 5)] >> (u & 31)) & 1u;
-}
-
-// Position of new token u of sequence b in the factor tables.
-__device__ __forceinline__ int new_position(const CacheAttnArgs &a, int b, const Seq &s, int u) {
-  const long long p = (long long)s.prefix + (a.depths ? a.depths[(long long)b * a.T + u] : u);
-  if (p < 0 || p >= a.P) {
-    atomicOr(a.flags, kFlagRange);
-    return p < 0 ? 0 : a.P - 1;
-  }
-  return int(p);
-}
-
-// Non-finite values in a word of value codes, the word without them, and one such value (0 for a finite one).
-template <bool E4M3>
-__device__ __forceinline__ uint32_t even_word(uint32_t w) {
-  if constexpr (E4M3) {
-#pragma unroll
-    for (int i = 0; i < 32; i += 8)
-      if (((w >> i) & 0x7fu) == 0x7fu) w &= ~(0xffu << i);
-  } else {
-    if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
-    if ((w & 0x7f800000u) == 0x7f800000u) w &= 0xffffu;
-  }
-  return w;
-}
-template <bool E4M3>
-__device__ __forceinline__ bool odd_word(uint32_t w) {
-  return even_word<E4M3>(w) != w;
-}
-template <bool E4M3>
-__device__ __forceinline__ float odd_value(const uint8_t *row, int at) {
-  if constexpr (E4M3) {
-    return (row[at] & 0x7fu) == 0x7fu ? __uint_as_float(0x7fffffffu) : 0.f;
-  } else {
-    const uint32_t v = reinterpret_cast<const uint16_t *>(row)[at];
-    return (v & 0x7f80u) == 0x7f80u ? __uint_as_float(v << 16) : 0.f;
-  }
-}
-
-// Value dd of one output row, from the sums relative to exp(top); row t of a sequence that brings fewer tokens is 0.
-__device__ __forceinline__ void write_row(const CacheAttnArgs &a, const Seq &s, long long row, int t, int dd, float top,
-                                          float sum, float val) {
-  const bool none = t >= s.count || top == -INFINITY;
-  if (dd < a.d) a.O[row * a.d + dd] = __float2bfloat16_rn(none ? 0.f : val / sum);
-  if (dd == 0) a.LSE[row] = none ? -INFINITY : top + logf(sum);
-}
-
-template <int D, bool E4M3, int NB, int BIAS>
-struct Smem {
+template <int D, int NB>
+struct Join {  // over the ring, once a segment's keys are done
   float o[kWarps][8 * NB][D];
   float m[kWarps][8 * NB], l[kWarps][8 * NB], e[kWarps][8 * NB];
-  uint4 fq[BIAS == 2 ? NB * 8 * 32 : 1];  // phi_q as matrix operands: [block][16 ranks][lane]
-  int last;
 };
 
+template <int NB, int BIAS>
+struct Smem {
+  uint4 fq[BIAS == 2 ? NB * 8 * 32 : 1];  // phi_q as matrix operands: [block][16 ranks][lane]
+  int last;
+  int odd;  // a non-finite value left the products of this segment
+  int pad[2];
+};
+
+template <int D, bool E4M3, int BIAS>
+constexpr int stage_bytes(int RP) {
+  return Lay<D, E4M3>::BASE + (BIAS == 1 ? 256 : (BIAS == 2 ? RP / 16 * 2 * 512 : 0));
+}
+
 template <int D, bool E4M3, int NB, int BIAS>
-__global__ void __launch_bounds__(kWarps * 32, NB == 1 ? 3 : 2) attn_cache_kernel(const CacheAttnArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, cta_per_sm(NB)) attn_cache_kernel(const CacheAttnArgs a, const int stages) {
   using L = Lay<D, E4M3>;
-  constexpr int KM = L::KM, KS = D / 16, ROWS = 8 * NB;
-  constexpr int BK = kWarps * 16 * KM;  // keys per block
+  constexpr int KS = D / 16, ROWS = 8 * NB;
+  constexpr int BK = kBlockKeys;
   extern __shared__ __align__(16) uint8_t smem_raw[];
-  auto &sm = *reinterpret_cast<Smem<D, E4M3, NB, BIAS> *>(smem_raw);
+  auto &sm = *reinterpret_cast<Smem<NB, BIAS> *>(smem_raw);
+  auto &join = *reinterpret_cast<Join<D, NB> *>(smem_raw + sizeof(sm));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
   griddep_wait();
 
-  // ---- this CTA's run of blocks, [lo, hi) of all blocks of all items
-  const int HC = a.H * a.chunks;
-  auto blocks_of = [&](int b) {
-    const Seq s = sequence(a, b, false);
-    return max(1, (s.len + BK - 1) / BK);
-  };
-  long long total = 0;
-  for (int b0 = 0; b0 < a.B; b0 += 32) total += __reduce_add_sync(0xffffffffu, b0 + lane < a.B ? blocks_of(b0 + lane) : 0);
-  total *= HC;
-  const long long N = min((long long)gridDim.x, total);  // CTAs with work
-  if (blockIdx.x >= N) return;
-  auto first_block = [&](long long c) { return c * total / N; };
-  auto owner = [&](long long x) {  // the CTA whose run holds block x
-    long long c = x * N / total;
-    while (c + 1 < N && first_block(c + 1) <= x) ++c;
-    while (c > 0 && first_block(c) > x) --c;
-    return int(c);
-  };
-  const long long lo = first_block(blockIdx.x), hi = first_block(blockIdx.x + 1);
-  int b = 0;
-  long long bstart = 0;  // the first block of sequence b
-  for (int b0 = 0; b0 < a.B; b0 += 32) {
-    const int mine = b0 + lane < a.B ? blocks_of(b0 + lane) : 0;
-    int incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
-    }
-    const bool past = b0 + lane >= a.B || bstart + (long long)incl * HC > lo;
-    const unsigned vote = __ballot_sync(0xffffffffu, past);
-    if (vote) {
-      const int f = __ffs(vote) - 1;
-      b = b0 + f;
-      bstart += (long long)(__shfl_sync(0xffffffffu, incl, f) - __shfl_sync(0xffffffffu, mine, f)) * HC;
-      break;
-    }
-    bstart += (long long)__shfl_sync(0xffffffffu, incl, 31) * HC;
-  }
-
-  long long pos = lo;
-  while (pos < hi && b < a.B) {
-    Seq s = sequence(a, b, true);
-    const int nb = max(1, (s.len + BK - 1) / BK);
-    if (pos >= bstart + (long long)nb * HC) {
-      bstart += (long long)nb * HC;
-      ++b;
-      continue;
-    }
-    const int item = int((pos - bstart) / nb);
-    const int k0 = int((pos - bstart) - (long long)item * nb);
-    const int k1 = int(min((long long)nb, k0 + (hi - pos)));
-    const int h = item / a.chunks, r0 = (item - h * a.chunks) * ROWS;
+  // ---- this CTA's run of blocks of all items
+  Walk walk(a, BK, lane);
+  if (blockIdx.x >= walk.ctas) return;
+  Segment seg;
+  while (walk.next(a, seg)) {
+    const Seq &s = seg.s;
+    const int b = seg.b, nb = seg.blocks, k0 = seg.k0, k1 = seg.k1;
+    const int h = seg.item / a.chunks, r0 = (seg.item - h * a.chunks) * ROWS;
     const long long qrow0 = ((long long)b * a.Hq + (long long)h * a.G) * a.T;  // row r of the item is output row qrow0 + r
 
-    // ---- queries as the matrix operand: lane (g, t4) holds row g's values at the d that its key loads have
-    uint32_t qf[NB][KS][2];
-    float mult[NB][2];  // scale, and the power of two taken out of an fp16 query row
+    // ---- queries as the matrix operand: lane (g, t4) holds row g's values at the d that its key loads have. For an
+    // 8-bit cache each row is a power of two times two e4m3 parts, hi + lo / 16: with the row's largest value in
+    // (224, 448] hi holds four bits of every value and lo the four that are left of a bf16, so the sum is exact, or
+    // off by 2^-23 of the largest value where lo is subnormal. The keys' codes then are operands as they are.
+    uint32_t qf[NB][KS][2];  // bf16 pairs; e4m3: [32 d][hi words], then [32 d][lo words]
+    float mult[NB][2];       // scale, and the power of two taken out of a query row
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
       const int r = r0 + n * 8 + g;
       const bool in = r < a.rows;
       const __nv_bfloat16 *q = a.Q + (qrow0 + (in ? r : 0)) * a.d;
+      uint32_t u[KS][2];
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
         constexpr int per = L::KL * 4 / L::ES;  // values per load and lane
         const int d0 = (k * 4 / per) * (4 * per) + t4 * per + (k * 4) % per;
-        uint2 u = make_uint2(0u, 0u);
-        if (in && d0 < a.d) u = __ldg(reinterpret_cast<const uint2 *>(q + d0));
-        qf[n][k][0] = u.x, qf[n][k][1] = u.y;
+        uint2 v = make_uint2(0u, 0u);
+        if (in && d0 < a.d) v = __ldg(reinterpret_cast<const uint2 *>(q + d0));
+        u[k][0] = v.x, u[k][1] = v.y;
       }
       mult[n][0] = mult[n][1] = a.scale;
-      if constexpr (E4M3) {
-        // fp16 queries: each row times a power of two that brings its largest value to [2^14, 2^15), so that
-        // values down to 2^-38 of it keep a bit; bf16's 8 bits fit fp16's 11.
+      if constexpr (!E4M3) {
+#pragma unroll
+        for (int k = 0; k < KS; ++k) qf[n][k][0] = u[k][0], qf[n][k][1] = u[k][1];
+      } else {
         float top = 0.f;
 #pragma unroll
         for (int k = 0; k < KS; ++k)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float x0 = fabsf(__uint_as_float(qf[n][k][i] << 16)), x1 = fabsf(__uint_as_float(qf[n][k][i] & 0xffff0000u));
+            const float x0 = fabsf(__uint_as_float(u[k][i] << 16)), x1 = fabsf(__uint_as_float(u[k][i] & 0xffff0000u));
             top = fmaxf(top, fmaxf(x0 < INFINITY ? x0 : 0.f, x1 < INFINITY ? x1 : 0.f));
           }
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const int e = int(__float_as_uint(top) >> 23) - 127 - 14;
+        // top = 1.m 2^(f - 127), 448 = 1.75 2^8
+        const uint32_t bits = __float_as_uint(top);
+        const int e = int(bits >> 23) - 135 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
         const float down = pow2i(-e), up = pow2i(e);
 #pragma unroll
-        for (int k = 0; k < KS; ++k)
+        for (int k = 0; k < KS; ++k) {
+          float x[4] = {__uint_as_float(u[k][0] << 16), __uint_as_float(u[k][0] & 0xffff0000u),
+                        __uint_as_float(u[k][1] << 16), __uint_as_float(u[k][1] & 0xffff0000u)};
+          float lo[4];
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-            qf[n][k][i] = pack_f16x2(__uint_as_float(qf[n][k][i] << 16) * down,
-                                     __uint_as_float(qf[n][k][i] & 0xffff0000u) * down);
+          for (int i = 0; i < 4; ++i) {
+            x[i] *= down;
+            if (!(fabsf(x[i]) < INFINITY)) x[i] = __uint_as_float(0x7fffffffu);
+          }
+          const uint32_t h = e4m3_codes(x);
+          const uint32_t l0 = e4m3_lo(h), l1 = e4m3_hi(h);
+          const float2 f0 = __half22float2(*reinterpret_cast<const __half2 *>(&l0));
+          const float2 f1 = __half22float2(*reinterpret_cast<const __half2 *>(&l1));
+          lo[0] = (x[0] - f0.x) * 16.f, lo[1] = (x[1] - f0.y) * 16.f, lo[2] = (x[2] - f1.x) * 16.f, lo[3] = (x[3] - f1.y) * 16.f;
+          qf[n][k / 2][k & 1] = h;
+          qf[n][KS / 2 + k / 2][k & 1] = e4m3_codes(lo);
+        }
         mult[n][0] *= __shfl_sync(0xffffffffu, up, t4 * 8);
         mult[n][1] *= __shfl_sync(0xffffffffu, up, t4 * 8 + 4);
       }
@@ -343,204 +290,235 @@ __global__ void __launch_bounds__(kWarps * 32, NB == 1 ? 3 : 2) attn_cache_kerne
       for (int i = 0; i < 2; ++i) m[n][i] = -INFINITY, l[n][i] = 0.f, ex[n][i] = -INFINITY;
     }
 
+    if (threadIdx.x == 0) sm.odd = 0;
+    __syncthreads();  // sm.odd; and the last segment's readers of shared memory are done
     const int *table = a.table + (long long)b * a.max_pages;
-    const int jend = min(s.len, k1 * BK);
+    const int jend = min(s.len, k1 * BK), jstart = k0 * BK + warp * 16;
     const int hk = BIAS ? (a.fk_heads > 1 ? h : 0) : 0;
-    int pages[KM];
-    auto fetch_pages = [&](int j0) {
-#pragma unroll
-      for (int mb = 0; mb < KM; ++mb) {
-        const int j = j0 + mb * 16;
-        pages[mb] = j < jend ? __ldg(table + (j >> a.page_shift)) : 0;
+    const int stage = stage_bytes<D, E4M3, BIAS>(a.RP);
+    const uint8_t *ring = smem_raw + sizeof(sm) + warp * stages * stage;
+    auto page_of = [&](int j) { return j < jend ? __ldg(table + (j >> a.page_shift)) : 0; };
+    int next_page = page_of(jstart);
+    // Copy the group at j into ring slot `slot`; false where the table leads nowhere (zeros are copied).
+    auto fetch = [&](int j, int slot) {
+      const int page = next_page;
+      next_page = page_of(j + BK);
+      bool alive = j < jend;
+      if (alive && (page < 0 || page >= a.num_pages)) {
+        if (lane == 0) atomicOr(a.flags, kFlagRange);
+        alive = false;
       }
-    };
-    int j0 = k0 * BK + warp * 16 * KM;
-    fetch_pages(j0);
-    for (; j0 < jend; j0 += BK) {
-      // ---- loads
-      uint32_t kr[KM][2][L::KW], vr[KM][4][L::VW];
-      uint32_t sk[KM][2], sv[KM][2];
-      float fk[KM][2][BIAS == 1 ? 4 : 1];
-      int kpos[KM][2];
-      bool alive[KM];
-      long long prow[KM];
+      const long long prow = (((long long)(alive ? page : 0) * a.H + h) << a.page_shift) + (j & ((1 << a.page_shift) - 1));
+      const uint32_t dst = smem_u32(ring + slot * stage);
+      const uint8_t *kb = static_cast<const uint8_t *>(a.kp) + prow * (a.d * L::ES);
+      const uint8_t *vb = static_cast<const uint8_t *>(a.vp) + prow * (a.d * L::ES);
+      const int left = alive ? s.len - j : 0;  // keys of the group
+      if (left >= 16 && a.d == D) {  // whole rows: fixed offsets from one address a side
+        // K: the group's 16 rows lie one after the other, so the lanes take 16-byte chunks in order (a load of 64 bytes
+        // of a row brings the whole 128-byte line, half of it twice) and put each where its user will look
+        const uint8_t *vl = vb + t4 * (2 * D * L::ES) + g * (L::VL0 * 4);
+        const uint32_t vd = dst + L::KBYTES + lane * (L::VL0 * 4);
+        constexpr int cpr = D * L::ES / 16;  // chunks of a row
 #pragma unroll
-      for (int mb = 0; mb < KM; ++mb) {
-        alive[mb] = j0 + mb * 16 < jend;
-        if (alive[mb] && (pages[mb] < 0 || pages[mb] >= a.num_pages)) {
-          if (lane == 0) atomicOr(a.flags, kFlagRange);
-          alive[mb] = false;
+        for (int q = 0; q < cpr / 2; ++q) {
+          const int at = q * 32 + lane, row = at / cpr, ch = at % cpr;
+          const int piece = (row >> 3) * (L::KW / L::KL) + (L::KL == 4 ? ch >> 2 : ch >> 1);
+          const int place = (row & 7) * 4 + (L::KL == 4 ? ch & 3 : (ch & 1) * 2);
+          copy_whole<4>(dst + (piece * 32 + place) * (L::KL * 4), kb + at * 16);
         }
-        prow[mb] = (((long long)pages[mb] * a.H + h) << a.page_shift) + ((j0 + mb * 16) & ((1 << a.page_shift) - 1));
-        const uint8_t *kb = static_cast<const uint8_t *>(a.kp) + prow[mb] * (a.d * L::ES);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int jj = g + 8 * i;
-          const bool in = alive[mb] && j0 + mb * 16 + jj < s.len;
-#pragma unroll
-          for (int c = 0; c < L::KW / L::KL; ++c) {
-            constexpr int per = L::KL * 4 / L::ES;
-            const int d0 = c * 4 * per + t4 * per;
-#pragma unroll
-            for (int w = 0; w < L::KL; ++w) kr[mb][i][c * L::KL + w] = 0u;
-            if (in && d0 < a.d) load_words<L::KL>(kb + (jj * a.d + d0) * L::ES, &kr[mb][i][c * L::KL]);
-          }
-          if constexpr (E4M3) {
-            sk[mb][i] = in ? __ldg(a.ks + prow[mb] + jj) : 127u;
-            sv[mb][i] = in ? __ldg(a.vs + prow[mb] + jj) : 127u;
-          }
-        }
-      }
-#pragma unroll
-      for (int mb = 0; mb < KM; ++mb) {
-        const uint8_t *vb = static_cast<const uint8_t *>(a.vp) + prow[mb] * (a.d * L::ES);
+        constexpr int pieces = D == 96 ? 1 : L::VW / L::VL0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int jj = 2 * t4 + (i & 1) + 8 * (i >> 1);
-          const bool in = alive[mb] && j0 + mb * 16 + jj < s.len;
+          const int off = ((i & 1) + 8 * (i >> 1)) * D * L::ES;
 #pragma unroll
-          for (int w = 0; w < L::VW; ++w) vr[mb][i][w] = 0u;
-          constexpr int per = L::VL0 * 4 / L::ES;
-          constexpr int pieces = D == 96 ? 1 : L::VW / L::VL0;
+          for (int c = 0; c < pieces; ++c)
+            copy_whole<L::VL0>(vd + i * (L::VW * 4 * 32) + c * (32 * L::VL0 * 4), vl + off + c * (8 * L::VL0 * 4));
+          if constexpr (D == 96)
+            copy_whole<L::VL0 / 2>(dst + L::KBYTES + i * (L::VW * 4 * 32) + 32 * (L::VL0 * 4) + lane * (L::VL0 * 2),
+                                   vb + t4 * (2 * D * L::ES) + off + 64 * L::ES + g * (L::VL0 * 2));
+        }
+      } else {
 #pragma unroll
-          for (int c = 0; c < pieces; ++c) {
-            const int d0 = c * 8 * per + g * per;
-            if (in && d0 < a.d) load_words<L::VL0>(vb + (jj * a.d + d0) * L::ES, &vr[mb][i][c * L::VL0]);
-          }
-          if constexpr (D == 96) {
-            const int d0 = 64 + g * (per / 2);
-            if (in && d0 < a.d) load_words<L::VL0 / 2>(vb + (jj * a.d + d0) * L::ES, &vr[mb][i][L::VL0]);
+      for (int i = 0; i < 2; ++i) {
+        const int jj = g + 8 * i;
+#pragma unroll
+        for (int c = 0; c < L::KW / L::KL; ++c) {
+          constexpr int per = L::KL * 4 / L::ES;
+          const int d0 = c * 4 * per + t4 * per;
+          const bool in = jj < left && d0 < a.d;
+          copy_words<L::KL>(dst + ((i * (L::KW / L::KL) + c) * 32 + lane) * (L::KL * 4),
+                            in ? kb + (jj * a.d + d0) * L::ES : kb, in);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int jj = 2 * t4 + (i & 1) + 8 * (i >> 1);
+        constexpr int per = L::VL0 * 4 / L::ES;
+        constexpr int pieces = D == 96 ? 1 : L::VW / L::VL0;
+        const uint32_t vdst = dst + L::KBYTES + i * (L::VW * 4 * 32);
+#pragma unroll
+        for (int c = 0; c < pieces; ++c) {
+          const int d0 = c * 8 * per + g * per;
+          const bool in = jj < left && d0 < a.d;
+          copy_words<L::VL0>(vdst + (c * 32 + lane) * (L::VL0 * 4), in ? vb + (jj * a.d + d0) * L::ES : vb, in);
+        }
+        if constexpr (D == 96) {
+          const int d0 = 64 + g * (per / 2);
+          const bool in = jj < left && d0 < a.d;
+          copy_words<L::VL0 / 2>(vdst + 32 * (L::VL0 * 4) + lane * (L::VL0 * 2), in ? vb + (jj * a.d + d0) * L::ES : vb, in);
+        }
+      }
+      }
+      if constexpr (E4M3) {  // 16 scale bytes of either side: a group starts at a multiple of 16 rows
+        if (lane < 2) copy_words<4>(dst + L::KBYTES + L::VBYTES + lane * 16, (lane ? a.vs : a.ks) + prow, alive);
+      }
+      if constexpr (BIAS != 0) {
+        auto position = [&](int jj) {
+          const int jk = j + jj;
+          if (jj >= left) return 0;
+          if (jk >= s.prefix) return new_position(a, b, s, jk - s.prefix);
+          if (jk < a.P) return jk;
+          atomicOr(a.flags, kFlagRange);
+          return a.P - 1;
+        };
+        if constexpr (BIAS == 1) {
+          if (lane < 16)
+            copy_words<4>(dst + L::BASE + lane * 16, static_cast<const float4 *>(a.fk) + (long long)hk * a.P + position(lane),
+                          lane < left);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint4 *f = static_cast<const uint4 *>(a.fk) + ((long long)hk * a.P + position(g + 8 * i)) * (a.RP / 4) + t4;
+            for (int c = 0; c < a.RP / 16; ++c)
+              copy_words<4>(dst + L::BASE + ((c * 2 + i) * 32 + lane) * 16, f + c * 4, g + 8 * i < left);
           }
         }
       }
-      const bool tail = j0 + 16 * KM > s.prefix;  // drafted keys, or rows past the end
-#pragma unroll
-      for (int mb = 0; mb < KM; ++mb)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int j = j0 + mb * 16 + g + 8 * i;
-          kpos[mb][i] = j;
-          if constexpr (BIAS != 0) {
-            if (j >= s.prefix) kpos[mb][i] = j < s.len ? new_position(a, b, s, j - s.prefix) : 0;
-            if (kpos[mb][i] >= a.P) {
-              atomicOr(a.flags, kFlagRange);
-              kpos[mb][i] = a.P - 1;
-            }
-          }
-          if constexpr (BIAS == 1) {
-            const float4 f = __ldg(static_cast<const float4 *>(a.fk) + (long long)hk * a.P + kpos[mb][i]);
-            fk[mb][i][0] = f.x, fk[mb][i][1] = f.y, fk[mb][i][2] = f.z, fk[mb][i][3] = f.w;
-          }
-        }
-      fetch_pages(j0 + BK);
+      return alive;
+    };
+    unsigned alive_bits = 0;  // bit s: the group in ring slot s
+    for (int i = 0; i < stages - 1; ++i) {
+      alive_bits |= unsigned(fetch(jstart + i * BK, i)) << i;
+      copies_commit();
+    }
+    int slot = 0;
+    for (int j0 = jstart; j0 < jend; j0 += BK) {
+      const int ahead = slot == 0 ? stages - 1 : slot - 1;
+      const bool there = fetch(j0 + (stages - 1) * BK, ahead);
+      copies_commit();
+      alive_bits = (alive_bits & ~(1u << ahead)) | unsigned(there) << ahead;
+      copies_wait(stages - 1);
+      __syncwarp();  // scales and factors were copied by other lanes
+      const bool alive = (alive_bits >> slot) & 1u;
+      const uint8_t *src = ring + slot * stage;
+      const bool tail = j0 + 16 > s.prefix;  // drafted keys, or rows past the end
 
       // ---- scores: S^T = K Q^T (16 keys x 8 rows per block)
-      float x[KM][NB][4];
+      float x[NB][4], xl[NB][E4M3 ? 4 : 1];
 #pragma unroll
-      for (int mb = 0; mb < KM; ++mb) {
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[n][i] = xl[n][E4M3 ? i : 0] = 0.f;
+#pragma unroll
+      for (int c = 0; c < L::KW / L::KL; ++c) {
+        uint32_t kr[2][L::KL];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          read_words<L::KL>(src + ((i * (L::KW / L::KL) + c) * 32 + lane) * (L::KL * 4), kr[i]);
+#pragma unroll
+        for (int kk = 0; kk < L::KL / 2; ++kk) {
+          const int k = c * (L::KL / 2) + kk;
+#pragma unroll
+          for (int n = 0; n < NB; ++n) {
+            if constexpr (E4M3) {
+              mma_e4m3(x[n], kr[0][2 * kk], kr[1][2 * kk], kr[0][2 * kk + 1], kr[1][2 * kk + 1], qf[n][k][0], qf[n][k][1]);
+              mma_e4m3(xl[n], kr[0][2 * kk], kr[1][2 * kk], kr[0][2 * kk + 1], kr[1][2 * kk + 1], qf[n][KS / 2 + k][0],
+                       qf[n][KS / 2 + k][1]);
+            } else {
+              mma_bf16(x[n], kr[0][2 * kk], kr[1][2 * kk], kr[0][2 * kk + 1], kr[1][2 * kk + 1], qf[n][k][0], qf[n][k][1]);
+            }
+          }
+        }
+      }
+      if constexpr (E4M3) {
 #pragma unroll
         for (int n = 0; n < NB; ++n)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) x[mb][n][i] = 0.f;
-#pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          uint32_t a0, a1, a2, a3;
-          if constexpr (E4M3) {
-            a0 = e4m3_lo(kr[mb][0][k]), a2 = e4m3_hi(kr[mb][0][k]);
-            a1 = e4m3_lo(kr[mb][1][k]), a3 = e4m3_hi(kr[mb][1][k]);
-          } else {
-            a0 = kr[mb][0][2 * k], a2 = kr[mb][0][2 * k + 1];
-            a1 = kr[mb][1][2 * k], a3 = kr[mb][1][2 * k + 1];
-          }
-#pragma unroll
-          for (int n = 0; n < NB; ++n) {
-            if constexpr (E4M3)
-              mma_f16(x[mb][n], a0, a1, a2, a3, qf[n][k][0], qf[n][k][1]);
-            else
-              mma_bf16(x[mb][n], a0, a1, a2, a3, qf[n][k][0], qf[n][k][1]);
-          }
-        }
+          for (int i = 0; i < 4; ++i) x[n][i] = fmaf(xl[n][i], 0.0625f, x[n][i]);
       }
       // ---- scale and bias
-      float bias[KM][NB][BIAS == 2 ? 4 : 1];
+      float bias[NB][BIAS == 2 ? 4 : 1];
       if constexpr (BIAS == 2) {
+        float low[NB][4];  // the two small products
 #pragma unroll
-        for (int mb = 0; mb < KM; ++mb)
+        for (int n = 0; n < NB; ++n)
 #pragma unroll
-          for (int n = 0; n < NB; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) bias[mb][n][i] = 0.f;
-        const uint4 *fb = static_cast<const uint4 *>(a.fk) + (long long)hk * a.P * (a.RP / 4) + t4;
+          for (int i = 0; i < 4; ++i) bias[n][i] = low[n][i] = 0.f;
         for (int c = 0; c < a.RP / 16; ++c) {
-          uint4 f[KM][2];
+          uint32_t f[2][4];  // 4 hi, 4 lo
 #pragma unroll
-          for (int mb = 0; mb < KM; ++mb)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) f[mb][i] = __ldg(fb + (long long)kpos[mb][i] * (a.RP / 4) + c * 4);
+          for (int i = 0; i < 2; ++i) read_words<4>(src + L::BASE + ((c * 2 + i) * 32 + lane) * 16, f[i]);
 #pragma unroll
           for (int n = 0; n < NB; ++n) {
             const uint4 q = sm.fq[(n * 8 + c) * 32 + lane];
             // (kh + kl)(qh + ql) without the last 2^-22
-#pragma unroll
-            for (int mb = 0; mb < KM; ++mb) {
-              mma_f16(bias[mb][n], f[mb][0].z, f[mb][1].z, f[mb][0].w, f[mb][1].w, q.x, q.y);
-              mma_f16(bias[mb][n], f[mb][0].x, f[mb][1].x, f[mb][0].y, f[mb][1].y, q.z, q.w);
-              mma_f16(bias[mb][n], f[mb][0].x, f[mb][1].x, f[mb][0].y, f[mb][1].y, q.x, q.y);
-            }
+            mma_f16(low[n], f[0][2], f[1][2], f[0][3], f[1][3], q.x, q.y);
+            mma_f16(bias[n], f[0][0], f[1][0], f[0][1], f[1][1], q.x, q.y);
+            mma_f16(low[n], f[0][0], f[1][0], f[0][1], f[1][1], q.z, q.w);
           }
         }
-      }
-      uint32_t need = 0;
 #pragma unroll
-      for (int mb = 0; mb < KM; ++mb)
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) bias[n][i] += low[n][i];
+      }
+      float fk[2][BIAS == 1 ? 4 : 1], skf[2], svf[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if constexpr (BIAS == 1) read_words<4>(src + L::BASE + (g + 8 * i) * 16, reinterpret_cast<uint32_t *>(fk[i]));
+        skf[i] = svf[i] = 0.f;
+        if constexpr (E4M3) {
+          const uint32_t k8 = src[L::KBYTES + L::VBYTES + g + 8 * i], v8 = src[L::KBYTES + L::VBYTES + 16 + g + 8 * i];
+          skf[i] = k8 == 255u ? __uint_as_float(0x7fffffffu) : pow2i(int(k8) - 127);
+          svf[i] = v8 == 255u ? __uint_as_float(0x7fffffffu) : float(int(v8) - 127);
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int kk = i >> 1, rr = i & 1;
+          float f = mult[n][rr];
+          if constexpr (E4M3) f *= skf[kk];
+          if constexpr (BIAS == 1) {
+            float y = fk[kk][0] * fq[n][rr][0];
+#pragma unroll
+            for (int r = 1; r < 4; ++r) y = fmaf(fk[kk][r], fq[n][rr][r], y);
+            x[n][i] = fmaf(x[n][i], f, y);
+          } else if constexpr (BIAS == 2) {
+            x[n][i] = fmaf(x[n][i], f, bias[n][i]);
+          } else {
+            x[n][i] *= f;
+          }
+        }
+      if (tail || !alive) {
 #pragma unroll
         for (int n = 0; n < NB; ++n)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int kk = i >> 1, rr = i & 1;
-            float f = mult[n][rr];
-            if constexpr (E4M3) f *= sk[mb][kk] == 255u ? __uint_as_float(0x7fffffffu) : pow2i(int(sk[mb][kk]) - 127);
-            if constexpr (BIAS == 1) {
-              float y = fk[mb][kk][0] * fq[n][rr][0];
-#pragma unroll
-              for (int r = 1; r < 4; ++r) y = fmaf(fk[mb][kk][r], fq[n][rr][r], y);
-              x[mb][n][i] = fmaf(x[mb][n][i], f, y);
-            } else if constexpr (BIAS == 2) {
-              x[mb][n][i] = fmaf(x[mb][n][i], f, bias[mb][n][i]);
-            } else {
-              x[mb][n][i] *= f;
-            }
-          }
-      if (tail) {
-#pragma unroll
-        for (int mb = 0; mb < KM; ++mb)
-#pragma unroll
-          for (int n = 0; n < NB; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int j = j0 + mb * 16 + g + 8 * (i >> 1), u = j - s.prefix, t = tok[n][i & 1];
-              const bool see = alive[mb] && j < s.len && (u < 0 || (t >= 0 && drafted_visible(a, b, t, u)));
-              if (!see) x[mb][n][i] = -INFINITY;
-            }
-      } else {
-#pragma unroll
-        for (int mb = 0; mb < KM; ++mb)
-          if (!alive[mb]) {
-#pragma unroll
-            for (int n = 0; n < NB; ++n)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) x[mb][n][i] = -INFINITY;
+            const int j = j0 + g + 8 * (i >> 1), u = j - s.prefix, t = tok[n][i & 1];
+            const bool see = alive && j < s.len && (u < 0 || (t >= 0 && drafted_visible(a, b, t, u)));
+            if (!see) x[n][i] = -INFINITY;
           }
       }
       // ---- running maximum, raised only when a score passes it by more than 8 (exp stays below e^8)
       float top[NB][2];
+      bool need = false;
 #pragma unroll
       for (int n = 0; n < NB; ++n)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          top[n][i] = -INFINITY;
-#pragma unroll
-          for (int mb = 0; mb < KM; ++mb) top[n][i] = fmaxf(top[n][i], fmaxf(x[mb][n][i], x[mb][n][i + 2]));
+          top[n][i] = fmaxf(x[n][i], x[n][i + 2]);
           need |= top[n][i] > m[n][i] + 8.f;
         }
       if (__any_sync(0xffffffffu, need)) {
@@ -553,7 +531,7 @@ __global__ void __launch_bounds__(kWarps * 32, NB == 1 ? 3 : 2) attn_cache_kerne
             for (int w = 4; w < 32; w <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, w));
             const float mn = fmaxf(m[n][i], v);
             if (mn > m[n][i]) {
-              const float down = (m[n][i] - mn) * kLog2e;  // -inf at the first
+              const float down = (m[n][i] - mn) * kCacheLog2e;  // -inf at the first
               const float alpha = ex2_approx(down);
               l[n][i] *= alpha;
               if constexpr (E4M3) {
@@ -567,15 +545,9 @@ __global__ void __launch_bounds__(kWarps * 32, NB == 1 ? 3 : 2) attn_cache_kerne
           }
       }
       // ---- probabilities; e4m3 values: each key's weight takes the value row's power of two, fp16 in O's unit
-      uint32_t pf[KM][NB][2];
+      uint32_t pf[NB][2];
       if constexpr (E4M3) {
-        float svf[KM][2];
-#pragma unroll
-        for (int mb = 0; mb < KM; ++mb)
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            svf[mb][i] = sv[mb][i] == 255u ? __uint_as_float(0x7fffffffu) : float(int(sv[mb][i]) - 127);
-        uint32_t grow = 0;
+        bool grow = false;
         float ytop[NB][2];
 #pragma unroll
         for (int n = 0; n < NB; ++n)
@@ -584,14 +556,12 @@ __global__ void __launch_bounds__(kWarps * 32, NB == 1 ? 3 : 2) attn_cache_kerne
             const float mu = m[n][i] == -INFINITY ? 0.f : m[n][i];
             ytop[n][i] = -INFINITY;
 #pragma unroll
-            for (int mb = 0; mb < KM; ++mb)
-#pragma unroll
-              for (int kk = 0; kk < 2; ++kk) {
-                const float y = (x[mb][n][2 * kk + i] - mu) * kLog2e;
-                x[mb][n][2 * kk + i] = y;
-                l[n][i] += ex2_approx(y);
-                ytop[n][i] = fmaxf(ytop[n][i], y + svf[mb][kk]);
-              }
+            for (int kk = 0; kk < 2; ++kk) {
+              const float y = (x[n][2 * kk + i] - mu) * kCacheLog2e;
+              x[n][2 * kk + i] = y;
+              l[n][i] += ex2_approx(y);
+              ytop[n][i] = fmaxf(ytop[n][i], y + svf[kk]);
+            }
             grow |= ytop[n][i] - 15.f > ex[n][i];  // the largest weight is kept below 2^15
           }
         if (__any_sync(0xffffffffu, grow)) {
@@ -612,101 +582,92 @@ __global__ void __launch_bounds__(kWarps * 32, NB == 1 ? 3 : 2) attn_cache_kerne
             }
         }
 #pragma unroll
-        for (int mb = 0; mb < KM; ++mb)
+        for (int n = 0; n < NB; ++n) {
 #pragma unroll
-          for (int n = 0; n < NB; ++n) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float y = x[mb][n][i];
-              x[mb][n][i] = y == -INFINITY ? 0.f : ex2_approx(y + (svf[mb][i >> 1] - ex[n][i & 1]));
-            }
-            pf[mb][n][0] = transpose8x8(pack_f16x2(x[mb][n][0], x[mb][n][1]));
-            pf[mb][n][1] = transpose8x8(pack_f16x2(x[mb][n][2], x[mb][n][3]));
+          for (int i = 0; i < 4; ++i) {
+            const float y = x[n][i];
+            x[n][i] = y == -INFINITY ? 0.f : ex2_approx(y + (svf[i >> 1] - ex[n][i & 1]));
           }
+          pf[n][0] = transpose8x8(pack_f16x2(x[n][0], x[n][1]));
+          pf[n][1] = transpose8x8(pack_f16x2(x[n][2], x[n][3]));
+        }
       } else {
-        // weights rounded to bf16 (2^-9 each, independent, next to O's own rounding); their sum stays fp32
+        // weights rounded to bf16 (2^-8 at most, each its own, next to O's own rounding); their sum stays fp32
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
           const float m0 = m[n][0] == -INFINITY ? 0.f : m[n][0], m1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
 #pragma unroll
-          for (int mb = 0; mb < KM; ++mb) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              x[mb][n][i] = ex2_approx((x[mb][n][i] - (i & 1 ? m1 : m0)) * kLog2e);
-              l[n][i & 1] += x[mb][n][i];
-            }
-            pf[mb][n][0] = transpose8x8(pack_bf16x2(x[mb][n][0], x[mb][n][1]));
-            pf[mb][n][1] = transpose8x8(pack_bf16x2(x[mb][n][2], x[mb][n][3]));
+          for (int i = 0; i < 4; ++i) {
+            x[n][i] = ex2_approx((x[n][i] - (i & 1 ? m1 : m0)) * kCacheLog2e);
+            l[n][i & 1] += x[n][i];
           }
-        }
-      }
-      // ---- a drafted value that is infinite or NaN must not reach the rows that do not see it (0 * inf): it
-      // leaves the product and is added to the rows that do
-      if (tail) {
-        bool odd = false;
-#pragma unroll
-        for (int mb = 0; mb < KM; ++mb)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int w = 0; w < L::VW; ++w) odd |= odd_word<E4M3>(vr[mb][i][w]);
-        if (__any_sync(0xffffffffu, odd)) {
-#pragma unroll
-          for (int mb = 0; mb < KM; ++mb) {
-            if (!alive[mb]) continue;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-              for (int w = 0; w < L::VW; ++w) vr[mb][i][w] = even_word<E4M3>(vr[mb][i][w]);
-            const uint8_t *vb = static_cast<const uint8_t *>(a.vp) + prow[mb] * (a.d * L::ES);
-            for (int jj = 0; jj < 16; ++jj) {
-              const int j = j0 + mb * 16 + jj, u = j - s.prefix;
-              if (j >= s.len) break;
-#pragma unroll
-              for (int n = 0; n < NB; ++n)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                  const int t = tok[n][i];
-                  if (!(u < 0 || (t >= 0 && drafted_visible(a, b, t, u)))) continue;
-#pragma unroll
-                  for (int v = 0; v < D / 8; ++v) {
-                    const int dd = L::vd(g, v);
-                    const float bad = dd < a.d ? odd_value<E4M3>(vb, jj * a.d + dd) : 0.f;
-                    o[v / 2][n][(v & 1) * 2 + i] += bad;
-                  }
-                }
-            }
-          }
+          pf[n][0] = transpose8x8(pack_bf16x2(x[n][0], x[n][1]));
+          pf[n][1] = transpose8x8(pack_bf16x2(x[n][2], x[n][3]));
         }
       }
       // ---- O^T += V^T P^T
+      constexpr int VP = L::VL0;
+      constexpr int pieces = L::VW / VP + (D == 96 ? 1 : 0);
 #pragma unroll
-      for (int mb = 0; mb < KM; ++mb)
+      for (int c = 0; c < pieces; ++c) {
+        constexpr int full = D == 96 ? 1 : pieces;
+        const bool last = c >= full;  // the half piece of D = 96
+        uint32_t vr[4][VP];
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
+        for (int i = 0; i < 4; ++i) {
+          const uint8_t *vsrc = src + L::KBYTES + i * (L::VW * 4 * 32);
+          if (!last)
+            read_words<VP>(vsrc + (c * 32 + lane) * (VP * 4), vr[i]);
+          else
+            read_words<(VP + 1) / 2>(vsrc + 32 * (VP * 4) + lane * (VP * 2), vr[i]);
+        }
+        // an infinite or NaN value must not reach the rows that do not see its key (0 * inf): where new tokens are
+        // among the keys it leaves the product, and the rows that see it get it back when the segment is joined
+        if (tail) {
+          bool odd = false;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int w = 0; w < VP; ++w) {
+              if (last && w >= VP / 2) continue;
+              const uint32_t even = even_word<E4M3>(vr[i][w]);
+              odd |= even != vr[i][w];
+              vr[i][w] = even;
+            }
+          if (odd) sm.odd = 1;
+        }
+        constexpr int per = E4M3 ? VP * 2 : VP;  // products per piece
+#pragma unroll
+        for (int kk = 0; kk < per; ++kk) {
+          if (last && kk >= per / 2) continue;
+          const int k = c * per + kk;
           uint32_t a0, a1, a2, a3;
           if constexpr (E4M3) {
-            const int w = k / 2;
-            const uint32_t sel = k & 1 ? 0x7362u : 0x5140u;  // the two keys' bytes side by side
-            const uint32_t u = __byte_perm(vr[mb][0][w], vr[mb][1][w], sel);
-            const uint32_t v = __byte_perm(vr[mb][2][w], vr[mb][3][w], sel);
+            const int w = kk / 2;
+            const uint32_t sel = kk & 1 ? 0x7362u : 0x5140u;  // the two keys' bytes side by side
+            const uint32_t u = __byte_perm(vr[0][w], vr[1][w], sel);
+            const uint32_t v = __byte_perm(vr[2][w], vr[3][w], sel);
             a0 = e4m3_lo(u), a1 = e4m3_hi(u), a2 = e4m3_lo(v), a3 = e4m3_hi(v);
           } else {
-            a0 = __byte_perm(vr[mb][0][k], vr[mb][1][k], 0x5410), a1 = __byte_perm(vr[mb][0][k], vr[mb][1][k], 0x7632);
-            a2 = __byte_perm(vr[mb][2][k], vr[mb][3][k], 0x5410), a3 = __byte_perm(vr[mb][2][k], vr[mb][3][k], 0x7632);
+            a0 = __byte_perm(vr[0][kk], vr[1][kk], 0x5410), a1 = __byte_perm(vr[0][kk], vr[1][kk], 0x7632);
+            a2 = __byte_perm(vr[2][kk], vr[3][kk], 0x5410), a3 = __byte_perm(vr[2][kk], vr[3][kk], 0x7632);
           }
 #pragma unroll
           for (int n = 0; n < NB; ++n) {
             if constexpr (E4M3)
-              mma_f16(o[k][n], a0, a1, a2, a3, pf[mb][n][0], pf[mb][n][1]);
+              mma_f16(o[k][n], a0, a1, a2, a3, pf[n][0], pf[n][1]);
             else
-              mma_bf16(o[k][n], a0, a1, a2, a3, pf[mb][n][0], pf[mb][n][1]);
+              mma_bf16(o[k][n], a0, a1, a2, a3, pf[n][0], pf[n][1]);
           }
         }
+      }
+      slot = slot + 1 == stages ? 0 : slot + 1;
+      __syncwarp();  // the slot's readers are done before it is filled again
     }
+    copies_wait(0);
 
+    __syncthreads();  // the ring becomes the join's memory
     // ---- the warps' parts of the segment
-    __syncthreads();  // the last segment's readers of shared memory are done
 #pragma unroll
     for (int n = 0; n < NB; ++n)
 #pragma unroll
@@ -715,38 +676,38 @@ __global__ void __launch_bounds__(kWarps * 32, NB == 1 ? 3 : 2) attn_cache_kerne
 #pragma unroll
         for (int w = 4; w < 32; w <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
         const int row = n * 8 + 2 * t4 + i;
-        if (g == 0) sm.m[warp][row] = m[n][i], sm.l[warp][row] = sum, sm.e[warp][row] = E4M3 ? ex[n][i] : 0.f;
+        if (g == 0) join.m[warp][row] = m[n][i], join.l[warp][row] = sum, join.e[warp][row] = E4M3 ? ex[n][i] : 0.f;
 #pragma unroll
-        for (int v = 0; v < D / 8; ++v) sm.o[warp][row][L::vd(g, v)] = o[v / 2][n][(v & 1) * 2 + i];
+        for (int v = 0; v < D / 8; ++v) join.o[warp][row][L::vd(g, v)] = o[v / 2][n][(v & 1) * 2 + i];
       }
     __syncthreads();
     const bool whole = k0 == 0 && k1 == nb;
     const int nrows = min(ROWS, a.rows - r0);
     constexpr long long kSlot = ROWS * (D + 2);
-    float *slot = a.part + (2ll * blockIdx.x + (k0 == 0)) * kSlot;
+    float *mine = a.part + (2ll * blockIdx.x + (k0 == 0)) * kSlot;
     for (int i = threadIdx.x; i < nrows * D; i += kWarps * 32) {
       const int row = i / D, dd = i % D;
-      float top = sm.m[0][row];
+      float top = join.m[0][row];
 #pragma unroll
-      for (int w = 1; w < kWarps; ++w) top = fmaxf(top, sm.m[w][row]);
+      for (int w = 1; w < kWarps; ++w) top = fmaxf(top, join.m[w][row]);
       float sum = 0.f, val = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        if (sm.m[w][row] == -INFINITY) continue;
-        const float y = (sm.m[w][row] - top) * kLog2e;
-        sum += sm.l[w][row] * ex2_approx(y);
-        val += sm.o[w][row][dd] * ex2_approx(y + sm.e[w][row]);
+        if (join.m[w][row] == -INFINITY) continue;
+        const float y = (join.m[w][row] - top) * kCacheLog2e;
+        sum += join.l[w][row] * ex2_approx(y);
+        val += join.o[w][row][dd] * ex2_approx(y + join.e[w][row]);
       }
+      if (sm.odd && dd < a.d) val += odd_sum<E4M3>(a, s, b, h, (r0 + row) % a.T, dd, max(k0 * BK, s.prefix / 16 * 16), jend);
       if (whole) {
         write_row(a, s, qrow0 + r0 + row, (r0 + row) % a.T, dd, top, sum, val);
       } else {
-        slot[row * (D + 2) + dd] = val;
-        if (dd == 0) slot[row * (D + 2) + D] = top, slot[row * (D + 2) + D + 1] = sum;
+        mine[row * (D + 2) + dd] = val;
+        if (dd == 0) mine[row * (D + 2) + D] = top, mine[row * (D + 2) + D + 1] = sum;
       }
     }
     if (!whole) {
-      const long long start = bstart + (long long)item * nb;
-      const int c0 = owner(start), c1 = owner(start + nb - 1);
+      const int c0 = walk.owner(seg.start), c1 = walk.owner(seg.start + nb - 1);
       __threadfence();
       __syncthreads();
       if (threadIdx.x == 0) sm.last = atomicAdd(a.counters + c0, 1u) == unsigned(c1 - c0);
@@ -762,7 +723,7 @@ __global__ void __launch_bounds__(kWarps * 32, NB == 1 ? 3 : 2) attn_cache_kerne
             if (mc == -INFINITY) continue;
             const float sc = __ldcg(p + D + 1), vc = __ldcg(p + dd);
             const float mn = fmaxf(top, mc);
-            const float f0 = ex2_approx((top - mn) * kLog2e), f1 = ex2_approx((mc - mn) * kLog2e);
+            const float f0 = ex2_approx((top - mn) * kCacheLog2e), f1 = ex2_approx((mc - mn) * kCacheLog2e);
             sum = sum * f0 + sc * f1;
             val = val * f0 + vc * f1;
             top = mn;
@@ -772,28 +733,40 @@ __global__ void __launch_bounds__(kWarps * 32, NB == 1 ? 3 : 2) attn_cache_kerne
         if (threadIdx.x == 0) a.counters[c0] = 0u;  // for the next call
       }
     }
-    pos += k1 - k0;
   }
 }
 
+template <int D, bool E4M3, int NB, int BIAS>
+cudaError_t launch_bias(const CacheAttnArgs &a, int sms, cudaStream_t st) {
+  auto *k = attn_cache_kernel<D, E4M3, NB, BIAS>;
+  const int stage = kWarps * stage_bytes<D, E4M3, BIAS>(a.RP);
+  const int fixed = sizeof(Smem<NB, BIAS>), join = sizeof(Join<D, NB>);
+  // CTAs on an SM: as many as leave each a ring of three stages in the 227 KB (1 KB a CTA is the system's); every
+  // CTA of the grid is resident, so the equal runs of keys also end together
+  int ctas = cta_per_sm(NB) + 1, stages = 0;
+  while (stages < 3 && ctas > 1) {
+    --ctas;
+    stages = std::min(kMaxStages, (227 * 1024 / ctas - 1024 - fixed) / stage);
+  }
+  stages = std::max(2, stages);
+  const int smem = fixed + std::max(join, stages * stage);
+  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const long long blocks = std::max<long long>(1, (((long long)a.max_pages << a.page_shift) + kBlockKeys - 1) / kBlockKeys);
+  const int grid = int(std::min<long long>((long long)a.B * a.H * a.chunks * blocks, (long long)sms * ctas));
+  return launch_programmatic(k, dim3(unsigned(grid)), dim3(kWarps * 32), size_t(smem), st, a, stages);
+}
+
 template <int D, bool E4M3, int NB>
-cudaError_t launch_nb(const CacheAttnArgs &a, int grid, cudaStream_t st) {
-  const int bias = a.R == 0 ? 0 : (a.R <= kCacheBiasExact ? 1 : 2);
-  void (*k)(const CacheAttnArgs) = bias == 0 ? attn_cache_kernel<D, E4M3, NB, 0>
-                                             : (bias == 1 ? attn_cache_kernel<D, E4M3, NB, 1> : attn_cache_kernel<D, E4M3, NB, 2>);
-  const size_t smem = bias == 2 ? sizeof(Smem<D, E4M3, NB, 2>) : sizeof(Smem<D, E4M3, NB, 0>);
-  static_assert(sizeof(Smem<D, E4M3, NB, 2>) <= 48 * 1024, "shared memory without opting in");
-  return launch_programmatic(k, dim3(unsigned(grid)), dim3(kWarps * 32), smem, st, a);
+cudaError_t launch_nb(CacheAttnArgs &a, int sms, cudaStream_t st) {
+  a.chunks = (a.rows + 8 * NB - 1) / (8 * NB);
+  if (a.R == 0) return launch_bias<D, E4M3, NB, 0>(a, sms, st);
+  return a.R <= kCacheBiasExact ? launch_bias<D, E4M3, NB, 1>(a, sms, st) : launch_bias<D, E4M3, NB, 2>(a, sms, st);
 }
 
 template <int D, bool E4M3>
 cudaError_t launch_d(CacheAttnArgs &a, int sms, cudaStream_t st) {
-  constexpr int BK = kWarps * 16 * Lay<D, E4M3>::KM;
-  const int nb = a.rows <= 8 ? 1 : 2;
-  a.chunks = (a.rows + 8 * nb - 1) / (8 * nb);
-  const long long most = (long long)a.B * a.H * a.chunks * ((((long long)a.max_pages << a.page_shift) + BK - 1) / BK);
-  const int grid = int(std::min<long long>(most, (long long)sms * (nb == 1 ? 3 : 2)));
-  return nb == 1 ? launch_nb<D, E4M3, 1>(a, grid, st) : launch_nb<D, E4M3, 2>(a, grid, st);
+  return a.rows <= 8 ? launch_nb<D, E4M3, 1>(a, sms, st) : launch_nb<D, E4M3, 2>(a, sms, st);
 }
 
 }  // namespace
@@ -801,16 +774,18 @@ cudaError_t launch_d(CacheAttnArgs &a, int sms, cudaStream_t st) {
 size_t cache_attn_part_floats(int d, int T, int G, int sms) {
   const int nb = (long long)T * G <= 8 ? 1 : 2;
   const int D = (d + 31) / 32 * 32;
-  return size_t(2) * sms * (nb == 1 ? 3 : 2) * (8 * nb) * (D + 2);
+  return size_t(2) * sms * cta_per_sm(nb) * (8 * nb) * (D + 2);
 }
 
 cudaError_t launch_attn_cache(CacheAttnArgs a, int e4m3, int sms, cudaStream_t st) {
   const int D = (a.d + 31) / 32;
   if (e4m3)
     return D == 1 ? launch_d<32, true>(a, sms, st)
-                  : (D == 2 ? launch_d<64, true>(a, sms, st) : (D == 3 ? launch_d<96, true>(a, sms, st) : launch_d<128, true>(a, sms, st)));
+                  : (D == 2 ? launch_d<64, true>(a, sms, st)
+                            : (D == 3 ? launch_d<96, true>(a, sms, st) : launch_d<128, true>(a, sms, st)));
   return D == 1 ? launch_d<32, false>(a, sms, st)
-                : (D == 2 ? launch_d<64, false>(a, sms, st) : (D == 3 ? launch_d<96, false>(a, sms, st) : launch_d<128, false>(a, sms, st)));
+                : (D == 2 ? launch_d<64, false>(a, sms, st)
+                          : (D == 3 ? launch_d<96, false>(a, sms, st) : launch_d<128, false>(a, sms, st)));
 }
 
 }  // namespace fb

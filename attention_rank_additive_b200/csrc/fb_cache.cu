@@ -29,7 +29,8 @@ struct CacheArgs {
   int B, H, N, d, page, shift;       // N: tokens a sequence at most; page = 1 << shift
   int num_pages, max_pages;
   const int *table, *starts, *counts;
-  int lanes, lanes_shift;  // lanes of a row, a power of two
+  int lanes, lanes_shift;            // lanes of a row, a power of two
+  int tok_shift, head_shift;         // a block: 2^tok_shift tokens by 2^head_shift heads, and kSteps such blocks of tokens
   int *flags;
 };
 
@@ -72,21 +73,19 @@ __device__ __forceinline__ long long pool_row(const CacheArgs &a, int b, int h, 
   return ((long long)page * a.H + h) * a.page + (pos & (a.page - 1));
 }
 
-// Which row this thread's group of lanes works on: h fastest above tokens.
+// Which rows this thread's group of lanes works on: n, n + step, ...
+constexpr int kSteps = 4;
 struct Row {
-  int b, h, n, lane;
-  bool ok;
+  int b, h, n, step, lane;
 };
 __device__ __forceinline__ Row row_of(const CacheArgs &a) {
-  const long long id = blockIdx.x * (long long)blockDim.x + threadIdx.x;
-  const long long row = id >> a.lanes_shift;
   Row r;
-  r.lane = int(id & (a.lanes - 1));
-  r.ok = row < (long long)a.B * a.H * a.N;
-  r.n = int(row % a.N);
-  const long long bh = row / a.N;
-  r.h = int(bh % a.H);
-  r.b = int(bh / a.H);
+  const int row = threadIdx.x >> a.lanes_shift;
+  r.lane = threadIdx.x & (a.lanes - 1);
+  r.b = blockIdx.x;
+  r.h = (blockIdx.z << a.head_shift) + (row >> a.tok_shift);
+  r.step = 1 << a.tok_shift;
+  r.n = blockIdx.y * (kSteps << a.tok_shift) + (row & (r.step - 1));
   return r;
 }
 
@@ -94,42 +93,87 @@ template <typename T, bool E4M3>
 __global__ void __launch_bounds__(256) cache_write_kernel(const CacheArgs a) {
   const Row r = row_of(a);
   griddep_wait();
-  bool live = r.ok && r.n < (a.counts ? a.counts[r.b] : a.N);
-  long long row = -1;
-  if (live) row = pool_row(a, r.b, r.h, (long long)a.starts[r.b] + r.n);
-  live = row >= 0 && r.lane * 8 < a.d;
+  const int count = r.h < a.H ? min(a.counts ? a.counts[r.b] : a.N, a.N) : 0;
+  const long long start = a.starts[r.b];
 #pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    float x[8];
-    if (live) {
-      const long long at = w ? r.b * a.yb + r.h * a.yh + r.n * a.yn : r.b * a.xb + r.h * a.xh + r.n * a.xn;
-      load8(static_cast<const T *>(a.src[w]) + at + r.lane * 8, x);
-    } else {
+  for (int i = 0; i < kSteps; ++i) {
+    const int n = r.n + i * r.step;
+    if (__all_sync(0xffffffffu, n >= count)) break;
+    long long row = -1;
+    if (n < count) row = pool_row(a, r.b, r.h, start + n);
+    const bool live = row >= 0 && r.lane * 8 < a.d;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = 0.f;
-    }
-    if constexpr (!E4M3) {
-      if (live) store8(static_cast<__nv_bfloat16 *>(a.dst[w]) + row * a.d + r.lane * 8, x);
-    } else {
-      // the row's largest finite magnitude
-      float top = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float m = fabsf(x[i]);
-        top = fmaxf(top, m < INFINITY ? m : 0.f);
-      }
-      for (int o = a.lanes >> 1; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      // top = 1.m 2^(f - 127); the scale's exponent is f - 127 - 8, one more where 1.m > 1.75 (448 = 1.75 2^8)
-      const uint32_t bits = __float_as_uint(top);
-      int e = int(bits >> 23) - 135 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
-      e = max(e, -126);
-      const float inv = __uint_as_float(uint32_t(127 - e) << 23);
+    for (int w = 0; w < 2; ++w) {
+      float x[8];
       if (live) {
-        const uint32_t lo = e4m3x2(x[0] * inv, x[1] * inv) | (e4m3x2(x[2] * inv, x[3] * inv) << 16);
-        const uint32_t hi = e4m3x2(x[4] * inv, x[5] * inv) | (e4m3x2(x[6] * inv, x[7] * inv) << 16);
-        *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(a.dst[w]) + row * a.d + r.lane * 8) = make_uint2(lo, hi);
-        if (r.lane == 0) a.scale[w][row] = uint8_t(e + 127);
+        const long long at = w ? r.b * a.yb + r.h * a.yh + n * a.yn : r.b * a.xb + r.h * a.xh + n * a.xn;
+        load8(static_cast<const T *>(a.src[w]) + at + r.lane * 8, x);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = 0.f;
       }
+      if constexpr (!E4M3) {
+        if (live) store8(static_cast<__nv_bfloat16 *>(a.dst[w]) + row * a.d + r.lane * 8, x);
+      } else {
+        // the row's largest finite magnitude
+        float top = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float m = fabsf(x[k]);
+          top = fmaxf(top, m < INFINITY ? m : 0.f);
+        }
+        for (int o = a.lanes >> 1; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        // top = 1.m 2^(f - 127); the scale's exponent is f - 127 - 8, one more where 1.m > 1.75 (448 = 1.75 2^8)
+        const uint32_t bits = __float_as_uint(top);
+        int e = int(bits >> 23) - 135 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
+        e = max(e, -126);
+        const float inv = __uint_as_float(uint32_t(127 - e) << 23);
+        if (live) {
+          const uint32_t lo = e4m3x2(x[0] * inv, x[1] * inv) | (e4m3x2(x[2] * inv, x[3] * inv) << 16);
+          const uint32_t hi = e4m3x2(x[4] * inv, x[5] * inv) | (e4m3x2(x[6] * inv, x[7] * inv) << 16);
+          *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(a.dst[w]) + row * a.d + r.lane * 8) = make_uint2(lo, hi);
+          if (r.lane == 0) a.scale[w][row] = uint8_t(e + 127);
+        }
+      }
+    }
+  }
+}
+
+// Eight values of a pool row.
+template <bool E4M3>
+struct Piece {
+  uint4 v;  // bf16, or codes in x, y and the scale byte in z
+};
+template <bool E4M3>
+__device__ __forceinline__ Piece<E4M3> fetch(const void *pool, const uint8_t *scale, long long row, int d, int lane) {
+  Piece<E4M3> p;
+  if constexpr (E4M3) {
+    const uint2 u = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(pool) + row * d + lane * 8));
+    p.v = make_uint4(u.x, u.y, __ldg(scale + row), 0u);
+  } else {
+    p.v = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(pool) + row * d + lane * 8));
+  }
+  return p;
+}
+template <bool E4M3>
+__device__ __forceinline__ void expand(const Piece<E4M3> &p, float *x) {
+  if constexpr (E4M3) {
+    // 2^(s - 127); s = 0 is 2^-127, a subnormal
+    const float scale = __uint_as_float(p.v.z ? p.v.z << 23 : 0x400000u);
+    const uint32_t v[2] = {p.v.x, p.v.y};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(v[i / 2] >> (16 * (i % 2))), __NV_E4M3);
+      const float2 f = __half22float2(__half2(h));
+      x[2 * i] = f.x * scale;
+      x[2 * i + 1] = f.y * scale;
+    }
+  } else {
+    const uint32_t w[4] = {p.v.x, p.v.y, p.v.z, p.v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
   }
 }
@@ -138,35 +182,32 @@ template <typename T, bool E4M3>
 __global__ void __launch_bounds__(256) cache_read_kernel(const CacheArgs a) {
   const Row r = row_of(a);
   griddep_wait();
-  if (!r.ok || r.lane * 8 >= a.d) return;
-  long long row = -1;
-  if (r.n < (a.counts ? a.counts[r.b] : a.N))
-    row = pool_row(a, r.b, r.h, (long long)(a.starts ? a.starts[r.b] : 0) + r.n);
-  const long long out = (((long long)r.b * a.H + r.h) * a.N + r.n) * a.d + r.lane * 8;
+  if (r.h >= a.H || r.lane * 8 >= a.d) return;
+  const int count = a.counts ? a.counts[r.b] : a.N;
+  const long long start = a.starts ? a.starts[r.b] : 0;
+  Piece<E4M3> p[kSteps][2];  // all loads before the first store: a step costs one memory latency
 #pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    float x[8];
+  for (int i = 0; i < kSteps; ++i) {
+    const int n = r.n + i * r.step;
+    long long row = -1;
+    if (n < count && n < a.N) row = pool_row(a, r.b, r.h, start + n);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = 0.f;
-    if (row >= 0) {
-      if constexpr (E4M3) {
-        const uint2 u = *reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(a.src[w]) + row * a.d + r.lane * 8);
-        // 2^(s - 127); s = 0 is 2^-127, a subnormal
-        const uint32_t s = a.scale[w][row];
-        const float scale = __uint_as_float(s ? s << 23 : 0x400000u);
-        const uint32_t v[2] = {u.x, u.y};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(v[i / 2] >> (16 * (i % 2))), __NV_E4M3);
-          const float2 f = __half22float2(__half2(h));
-          x[2 * i] = f.x * scale;
-          x[2 * i + 1] = f.y * scale;
-        }
-      } else {
-        load8(static_cast<const __nv_bfloat16 *>(a.src[w]) + row * a.d + r.lane * 8, x);
-      }
+    for (int w = 0; w < 2; ++w) {
+      p[i][w].v = make_uint4(0u, 0u, 0u, 0u);
+      if (row >= 0) p[i][w] = fetch<E4M3>(a.src[w], a.scale[w], row, a.d, r.lane);
     }
-    store8(static_cast<T *>(a.dst[w]) + out, x);
+  }
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) {
+    const int n = r.n + i * r.step;
+    if (n >= a.N) break;
+    const long long out = (((long long)r.b * a.H + r.h) * a.N + n) * a.d + r.lane * 8;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      float x[8];
+      expand<E4M3>(p[i][w], x);
+      store8(static_cast<T *>(a.dst[w]) + out, x);
+    }
   }
 }
 
@@ -188,10 +229,14 @@ cudaError_t launch_rows(void (*k)(const CacheArgs), CacheArgs &a, cudaStream_t s
   while ((1 << a.shift) < a.page) ++a.shift;
   a.lanes = 1, a.lanes_shift = 0;
   while (a.lanes * 8 < a.d) a.lanes *= 2, ++a.lanes_shift;
-  const long long threads = (long long)a.B * a.H * a.N * a.lanes;
-  const long long blocks = (threads + 255) / 256;
-  if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
-  return launch_programmatic(k, dim3(unsigned(blocks)), dim3(256), 0, st, a);
+  const int rows_shift = 8 - a.lanes_shift;  // rows of a block of 256 threads
+  a.tok_shift = 0;
+  while (a.tok_shift < rows_shift && (1 << a.tok_shift) < a.N) ++a.tok_shift;
+  a.head_shift = rows_shift - a.tok_shift;
+  const long long toks = (long long)kSteps << a.tok_shift, heads = 1ll << a.head_shift;
+  const long long by = (a.N + toks - 1) / toks, bz = (a.H + heads - 1) / heads;
+  if (by > 65535 || bz > 65535) return cudaErrorInvalidValue;
+  return launch_programmatic(k, dim3(unsigned(a.B), unsigned(by), unsigned(bz)), dim3(256), 0, st, a);
 }
 
 int status_of(cudaError_t e) {

@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(256) bias_exact_kernel(int R, long long rows_q
 int sm_count() {
   int dev = 0, n = 148;
   if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-  return std::min(n, kMaxCtas / 3);
+  return std::min(n, kMaxCtas / 4);
 }
 
 bool sizes_ok(int B, int Hq, int H, int T, int d) {
@@ -174,7 +174,8 @@ int fb_attn_cache_fwd(int cache_dt, int B, int Hq, int H, int T, int d, const vo
   if (cache_dt == FB_E4M3 && (!k_scale || !v_scale)) return FB_ERR_INVALID_ARG;
   const uintptr_t wide = reinterpret_cast<uintptr_t>(Q) | reinterpret_cast<uintptr_t>(k_pages) |
                          reinterpret_cast<uintptr_t>(v_pages) | reinterpret_cast<uintptr_t>(O) |
-                         reinterpret_cast<uintptr_t>(prepared_bias);
+                         reinterpret_cast<uintptr_t>(prepared_bias) | reinterpret_cast<uintptr_t>(k_scale) |
+                         reinterpret_cast<uintptr_t>(v_scale);
   const uintptr_t narrow = reinterpret_cast<uintptr_t>(block_table) | reinterpret_cast<uintptr_t>(prefix) |
                            reinterpret_cast<uintptr_t>(counts) | reinterpret_cast<uintptr_t>(tree_mask) |
                            reinterpret_cast<uintptr_t>(depths) | reinterpret_cast<uintptr_t>(LSE);

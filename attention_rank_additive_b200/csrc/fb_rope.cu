@@ -16,7 +16,9 @@
 // What bounds it: each value is read and written once (HBM) and costs about
 // three operations, while a sine and cosine cost about 40 instructions. So a
 // thread computes the V sine/cosine pairs of one token and walks over several
-// heads with them; V pairs are two 16-byte loads and two 16-byte stores.
+// heads with them; V pairs are two 16-byte loads and two 16-byte stores. The two
+// lie half the rotated part apart in either layout (interleaved: V / 2 pairs
+// each), so that neighbouring lanes read neighbouring 16 bytes.
 #include <cmath>
 
 #include "fb_internal.h"
@@ -67,15 +69,13 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) {
 // token's, so that a warp reads whole rows.
 template <typename T, int V, bool INTERLEAVED>
 __global__ void __launch_bounds__(256) rope_kernel(const RopeArgs a) {
-  const long long per_group = (long long)a.B * a.N * a.units;
-  const long long id = blockIdx.x * 256ll + threadIdx.x;
-  if (id >= per_group * a.hgroups) return;
-  const int hg = int(id / per_group);
-  const long long rest = id - hg * per_group;
-  const int u = int(rest % a.units);
-  const long long tok = rest / a.units;
-  const int n = int(tok % a.N);
-  const int b = int(tok / a.N);
+  const unsigned id = blockIdx.x * 256u + threadIdx.x;
+  const unsigned tok = id / unsigned(a.units);
+  if (tok >= unsigned(a.B) * unsigned(a.N)) return;
+  const int hg = blockIdx.y;
+  const int u = int(id - tok * unsigned(a.units));
+  const int b = int(tok / unsigned(a.N));
+  const int n = int(tok - unsigned(b) * unsigned(a.N));
   const bool turn = u < a.turn_units;
 
   int o0, o1;  // offsets of the unit's two vectors in a head
@@ -83,13 +83,14 @@ __global__ void __launch_bounds__(256) rope_kernel(const RopeArgs a) {
   float c[V], s[V];
   griddep_wait();
   if (turn) {
-    const int p0 = u * V;
-    o0 = INTERLEAVED ? 2 * p0 : p0;
-    o1 = INTERLEAVED ? 2 * p0 + V : a.rot / 2 + p0;
+    o0 = INTERLEAVED && V == 1 ? 2 * u : u * V;
+    o1 = INTERLEAVED && V == 1 ? o0 + 1 : a.rot / 2 + u * V;
     const long long pos = a.positions ? (long long)a.positions[b * a.pos_bs + n] : n;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const unsigned long long frac = a.turns[p0 + i] * (unsigned long long)pos;
+      // interleaved: V / 2 pairs in each vector
+      const int p = INTERLEAVED && V > 1 ? (i < V / 2 ? o0 / 2 + i : o1 / 2 + i - V / 2) : u * V + i;
+      const unsigned long long frac = a.turns[p] * (unsigned long long)pos;
       // signed upper half, in units of half turns
       const float half_turns = float(int(frac >> 32)) * 4.656612873077393e-10f;
       sincospif(half_turns, &s[i], &c[i]);
@@ -97,9 +98,15 @@ __global__ void __launch_bounds__(256) rope_kernel(const RopeArgs a) {
       s[i] *= a.factor * a.sign;
     }
   } else {
-    o0 = a.rot + (u - a.turn_units) * 2 * V;
-    o1 = o0 + V;
-    nv = min(2 * V, a.d - o0);
+    const int c = u - a.turn_units, half = (a.d - a.rot) / 2;
+    if (2 * half == a.d - a.rot && half % V == 0) {
+      o0 = a.rot + c * V;
+      o1 = o0 + half;
+    } else {
+      o0 = a.rot + c * 2 * V;
+      o1 = o0 + V;
+      nv = min(2 * V, a.d - o0);
+    }
   }
   const int h0 = hg * a.hpt, h1 = min(h0 + a.hpt, a.heads[0] + a.heads[1]);
 #pragma unroll 4
@@ -146,10 +153,10 @@ cudaError_t launch_v(RopeArgs a, int interleaved, cudaStream_t st) {
   a.hpt = int(hpt < 1 ? 1 : (hpt > 8 ? 8 : hpt));
   if (a.hpt > H) a.hpt = H;
   a.hgroups = (H + a.hpt - 1) / a.hpt;
-  const long long blocks = (tokens_units * a.hgroups + 255) / 256;
-  if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
+  if (tokens_units > 0xffffff00ll || a.hgroups > 65535) return cudaErrorInvalidValue;
+  const long long blocks = (tokens_units + 255) / 256;
   void (*k)(const RopeArgs) = interleaved ? rope_kernel<T, V, true> : rope_kernel<T, V, false>;
-  return launch_programmatic(k, dim3(unsigned(blocks)), dim3(256), 0, st, a);
+  return launch_programmatic(k, dim3(unsigned(blocks), unsigned(a.hgroups)), dim3(256), 0, st, a);
 }
 
 // The widest vectors that every address of the call allows.
