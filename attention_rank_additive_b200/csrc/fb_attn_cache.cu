@@ -17,11 +17,12 @@
 // swap halves the idle rows for a single token (8 columns, not 16 rows). P^T is
 // S^T's accumulator after one 8x8 transpose (movmatrix).
 //
-// Each warp walks over 16-key groups of its own. A lane copies the very bytes
-// that it will use itself into a ring in shared memory with cp.async, several
-// groups ahead: the ring needs no barrier and has no bank conflicts, and the
-// loads in flight cost no registers (held in registers, 32 keys a step, the
-// 16-head ALiBi decode step took 142 us, 45 % of the copy rate).
+// Each warp walks over 16-key groups of its own. A group lies in one page, so
+// its K, V, scales and (in the context) factors are one run of bytes each: one
+// lane fetches them with bulk copies into the warp's ring in shared memory,
+// several groups ahead, and the other lanes do no address work. With a cp.async
+// per lane and 16 bytes instead, half of the instructions were that work
+// (ALiBi decode step 122 us); with the loads in registers it took 142 us.
 //
 // Work is dealt out by keys: all blocks of keys of all (sequence, head) items,
 // as the lengths on the device say, are numbered through and each CTA takes an
@@ -41,7 +42,10 @@ namespace fb {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kBlockKeys = 16 * kWarps;  // a block: a 16-key group per warp
+
+// 16-key groups that a warp takes in one step: two where rows are short, which gives its chains of dependent
+// instructions something to overlap with (one group a step: ALiBi decode step 130 us).
+constexpr int groups_per_step(int D, bool E4M3, int NB) { return NB == 1 && D * (E4M3 ? 1 : 2) <= 128 ? 2 : 1; }
 
 // CTAs of 128 threads on an SM at most, by blocks of 8 query rows: the registers of O and Q allow no more.
 constexpr int cta_per_sm(int NB) { return NB == 1 ? 4 : (NB == 2 ? 3 : 2); }
@@ -87,19 +91,6 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<uint32_t *>(&v);
 }
-// Wait until at most `left` (0 to 7) of this thread's latest groups are in flight.
-__device__ __forceinline__ void copies_wait(int left) {
-  switch (left) {
-    case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
-    case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
-    case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
-    case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
-    case 4: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
-    case 5: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
-    case 6: asm volatile("cp.async.wait_group 6;" ::: "memory"); break;
-    default: asm volatile("cp.async.wait_group 7;" ::: "memory"); break;
-  }
-}
 // N words of shared memory: plain loads, which the compiler may start early and order among the products as it likes.
 template <int N>
 __device__ __forceinline__ void read_words(const uint8_t *src, uint32_t *w) {
@@ -129,9 +120,6 @@ struct Lay {
   static constexpr int KL = E4M3 && D % 64 != 0 ? 2 : 4;
   // V: a piece of 64 values (of 128 for e4m3 at D = 128) is spread over eight lanes, then one of 32
   static constexpr int VL0 = D == 32 ? VW : (E4M3 ? (D == 128 ? 4 : 2) : 4);
-  // a stage of the ring: K pieces, V pieces, then 32 scale bytes (e4m3) and the keys' factors
-  static constexpr int KBYTES = 2 * KW * 4 * 32, VBYTES = 4 * VW * 4 * 32, SBYTES = E4M3 ? 32 : 0;
-  static constexpr int BASE = KBYTES + VBYTES + SBYTES;
   // d of value v (0 .. D/8 - 1) of lane group g
   static __device__ __forceinline__ int vd(int g, int v) {
     constexpr int per0 = VL0 * 4 / ES;  // values of a piece per lane
@@ -151,21 +139,23 @@ struct Join {  // over the ring, once a segment's keys are done
 template <int NB, int BIAS>
 struct Smem {
   uint4 fq[BIAS == 2 ? NB * 8 * 32 : 1];  // phi_q as matrix operands: [block][16 ranks][lane]
+  uint64_t full[kWarps][kMaxStages];      // a ring slot's copies have landed
   int last;
   int odd;  // a non-finite value left the products of this segment
-  int pad[2];
+  int abort;
+  int pad;
 };
 
-template <int D, bool E4M3, int BIAS>
-constexpr int stage_bytes(int RP) {
-  return Lay<D, E4M3>::BASE + (BIAS == 1 ? 256 : (BIAS == 2 ? RP / 16 * 2 * 512 : 0));
+// A group in the ring: 16 rows of K, of V, 16 scale bytes of each (e4m3), 16 rows of factors; 16-byte multiples.
+__host__ __device__ __forceinline__ int stage_bytes(int d, bool e4m3, int bias, int RP) {
+  return 32 * d * (e4m3 ? 1 : 2) + (e4m3 ? 32 : 0) + (bias == 1 ? 256 : (bias == 2 ? 64 * RP : 0));
 }
 
 template <int D, bool E4M3, int NB, int BIAS>
 __global__ void __launch_bounds__(kWarps * 32, cta_per_sm(NB)) attn_cache_kernel(const CacheAttnArgs a, const int stages) {
   using L = Lay<D, E4M3>;
-  constexpr int KS = D / 16, ROWS = 8 * NB;
-  constexpr int BK = kBlockKeys;
+  constexpr int KS = D / 16, ROWS = 8 * NB, KM = groups_per_step(D, E4M3, NB);
+  constexpr int BK = 16 * KM * kWarps;  // a block of keys: a step of each warp
   extern __shared__ __align__(16) uint8_t smem_raw[];
   auto &sm = *reinterpret_cast<Smem<NB, BIAS> *>(smem_raw);
   auto &join = *reinterpret_cast<Join<D, NB> *>(smem_raw + sizeof(sm));
@@ -175,6 +165,11 @@ __global__ void __launch_bounds__(kWarps * 32, cta_per_sm(NB)) attn_cache_kernel
   // ---- this CTA's run of blocks of all items
   Walk walk(a, BK, lane);
   if (blockIdx.x >= walk.ctas) return;
+  if (threadIdx.x == 0) sm.abort = 0;
+  if (lane < stages) mbar_init(&sm.full[warp][lane], KM);
+  fence_mbar_init();
+  int slot = 0;         // of the next group to use
+  uint32_t parity = 0;  // of its barrier
   Segment seg;
   while (walk.next(a, seg)) {
     const Seq &s = seg.s;
@@ -291,225 +286,208 @@ __global__ void __launch_bounds__(kWarps * 32, cta_per_sm(NB)) attn_cache_kernel
     }
 
     if (threadIdx.x == 0) sm.odd = 0;
-    __syncthreads();  // sm.odd; and the last segment's readers of shared memory are done
+    fence_proxy_async_smem();  // the ring's bulk copies come after what was written and read there
+    __syncthreads();           // sm.odd; and the last segment's readers of shared memory are done
+    fence_proxy_async_smem();
     const int *table = a.table + (long long)b * a.max_pages;
-    const int jend = min(s.len, k1 * BK), jstart = k0 * BK + warp * 16;
+    const int jend = min(s.len, k1 * BK), jstart = k0 * BK + warp * 16 * KM;
     const int hk = BIAS ? (a.fk_heads > 1 ? h : 0) : 0;
-    const int stage = stage_bytes<D, E4M3, BIAS>(a.RP);
-    const uint8_t *ring = smem_raw + sizeof(sm) + warp * stages * stage;
-    auto page_of = [&](int j) { return j < jend ? __ldg(table + (j >> a.page_shift)) : 0; };
-    int next_page = page_of(jstart);
-    // Copy the group at j into ring slot `slot`; false where the table leads nowhere (zeros are copied).
-    auto fetch = [&](int j, int slot) {
-      const int page = next_page;
-      next_page = page_of(j + BK);
-      bool alive = j < jend;
-      if (alive && (page < 0 || page >= a.num_pages)) {
-        if (lane == 0) atomicOr(a.flags, kFlagRange);
-        alive = false;
-      }
-      const long long prow = (((long long)(alive ? page : 0) * a.H + h) << a.page_shift) + (j & ((1 << a.page_shift) - 1));
-      const uint32_t dst = smem_u32(ring + slot * stage);
-      const uint8_t *kb = static_cast<const uint8_t *>(a.kp) + prow * (a.d * L::ES);
-      const uint8_t *vb = static_cast<const uint8_t *>(a.vp) + prow * (a.d * L::ES);
-      const int left = alive ? s.len - j : 0;  // keys of the group
-      if (left >= 16 && a.d == D) {  // whole rows: fixed offsets from one address a side
-        // K: the group's 16 rows lie one after the other, so the lanes take 16-byte chunks in order (a load of 64 bytes
-        // of a row brings the whole 128-byte line, half of it twice) and put each where its user will look
-        const uint8_t *vl = vb + t4 * (2 * D * L::ES) + g * (L::VL0 * 4);
-        const uint32_t vd = dst + L::KBYTES + lane * (L::VL0 * 4);
-        constexpr int cpr = D * L::ES / 16;  // chunks of a row
-#pragma unroll
-        for (int q = 0; q < cpr / 2; ++q) {
-          const int at = q * 32 + lane, row = at / cpr, ch = at % cpr;
-          const int piece = (row >> 3) * (L::KW / L::KL) + (L::KL == 4 ? ch >> 2 : ch >> 1);
-          const int place = (row & 7) * 4 + (L::KL == 4 ? ch & 3 : (ch & 1) * 2);
-          copy_whole<4>(dst + (piece * 32 + place) * (L::KL * 4), kb + at * 16);
-        }
-        constexpr int pieces = D == 96 ? 1 : L::VW / L::VL0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int off = ((i & 1) + 8 * (i >> 1)) * D * L::ES;
-#pragma unroll
-          for (int c = 0; c < pieces; ++c)
-            copy_whole<L::VL0>(vd + i * (L::VW * 4 * 32) + c * (32 * L::VL0 * 4), vl + off + c * (8 * L::VL0 * 4));
-          if constexpr (D == 96)
-            copy_whole<L::VL0 / 2>(dst + L::KBYTES + i * (L::VW * 4 * 32) + 32 * (L::VL0 * 4) + lane * (L::VL0 * 2),
-                                   vb + t4 * (2 * D * L::ES) + off + 64 * L::ES + g * (L::VL0 * 2));
-        }
-      } else {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int jj = g + 8 * i;
-#pragma unroll
-        for (int c = 0; c < L::KW / L::KL; ++c) {
-          constexpr int per = L::KL * 4 / L::ES;
-          const int d0 = c * 4 * per + t4 * per;
-          const bool in = jj < left && d0 < a.d;
-          copy_words<L::KL>(dst + ((i * (L::KW / L::KL) + c) * 32 + lane) * (L::KL * 4),
-                            in ? kb + (jj * a.d + d0) * L::ES : kb, in);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int jj = 2 * t4 + (i & 1) + 8 * (i >> 1);
-        constexpr int per = L::VL0 * 4 / L::ES;
-        constexpr int pieces = D == 96 ? 1 : L::VW / L::VL0;
-        const uint32_t vdst = dst + L::KBYTES + i * (L::VW * 4 * 32);
-#pragma unroll
-        for (int c = 0; c < pieces; ++c) {
-          const int d0 = c * 8 * per + g * per;
-          const bool in = jj < left && d0 < a.d;
-          copy_words<L::VL0>(vdst + (c * 32 + lane) * (L::VL0 * 4), in ? vb + (jj * a.d + d0) * L::ES : vb, in);
-        }
-        if constexpr (D == 96) {
-          const int d0 = 64 + g * (per / 2);
-          const bool in = jj < left && d0 < a.d;
-          copy_words<L::VL0 / 2>(vdst + 32 * (L::VL0 * 4) + lane * (L::VL0 * 2), in ? vb + (jj * a.d + d0) * L::ES : vb, in);
-        }
-      }
-      }
-      if constexpr (E4M3) {  // 16 scale bytes of either side: a group starts at a multiple of 16 rows
-        if (lane < 2) copy_words<4>(dst + L::KBYTES + L::VBYTES + lane * 16, (lane ? a.vs : a.ks) + prow, alive);
-      }
-      if constexpr (BIAS != 0) {
-        auto position = [&](int jj) {
-          const int jk = j + jj;
-          if (jj >= left) return 0;
-          if (jk >= s.prefix) return new_position(a, b, s, jk - s.prefix);
-          if (jk < a.P) return jk;
-          atomicOr(a.flags, kFlagRange);
-          return a.P - 1;
-        };
-        if constexpr (BIAS == 1) {
-          if (lane < 16)
-            copy_words<4>(dst + L::BASE + lane * 16, static_cast<const float4 *>(a.fk) + (long long)hk * a.P + position(lane),
-                          lane < left);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint4 *f = static_cast<const uint4 *>(a.fk) + ((long long)hk * a.P + position(g + 8 * i)) * (a.RP / 4) + t4;
-            for (int c = 0; c < a.RP / 16; ++c)
-              copy_words<4>(dst + L::BASE + ((c * 2 + i) * 32 + lane) * 16, f + c * 4, g + 8 * i < left);
-          }
-        }
-      }
-      return alive;
+    const int rb = a.d * L::ES;  // bytes of a row
+    const int group = stage_bytes(a.d, E4M3, BIAS, a.RP);  // of the ring: a group, of which a slot has KM
+    const int fk_row = BIAS == 1 ? 16 : 4 * a.RP;
+    const uint8_t *fk_head = static_cast<const uint8_t *>(a.fk) + (BIAS ? (long long)hk * a.P * fk_row : 0ll);
+    uint8_t *ring = smem_raw + sizeof(sm) + warp * stages * KM * group;
+    // the page of lane i's group (i < KM) of the step at j
+    auto page_of = [&](int j) {
+      j += 16 * lane;
+      return lane < KM && j < jend ? __ldg(table + (j >> a.page_shift)) : -1;
     };
-    unsigned alive_bits = 0;  // bit s: the group in ring slot s
-    for (int i = 0; i < stages - 1; ++i) {
-      alive_bits |= unsigned(fetch(jstart + i * BK, i)) << i;
-      copies_commit();
+    auto page_ok = [&](int page) { return page >= 0 && page < a.num_pages; };
+    // Fetch the step at j into ring slot `to`: lane i its group i.
+    auto fetch = [&](int j, int page, int to) {
+      if (j >= jend || lane >= KM) return;
+      uint64_t *bar = &sm.full[warp][to];
+      uint8_t *dst = ring + (to * KM + lane) * group;
+      j += 16 * lane;
+      if (!page_ok(page)) {
+        if (j < jend) atomicOr(a.flags, kFlagRange);
+        mbar_arrive(bar);
+        return;
+      }
+      const long long prow = (((long long)page * a.H + h) << a.page_shift) + (j & ((1 << a.page_shift) - 1));
+      const bool factors = BIAS != 0 && j + 16 <= min(s.prefix, a.P);  // else read where they are used
+      mbar_arrive_expect_tx(bar, 32 * rb + (E4M3 ? 32 : 0) + (factors ? 16 * fk_row : 0));
+      bulk_load(dst, static_cast<const uint8_t *>(a.kp) + prow * rb, 16 * rb, bar);
+      bulk_load(dst + 16 * rb, static_cast<const uint8_t *>(a.vp) + prow * rb, 16 * rb, bar);
+      if constexpr (E4M3) {
+        bulk_load(dst + 32 * rb, a.ks + prow, 16, bar);
+        bulk_load(dst + 32 * rb + 16, a.vs + prow, 16, bar);
+      }
+      if (factors) bulk_load(dst + 32 * rb + (E4M3 ? 32 : 0), fk_head + (long long)j * fk_row, 16 * fk_row, bar);
+    };
+    // Lanes whose d lies past the row read its first bytes instead: the queries are 0 there, and O is not written.
+    int kat[L::KW / L::KL], vat[L::VW / L::VL0 + (D == 96 ? 1 : 0)];
+#pragma unroll
+    for (int c = 0; c < L::KW / L::KL; ++c) {
+      const int at = (c * 4 + t4) * (L::KL * 4);
+      kat[c] = g * rb + (at < rb ? at : 0);
     }
-    int slot = 0;
+#pragma unroll
+    for (int c = 0; c < L::VW / L::VL0 + (D == 96 ? 1 : 0); ++c) {
+      const int at = D == 96 && c == 1 ? 64 * L::ES + g * (L::VL0 * 2) : (c * 8 + g) * (L::VL0 * 4);
+      vat[c] = (16 + 2 * t4) * rb + (at < rb ? at : 0);
+    }
+    // page numbers one step ahead of their fetch
+    int fill = slot;
+    for (int i = 0; i < stages - 1; ++i) {
+      fetch(jstart + i * BK, page_of(jstart + i * BK), fill);
+      fill = fill + 1 == stages ? 0 : fill + 1;
+    }
+    int page_fill = page_of(jstart + (stages - 1) * BK);
+    int page_use = page_of(jstart);
     for (int j0 = jstart; j0 < jend; j0 += BK) {
-      const int ahead = slot == 0 ? stages - 1 : slot - 1;
-      const bool there = fetch(j0 + (stages - 1) * BK, ahead);
-      copies_commit();
-      alive_bits = (alive_bits & ~(1u << ahead)) | unsigned(there) << ahead;
-      copies_wait(stages - 1);
-      __syncwarp();  // scales and factors were copied by other lanes
-      const bool alive = (alive_bits >> slot) & 1u;
-      const uint8_t *src = ring + slot * stage;
-      const bool tail = j0 + 16 > s.prefix;  // drafted keys, or rows past the end
+      fetch(j0 + (stages - 1) * BK, page_fill, fill);
+      fill = fill + 1 == stages ? 0 : fill + 1;
+      page_fill = page_of(j0 + stages * BK);
+      const unsigned alive = __ballot_sync(0xffffffffu, page_ok(page_use));  // bit mb: group mb has a page
+      page_use = page_of(j0 + BK);
+      mbar_wait_long(&sm.full[warp][slot], parity, &sm.abort);
+      const uint8_t *src = ring + slot * KM * group;
+      const bool tail = j0 + 16 * KM > s.prefix || alive != (1u << KM) - 1u;  // new tokens, rows past the end, or no page
 
       // ---- scores: S^T = K Q^T (16 keys x 8 rows per block)
-      float x[NB][4], xl[NB][E4M3 ? 4 : 1];
+      float x[KM][NB][4];
 #pragma unroll
-      for (int n = 0; n < NB; ++n)
+      for (int mb = 0; mb < KM; ++mb) {
+        float xl[NB][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[n][i] = xl[n][E4M3 ? i : 0] = 0.f;
+        for (int n = 0; n < NB; ++n)
 #pragma unroll
-      for (int c = 0; c < L::KW / L::KL; ++c) {
-        uint32_t kr[2][L::KL];
+          for (int i = 0; i < 4; ++i) x[mb][n][i] = xl[n][i] = 0.f;
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          read_words<L::KL>(src + ((i * (L::KW / L::KL) + c) * 32 + lane) * (L::KL * 4), kr[i]);
+        for (int c = 0; c < L::KW / L::KL; ++c) {
+          uint32_t kr[2][L::KL];
 #pragma unroll
-        for (int kk = 0; kk < L::KL / 2; ++kk) {
-          const int k = c * (L::KL / 2) + kk;
+          for (int i = 0; i < 2; ++i) read_words<L::KL>(src + mb * group + 8 * i * rb + kat[c], kr[i]);
 #pragma unroll
-          for (int n = 0; n < NB; ++n) {
-            if constexpr (E4M3) {
-              mma_e4m3(x[n], kr[0][2 * kk], kr[1][2 * kk], kr[0][2 * kk + 1], kr[1][2 * kk + 1], qf[n][k][0], qf[n][k][1]);
-              mma_e4m3(xl[n], kr[0][2 * kk], kr[1][2 * kk], kr[0][2 * kk + 1], kr[1][2 * kk + 1], qf[n][KS / 2 + k][0],
-                       qf[n][KS / 2 + k][1]);
-            } else {
-              mma_bf16(x[n], kr[0][2 * kk], kr[1][2 * kk], kr[0][2 * kk + 1], kr[1][2 * kk + 1], qf[n][k][0], qf[n][k][1]);
+          for (int kk = 0; kk < L::KL / 2; ++kk) {
+            const int k = c * (L::KL / 2) + kk;
+            const uint32_t a0 = kr[0][2 * kk], a1 = kr[1][2 * kk], a2 = kr[0][2 * kk + 1], a3 = kr[1][2 * kk + 1];
+#pragma unroll
+            for (int n = 0; n < NB; ++n) {
+              if constexpr (E4M3) {
+                mma_e4m3(x[mb][n], a0, a1, a2, a3, qf[n][k][0], qf[n][k][1]);
+                mma_e4m3(xl[n], a0, a1, a2, a3, qf[n][KS / 2 + k][0], qf[n][KS / 2 + k][1]);
+              } else {
+                mma_bf16(x[mb][n], a0, a1, a2, a3, qf[n][k][0], qf[n][k][1]);
+              }
             }
           }
         }
-      }
-      if constexpr (E4M3) {
+        if constexpr (E4M3) {
 #pragma unroll
-        for (int n = 0; n < NB; ++n)
+          for (int n = 0; n < NB; ++n)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) x[n][i] = fmaf(xl[n][i], 0.0625f, x[n][i]);
+            for (int i = 0; i < 4; ++i) x[mb][n][i] = fmaf(xl[n][i], 0.0625f, x[mb][n][i]);
+        }
       }
       // ---- scale and bias
-      float bias[NB][BIAS == 2 ? 4 : 1];
-      if constexpr (BIAS == 2) {
-        float low[NB][4];  // the two small products
+      float svf[KM][2];
 #pragma unroll
-        for (int n = 0; n < NB; ++n)
+      for (int mb = 0; mb < KM; ++mb) {
+        const int j1 = j0 + 16 * mb;
+        const bool in_ring = BIAS != 0 && j1 + 16 <= min(s.prefix, a.P);
+        const uint8_t *fsrc = src + mb * group + 32 * rb + (E4M3 ? 32 : 0);
+        int kpos[2] = {0, 0};
+        if (BIAS != 0 && !in_ring) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) bias[n][i] = low[n][i] = 0.f;
-        for (int c = 0; c < a.RP / 16; ++c) {
-          uint32_t f[2][4];  // 4 hi, 4 lo
-#pragma unroll
-          for (int i = 0; i < 2; ++i) read_words<4>(src + L::BASE + ((c * 2 + i) * 32 + lane) * 16, f[i]);
-#pragma unroll
-          for (int n = 0; n < NB; ++n) {
-            const uint4 q = sm.fq[(n * 8 + c) * 32 + lane];
-            // (kh + kl)(qh + ql) without the last 2^-22
-            mma_f16(low[n], f[0][2], f[1][2], f[0][3], f[1][3], q.x, q.y);
-            mma_f16(bias[n], f[0][0], f[1][0], f[0][1], f[1][1], q.x, q.y);
-            mma_f16(low[n], f[0][0], f[1][0], f[0][1], f[1][1], q.z, q.w);
+          for (int i = 0; i < 2; ++i) {
+            const int jk = j1 + g + 8 * i;
+            if (jk >= s.len) continue;
+            kpos[i] = jk >= s.prefix ? new_position(a, b, s, jk - s.prefix) : jk;
+            if (kpos[i] >= a.P) {
+              atomicOr(a.flags, kFlagRange);
+              kpos[i] = a.P - 1;
+            }
           }
         }
+        float bias[NB][4];
+        if constexpr (BIAS == 2) {
+          float low[NB][4];  // the two small products
 #pragma unroll
-        for (int n = 0; n < NB; ++n)
+          for (int n = 0; n < NB; ++n)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) bias[n][i] += low[n][i];
-      }
-      float fk[2][BIAS == 1 ? 4 : 1], skf[2], svf[2];
+            for (int i = 0; i < 4; ++i) bias[n][i] = low[n][i] = 0.f;
+          for (int c = 0; c < a.RP / 16; ++c) {
+            uint32_t f[2][4];  // 4 hi, 4 lo
+            if (in_ring) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        if constexpr (BIAS == 1) read_words<4>(src + L::BASE + (g + 8 * i) * 16, reinterpret_cast<uint32_t *>(fk[i]));
-        skf[i] = svf[i] = 0.f;
-        if constexpr (E4M3) {
-          const uint32_t k8 = src[L::KBYTES + L::VBYTES + g + 8 * i], v8 = src[L::KBYTES + L::VBYTES + 16 + g + 8 * i];
-          skf[i] = k8 == 255u ? __uint_as_float(0x7fffffffu) : pow2i(int(k8) - 127);
-          svf[i] = v8 == 255u ? __uint_as_float(0x7fffffffu) : float(int(v8) - 127);
+              for (int i = 0; i < 2; ++i) read_words<4>(fsrc + (g + 8 * i) * fk_row + c * 64 + t4 * 16, f[i]);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const uint4 u = __ldg(reinterpret_cast<const uint4 *>(fk_head + (long long)kpos[i] * fk_row + c * 64 + t4 * 16));
+                f[i][0] = u.x, f[i][1] = u.y, f[i][2] = u.z, f[i][3] = u.w;
+              }
+            }
+#pragma unroll
+            for (int n = 0; n < NB; ++n) {
+              const uint4 q = sm.fq[(n * 8 + c) * 32 + lane];
+              // (kh + kl)(qh + ql) without the last 2^-22
+              mma_f16(low[n], f[0][2], f[1][2], f[0][3], f[1][3], q.x, q.y);
+              mma_f16(bias[n], f[0][0], f[1][0], f[0][1], f[1][1], q.x, q.y);
+              mma_f16(low[n], f[0][0], f[1][0], f[0][1], f[1][1], q.z, q.w);
+            }
+          }
+#pragma unroll
+          for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) bias[n][i] += low[n][i];
         }
-      }
+        float fk[2][4], skf[2];
 #pragma unroll
-      for (int n = 0; n < NB; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int kk = i >> 1, rr = i & 1;
-          float f = mult[n][rr];
-          if constexpr (E4M3) f *= skf[kk];
+        for (int i = 0; i < 2; ++i) {
           if constexpr (BIAS == 1) {
-            float y = fk[kk][0] * fq[n][rr][0];
-#pragma unroll
-            for (int r = 1; r < 4; ++r) y = fmaf(fk[kk][r], fq[n][rr][r], y);
-            x[n][i] = fmaf(x[n][i], f, y);
-          } else if constexpr (BIAS == 2) {
-            x[n][i] = fmaf(x[n][i], f, bias[n][i]);
-          } else {
-            x[n][i] *= f;
+            const float4 f = in_ring ? *reinterpret_cast<const float4 *>(fsrc + (g + 8 * i) * 16)
+                                     : __ldg(reinterpret_cast<const float4 *>(fk_head) + kpos[i]);
+            fk[i][0] = f.x, fk[i][1] = f.y, fk[i][2] = f.z, fk[i][3] = f.w;
+          }
+          skf[i] = svf[mb][i] = 0.f;
+          if constexpr (E4M3) {
+            // 2^(byte - 127); byte 255 is NaN, byte 0 (2^-127, which cache_write does not make) counts as 0
+            const uint32_t k8 = src[mb * group + 32 * rb + g + 8 * i], v8 = src[mb * group + 32 * rb + 16 + g + 8 * i];
+            skf[i] = __uint_as_float(k8 == 255u ? 0x7fffffffu : k8 << 23);
+            svf[mb][i] = v8 == 255u ? __uint_as_float(0x7fffffffu) : float(int(v8) - 127);
           }
         }
-      if (tail || !alive) {
 #pragma unroll
         for (int n = 0; n < NB; ++n)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int j = j0 + g + 8 * (i >> 1), u = j - s.prefix, t = tok[n][i & 1];
-            const bool see = alive && j < s.len && (u < 0 || (t >= 0 && drafted_visible(a, b, t, u)));
-            if (!see) x[n][i] = -INFINITY;
+            const int kk = i >> 1, rr = i & 1;
+            float f = mult[n][rr];
+            if constexpr (E4M3) f *= skf[kk];
+            if constexpr (BIAS == 1) {
+              float y = fk[kk][0] * fq[n][rr][0];
+#pragma unroll
+              for (int r = 1; r < 4; ++r) y = fmaf(fk[kk][r], fq[n][rr][r], y);
+              x[mb][n][i] = fmaf(x[mb][n][i], f, y);
+            } else if constexpr (BIAS == 2) {
+              x[mb][n][i] = fmaf(x[mb][n][i], f, bias[n][i]);
+            } else {
+              x[mb][n][i] *= f;
+            }
           }
+        if (tail) {
+#pragma unroll
+          for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int j = j1 + g + 8 * (i >> 1), u = j - s.prefix, t = tok[n][i & 1];
+              const bool see = ((alive >> mb) & 1u) && j < s.len && (u < 0 || (t >= 0 && drafted_visible(a, b, t, u)));
+              if (!see) x[mb][n][i] = -INFINITY;
+            }
+        }
       }
       // ---- running maximum, raised only when a score passes it by more than 8 (exp stays below e^8)
       float top[NB][2];
@@ -518,7 +496,9 @@ __global__ void __launch_bounds__(kWarps * 32, cta_per_sm(NB)) attn_cache_kernel
       for (int n = 0; n < NB; ++n)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          top[n][i] = fmaxf(x[n][i], x[n][i + 2]);
+          top[n][i] = fmaxf(x[0][n][i], x[0][n][i + 2]);
+#pragma unroll
+          for (int mb = 1; mb < KM; ++mb) top[n][i] = fmax3(top[n][i], x[mb][n][i], x[mb][n][i + 2]);
           need |= top[n][i] > m[n][i] + 8.f;
         }
       if (__any_sync(0xffffffffu, need)) {
@@ -545,7 +525,7 @@ __global__ void __launch_bounds__(kWarps * 32, cta_per_sm(NB)) attn_cache_kernel
           }
       }
       // ---- probabilities; e4m3 values: each key's weight takes the value row's power of two, fp16 in O's unit
-      uint32_t pf[NB][2];
+      uint32_t pf[KM][NB][2];
       if constexpr (E4M3) {
         bool grow = false;
         float ytop[NB][2];
@@ -556,12 +536,14 @@ __global__ void __launch_bounds__(kWarps * 32, cta_per_sm(NB)) attn_cache_kernel
             const float mu = m[n][i] == -INFINITY ? 0.f : m[n][i];
             ytop[n][i] = -INFINITY;
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {
-              const float y = (x[n][2 * kk + i] - mu) * kCacheLog2e;
-              x[n][2 * kk + i] = y;
-              l[n][i] += ex2_approx(y);
-              ytop[n][i] = fmaxf(ytop[n][i], y + svf[kk]);
-            }
+            for (int mb = 0; mb < KM; ++mb)
+#pragma unroll
+              for (int kk = 0; kk < 2; ++kk) {
+                const float y = (x[mb][n][2 * kk + i] - mu) * kCacheLog2e;
+                x[mb][n][2 * kk + i] = y;
+                l[n][i] += ex2_approx(y);
+                ytop[n][i] = fmaxf(ytop[n][i], y + svf[mb][kk]);
+              }
             grow |= ytop[n][i] - 15.f > ex[n][i];  // the largest weight is kept below 2^15
           }
         if (__any_sync(0xffffffffu, grow)) {
@@ -582,89 +564,98 @@ __global__ void __launch_bounds__(kWarps * 32, cta_per_sm(NB)) attn_cache_kernel
             }
         }
 #pragma unroll
-        for (int n = 0; n < NB; ++n) {
+        for (int mb = 0; mb < KM; ++mb)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float y = x[n][i];
-            x[n][i] = y == -INFINITY ? 0.f : ex2_approx(y + (svf[i >> 1] - ex[n][i & 1]));
+          for (int n = 0; n < NB; ++n) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float y = x[mb][n][i];
+              x[mb][n][i] = y == -INFINITY ? 0.f : ex2_approx(y + (svf[mb][i >> 1] - ex[n][i & 1]));
+            }
+            pf[mb][n][0] = transpose8x8(pack_f16x2(x[mb][n][0], x[mb][n][1]));
+            pf[mb][n][1] = transpose8x8(pack_f16x2(x[mb][n][2], x[mb][n][3]));
           }
-          pf[n][0] = transpose8x8(pack_f16x2(x[n][0], x[n][1]));
-          pf[n][1] = transpose8x8(pack_f16x2(x[n][2], x[n][3]));
-        }
       } else {
         // weights rounded to bf16 (2^-8 at most, each its own, next to O's own rounding); their sum stays fp32
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
           const float m0 = m[n][0] == -INFINITY ? 0.f : m[n][0], m1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            x[n][i] = ex2_approx((x[n][i] - (i & 1 ? m1 : m0)) * kCacheLog2e);
-            l[n][i & 1] += x[n][i];
+          for (int mb = 0; mb < KM; ++mb) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              x[mb][n][i] = ex2_approx((x[mb][n][i] - (i & 1 ? m1 : m0)) * kCacheLog2e);
+              l[n][i & 1] += x[mb][n][i];
+            }
+            pf[mb][n][0] = transpose8x8(pack_bf16x2(x[mb][n][0], x[mb][n][1]));
+            pf[mb][n][1] = transpose8x8(pack_bf16x2(x[mb][n][2], x[mb][n][3]));
           }
-          pf[n][0] = transpose8x8(pack_bf16x2(x[n][0], x[n][1]));
-          pf[n][1] = transpose8x8(pack_bf16x2(x[n][2], x[n][3]));
         }
       }
       // ---- O^T += V^T P^T
       constexpr int VP = L::VL0;
       constexpr int pieces = L::VW / VP + (D == 96 ? 1 : 0);
 #pragma unroll
-      for (int c = 0; c < pieces; ++c) {
-        constexpr int full = D == 96 ? 1 : pieces;
-        const bool last = c >= full;  // the half piece of D = 96
-        uint32_t vr[4][VP];
+      for (int mb = 0; mb < KM; ++mb)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint8_t *vsrc = src + L::KBYTES + i * (L::VW * 4 * 32);
-          if (!last)
-            read_words<VP>(vsrc + (c * 32 + lane) * (VP * 4), vr[i]);
-          else
-            read_words<(VP + 1) / 2>(vsrc + 32 * (VP * 4) + lane * (VP * 2), vr[i]);
-        }
-        // an infinite or NaN value must not reach the rows that do not see its key (0 * inf): where new tokens are
-        // among the keys it leaves the product, and the rows that see it get it back when the segment is joined
-        if (tail) {
-          bool odd = false;
+        for (int c = 0; c < pieces; ++c) {
+          constexpr int full = D == 96 ? 1 : pieces;
+          const bool last = c >= full;  // the half piece of D = 96
+          uint32_t vr[4][VP];
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int w = 0; w < VP; ++w) {
-              if (last && w >= VP / 2) continue;
-              const uint32_t even = even_word<E4M3>(vr[i][w]);
-              odd |= even != vr[i][w];
-              vr[i][w] = even;
-            }
-          if (odd) sm.odd = 1;
-        }
-        constexpr int per = E4M3 ? VP * 2 : VP;  // products per piece
-#pragma unroll
-        for (int kk = 0; kk < per; ++kk) {
-          if (last && kk >= per / 2) continue;
-          const int k = c * per + kk;
-          uint32_t a0, a1, a2, a3;
-          if constexpr (E4M3) {
-            const int w = kk / 2;
-            const uint32_t sel = kk & 1 ? 0x7362u : 0x5140u;  // the two keys' bytes side by side
-            const uint32_t u = __byte_perm(vr[0][w], vr[1][w], sel);
-            const uint32_t v = __byte_perm(vr[2][w], vr[3][w], sel);
-            a0 = e4m3_lo(u), a1 = e4m3_hi(u), a2 = e4m3_lo(v), a3 = e4m3_hi(v);
-          } else {
-            a0 = __byte_perm(vr[0][kk], vr[1][kk], 0x5410), a1 = __byte_perm(vr[0][kk], vr[1][kk], 0x7632);
-            a2 = __byte_perm(vr[2][kk], vr[3][kk], 0x5410), a3 = __byte_perm(vr[2][kk], vr[3][kk], 0x7632);
-          }
-#pragma unroll
-          for (int n = 0; n < NB; ++n) {
-            if constexpr (E4M3)
-              mma_f16(o[k][n], a0, a1, a2, a3, pf[n][0], pf[n][1]);
+          for (int i = 0; i < 4; ++i) {
+            const uint8_t *p = src + mb * group + ((i & 1) + 8 * (i >> 1)) * rb + vat[c];
+            if (!last)
+              read_words<VP>(p, vr[i]);
             else
-              mma_bf16(o[k][n], a0, a1, a2, a3, pf[n][0], pf[n][1]);
+              read_words<(VP + 1) / 2>(p, vr[i]);
+          }
+          // an infinite or NaN value must not reach the rows that do not see its key (0 * inf): where new tokens are
+          // among the keys it leaves the product, and the rows that see it get it back when the segment is joined;
+          // rows behind the last token, and those of no page, are nothing at all
+          if (tail) {
+            bool odd = false;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const bool real = ((alive >> mb) & 1u) && j0 + 16 * mb + 2 * t4 + (i & 1) + 8 * (i >> 1) < s.len;
+#pragma unroll
+              for (int w = 0; w < VP; ++w) {
+                if (last && w >= VP / 2) continue;
+                const uint32_t was = real ? vr[i][w] : 0u, even = even_word<E4M3>(was);
+                odd |= even != was;
+                vr[i][w] = even;
+              }
+            }
+            if (odd) sm.odd = 1;
+          }
+          constexpr int per = E4M3 ? VP * 2 : VP;  // products per piece
+#pragma unroll
+          for (int kk = 0; kk < per; ++kk) {
+            if (last && kk >= per / 2) continue;
+            const int k = c * per + kk;
+            uint32_t a0, a1, a2, a3;
+            if constexpr (E4M3) {
+              const int w = kk / 2;
+              const uint32_t sel = kk & 1 ? 0x7362u : 0x5140u;  // the two keys' bytes side by side
+              const uint32_t u = __byte_perm(vr[0][w], vr[1][w], sel);
+              const uint32_t v = __byte_perm(vr[2][w], vr[3][w], sel);
+              a0 = e4m3_lo(u), a1 = e4m3_hi(u), a2 = e4m3_lo(v), a3 = e4m3_hi(v);
+            } else {
+              a0 = __byte_perm(vr[0][kk], vr[1][kk], 0x5410), a1 = __byte_perm(vr[0][kk], vr[1][kk], 0x7632);
+              a2 = __byte_perm(vr[2][kk], vr[3][kk], 0x5410), a3 = __byte_perm(vr[2][kk], vr[3][kk], 0x7632);
+            }
+#pragma unroll
+            for (int n = 0; n < NB; ++n) {
+              if constexpr (E4M3)
+                mma_f16(o[k][n], a0, a1, a2, a3, pf[mb][n][0], pf[mb][n][1]);
+              else
+                mma_bf16(o[k][n], a0, a1, a2, a3, pf[mb][n][0], pf[mb][n][1]);
+            }
           }
         }
-      }
-      slot = slot + 1 == stages ? 0 : slot + 1;
+      if (++slot == stages) slot = 0, parity ^= 1u;
       __syncwarp();  // the slot's readers are done before it is filled again
     }
-    copies_wait(0);
 
     __syncthreads();  // the ring becomes the join's memory
     // ---- the warps' parts of the segment
@@ -698,7 +689,7 @@ __global__ void __launch_bounds__(kWarps * 32, cta_per_sm(NB)) attn_cache_kernel
         sum += join.l[w][row] * ex2_approx(y);
         val += join.o[w][row][dd] * ex2_approx(y + join.e[w][row]);
       }
-      if (sm.odd && dd < a.d) val += odd_sum<E4M3>(a, s, b, h, (r0 + row) % a.T, dd, max(k0 * BK, s.prefix / 16 * 16), jend);
+      if (sm.odd && dd < a.d) val += odd_sum<E4M3>(a, s, b, h, (r0 + row) % a.T, dd, max(k0 * BK, s.prefix / (16 * KM) * (16 * KM)), jend);
       if (whole) {
         write_row(a, s, qrow0 + r0 + row, (r0 + row) % a.T, dd, top, sum, val);
       } else {
@@ -734,17 +725,20 @@ __global__ void __launch_bounds__(kWarps * 32, cta_per_sm(NB)) attn_cache_kernel
       }
     }
   }
+  if (threadIdx.x == 0 && sm.abort) atomicOr(a.flags, kFlagTimeout);
 }
 
 template <int D, bool E4M3, int NB, int BIAS>
 cudaError_t launch_bias(const CacheAttnArgs &a, int sms, cudaStream_t st) {
   auto *k = attn_cache_kernel<D, E4M3, NB, BIAS>;
-  const int stage = kWarps * stage_bytes<D, E4M3, BIAS>(a.RP);
+  constexpr int keys = 16 * groups_per_step(D, E4M3, NB) * kWarps;  // a block's
+  const int stage = keys / 16 * stage_bytes(a.d, E4M3, BIAS, a.RP);
   const int fixed = sizeof(Smem<NB, BIAS>), join = sizeof(Join<D, NB>);
-  // CTAs on an SM: as many as leave each a ring of three stages in the 227 KB (1 KB a CTA is the system's); every
-  // CTA of the grid is resident, so the equal runs of keys also end together
+  // CTAs on an SM: as many as leave each a ring of four groups a warp (three, of one group a step) in the 227 KB (1 KB
+  // a CTA is the system's); every CTA of the grid is resident, so the equal runs of keys also end together
+  constexpr int least = groups_per_step(D, E4M3, NB) == 2 ? 2 : 3;
   int ctas = cta_per_sm(NB) + 1, stages = 0;
-  while (stages < 3 && ctas > 1) {
+  while (stages < least && ctas > 1) {
     --ctas;
     stages = std::min(kMaxStages, (227 * 1024 / ctas - 1024 - fixed) / stage);
   }
@@ -752,7 +746,7 @@ cudaError_t launch_bias(const CacheAttnArgs &a, int sms, cudaStream_t st) {
   const int smem = fixed + std::max(join, stages * stage);
   const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const long long blocks = std::max<long long>(1, (((long long)a.max_pages << a.page_shift) + kBlockKeys - 1) / kBlockKeys);
+  const long long blocks = std::max<long long>(1, (((long long)a.max_pages << a.page_shift) + keys - 1) / keys);
   const int grid = int(std::min<long long>((long long)a.B * a.H * a.chunks * blocks, (long long)sms * ctas));
   return launch_programmatic(k, dim3(unsigned(grid)), dim3(kWarps * 32), size_t(smem), st, a, stages);
 }
