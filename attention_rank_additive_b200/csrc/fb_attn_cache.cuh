@@ -98,6 +98,7 @@ __device__ __forceinline__ float odd_sum(const CacheAttnArgs &a, const Seq &s, i
     const int page = a.table[(long long)b * a.max_pages + (j >> a.page_shift)], u = j - s.prefix;
     if (page < 0 || page >= a.num_pages || !(u < 0 || drafted_visible(a, b, t, u))) continue;
     const long long row = (((long long)page * a.H + h) << a.page_shift) + (j & ((1 << a.page_shift) - 1));
+    if (E4M3 && a.vs[row] == 255) return __uint_as_float(0x7fffffffu);
     sum += odd_value<E4M3>(static_cast<const uint8_t *>(a.vp) + row * a.d * (E4M3 ? 1 : 2), dd);
   }
   return sum;

@@ -34,8 +34,13 @@ struct CacheAttnArgs {
   int *flags;
 };
 
-// Floats of partial rows that a call can need, and the launch (a cudaError_t).
+// The kernel for few query rows: floats of partial rows that a call can need, and the launch (a cudaError_t).
 size_t cache_attn_part_floats(int d, int T, int G, int sms);
 cudaError_t launch_attn_cache(CacheAttnArgs a, int e4m3, int sms, cudaStream_t st);
+
+// The kernel for many: whether its tiles fit, and the same.
+bool cache_tile_fits(int d, int R, int rows);
+size_t cache_tile_part_floats(int d, int sms);
+cudaError_t launch_attn_cache_tile(CacheAttnArgs a, int e4m3, int sms, cudaStream_t st);
 
 }  // namespace fb

@@ -1,0 +1,790 @@
+// fb_attn_cache_tile.cu -- attention of many query rows (drafted trees, grouped
+// heads) over a paged cache on the tcgen05 tensor cores. The mathematics, the
+// masks and the work split are those of fb_attn_cache.cu; here the matrix
+// products bound the time, so they run as 128 x 128 tiles.
+//
+// A CTA (one per SM) holds one or two tiles of 128 query rows of an item and
+// walks over its run of 128-key tiles:
+//   warps 0-3, 4-7  softmax of stream 0 and 1: a thread per row (TMEM lane)
+//   warps 8-11      K loader: codes or bf16 from the pages to a swizzled bf16
+//                   tile, and the keys' bias factors
+//   warps 12-14     V loader
+//   warp 15         MMA issuer: S = Q K^T (+ phi_q phi_k^T), O += P V
+// Stream t is row tile t (both walk over the same keys), or, when an item has
+// 128 rows or fewer, every second key tile of the one row tile: the streams
+// then end with a maximum, sum and O each and are joined like two CTAs' parts.
+// Either way the tensor cores work on one stream while the softmax of the other
+// runs: S_0(i), PV_1(i-1), S_1(i), PV_0(i). P overwrites the first half of S.
+//
+// 8-bit rows become bf16 in the loaders, exactly: a code's 3 bits of mantissa fit,
+// its exponent goes to bf16's with the row's power of two, so scores and values
+// need no further scaling. The order of d inside a group of four is (0, 2, 1, 3)
+// then, in Q, K, V and O alike, which saves a byte permutation per word.
+//
+// The bias joins S in the same accumulator: phi_q / scale, split into fp16 parts
+// again, times the keys' prepared parts (three products). Ranks up to 4 are fp32
+// multiply-adds in the softmax.
+#include <algorithm>
+
+#include "fb_attn_cache.cuh"
+
+namespace fb {
+namespace {
+
+constexpr int kThreads = 16 * 32;  // four warps a scheduler: 128 registers a thread
+constexpr int kVThreads = 96;
+constexpr int kIssuer = 15;
+constexpr int kTileKeys = 128;
+constexpr float kRaise = 8.f;  // log2 units: O is rescaled when the maximum grows by more
+
+struct TilePlan {
+  int tiles;  // row tiles of an item's chunk: 1 or 2
+  int split;  // one row tile, its key tiles dealt to two streams
+  int ks, vs; // K and V slots
+  int rpb;    // bias: columns reserved for the hi and for the lo parts (32, 64, 128), or 0
+  uint32_t q, fq, k, fk, v, planes, ctrl;  // shared memory offsets from the 1024-byte aligned base
+  uint32_t smem;
+};
+
+struct Ctrl {
+  uint64_t q_full;
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+  uint64_t s_full[2], p_full[2], o_final[2];
+  uint64_t drain;
+  unsigned alive[4];              // [tile & 3]: bit i: 16-key group i has a page
+  int odd[8];                     // [tile & 7]: tile number + 1 where a non-finite value left the products
+  int seg_odd[2];                 // [segment & 1]: segment number + 1 where one of its tiles was odd
+  uint32_t tmem;
+  int abort, last;
+};
+
+// 16-byte chunk `ch` of row `row` in a tile of 128-byte rows, swizzled; columns past 64 go to the next 128-row block.
+__device__ __forceinline__ uint32_t tile_at(int row, int ch) {
+  return uint32_t(ch >> 3) * (kTileKeys * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4);
+}
+__device__ __forceinline__ uint64_t desc_k(uint32_t base) { return make_smem_desc(base, 16, 1024, swizzle_code(128)); }
+__device__ __forceinline__ uint64_t desc_v(uint32_t base) {
+  return make_smem_desc(base, kTileKeys * 128, 1024, swizzle_code(128));
+}
+// Start-address offsets (16-byte units) of 16-column step kk of a K-major tile, and of 16-key step kk of V.
+__device__ __forceinline__ uint32_t step_k(int kk) { return uint32_t((kk >> 2) * (kTileKeys * 128) + (kk & 3) * 32) >> 4; }
+__device__ __forceinline__ uint32_t step_v(int kk) { return uint32_t(kk * 16 * 128) >> 4; }
+
+// Visibility of keys j0 .. j0 + 31 to new token t, a bit each (t < 0: none past the context).
+__device__ __forceinline__ uint32_t sees(const CacheAttnArgs &a, const Seq &s, int b, int t, int j0) {
+  auto word = [&](int w) -> uint32_t {  // new tokens 32 w .. 32 w + 31
+    if (t < 0 || w * 32 >= s.count) return 0u;
+    uint32_t m;
+    if (a.mask)
+      m = a.mask[((long long)b * a.T + t) * a.mask_words + w];
+    else
+      m = t >= w * 32 + 31 ? 0xffffffffu : (t < w * 32 ? 0u : (2u << (t - w * 32)) - 1u);
+    const int n = s.count - w * 32;
+    return n >= 32 ? m : m & ((1u << n) - 1u);
+  };
+  const int u0 = j0 - s.prefix;
+  if (u0 <= -32) return 0xffffffffu;
+  if (u0 < 0) return ((1u << -u0) - 1u) | (word(0) << -u0);
+  return __funnelshift_r(word(u0 >> 5), u0 & 31 ? word((u0 >> 5) + 1) : 0u, u0 & 31);
+}
+
+// Four e4m3 codes as bf16 pairs (values 0, 2 and 1, 3) times 2^120 c1 c2: the code's bits are bf16's four places
+// lower, with an exponent bias 120 smaller (subnormals too).
+struct RowScale {
+  __nv_bfloat162 c1;
+  float c2;  // 1 but for rows of 2^8 and more
+};
+__device__ __forceinline__ RowScale row_scale(uint32_t byte) {
+  RowScale r;
+  const int e = int(byte) - 127 + 120, e1 = min(e, 127);
+  r.c1 = __float2bfloat162_rn(byte == 255u ? __uint_as_float(0x7fffffffu) : pow2i(e1));
+  r.c2 = pow2i(e - e1);
+  return r;
+}
+__device__ __forceinline__ uint32_t scaled(uint32_t pair, const RowScale &r) {
+  __nv_bfloat162 v = __hmul2(*reinterpret_cast<__nv_bfloat162 *>(&pair), r.c1);
+  if (r.c2 != 1.f) v = __hmul2(v, __float2bfloat162_rn(r.c2));
+  return *reinterpret_cast<uint32_t *>(&v);
+}
+__device__ __forceinline__ void e4m3_to_bf16(uint32_t w, const RowScale &r, uint32_t &p02, uint32_t &p13) {
+  uint32_t e = ((w << 4) & 0x07f007f0u) | ((w << 8) & 0x80008000u);
+  uint32_t o = ((w >> 4) & 0x07f007f0u) | (w & 0x80008000u);
+  if (((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) {  // a NaN code
+    if ((w & 0x7fu) == 0x7fu) e |= 0x7fffu;
+    if ((w & 0x7f0000u) == 0x7f0000u) e |= 0x7fff0000u;
+    if ((w & 0x7f00u) == 0x7f00u) o |= 0x7fffu;
+    if ((w & 0x7f000000u) == 0x7f000000u) o |= 0x7fff0000u;
+  }
+  p02 = scaled(e, r);
+  p13 = scaled(o, r);
+}
+
+__device__ __forceinline__ void sts16(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  st_shared_v4(at, a, b, c, d);
+}
+
+// The page rows of a 128-key tile as one loader thread sees them.
+struct TileRows {
+  const CacheAttnArgs &a;
+  const Seq &s;
+  int b, h, j0, jend;
+  __device__ __forceinline__ int page(int row) const {
+    const int j = j0 + row;
+    if (j >= jend) return -1;
+    const int p = __ldg(a.table + (long long)b * a.max_pages + (j >> a.page_shift));
+    return p >= 0 && p < a.num_pages ? p : -1;
+  }
+  __device__ __forceinline__ long long pool_row(int page, int row) const {
+    return (((long long)page * a.H + h) << a.page_shift) + ((j0 + row) & ((1 << a.page_shift) - 1));
+  }
+};
+
+template <int DP, bool E4M3, int BIAS>
+__global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const CacheAttnArgs a, const TilePlan p) {
+  constexpr int ES = E4M3 ? 1 : 2;
+  constexpr int CPR = DP * ES / 16;  // 16-byte chunks of a pool row (padded); also the chunks of a tile per loader thread
+  constexpr uint32_t kTile = kTileKeys * DP * 2;
+  extern __shared__ __align__(16) uint8_t smem_dyn[];
+  uint8_t *sm = smem_dyn + ((1024u - (smem_u32(smem_dyn) & 1023u)) & 1023u);
+  Ctrl &c = *reinterpret_cast<Ctrl *>(sm + p.ctrl);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t base = smem_u32(sm);
+  // [tile & 3][rank][key]: the keys' factors, ranks up to 4
+  float(*planes)[4][kTileKeys] = reinterpret_cast<float(*)[4][kTileKeys]>(sm + p.planes);
+  const uint32_t fq_tile = kTileKeys * 4 * p.rpb, fk_tile = fq_tile;
+
+  if (threadIdx.x == 0) {
+    mbar_init(&c.q_full, p.tiles * 128);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&c.k_full[i], 128), mbar_init(&c.v_full[i], kVThreads);
+      mbar_init(&c.k_empty[i], 1), mbar_init(&c.v_empty[i], 1);
+      mbar_init(&c.s_full[i], 1), mbar_init(&c.p_full[i], 128), mbar_init(&c.o_final[i], 1);
+    }
+    mbar_init(&c.drain, 1);
+    for (int i = 0; i < 8; ++i) c.odd[i] = 0;
+    c.seg_odd[0] = c.seg_odd[1] = 0;
+    c.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == kIssuer) tmem_alloc(&c.tmem, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = c.tmem;
+  volatile int *abort = &c.abort;
+  griddep_wait();
+
+  // A wait that runs out marks the CTA: every role then runs on through its loops without waiting (all addresses stay
+  // in bounds, the result is garbage) and the call is flagged.
+  Walk walk(a, kTileKeys, lane);
+  Segment g;
+  const int nstreams = p.split || p.tiles == 2 ? 2 : 1;
+  // what a segment's streams do: stream t takes steps of key tiles first + t, first + t + 2, ... (split) or all
+  auto steps_of = [&](int t, int n, int rows) {
+    if (p.split) return (n + 1 - t) >> 1;
+    return t == 0 || rows > 128 ? n : 0;
+  };
+
+  if (blockIdx.x >= walk.ctas) {
+    // no work: only the teardown below
+  } else if (warp < 8) {
+    // ------------------------------------------------------------- softmax
+    const int t = warp >> 2, row = threadIdx.x & 127;
+    const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
+    const uint32_t s_tm = tmem + lane_base + 128u * t, o_tm = tmem + lane_base + 256u + 128u * t;
+    const float unit = BIAS == 1 ? kCacheLog2e : a.scale * kCacheLog2e;  // of the maximum, in log2
+    long long done = 0;    // key tiles of the segments before
+    uint32_t sphase = 0, ophase = 0;
+    int seg = 0;
+    constexpr int kSlot = 256 * (DP + 2);
+    for (; walk.next(a, g); ++seg) {
+      const Seq &s = g.s;
+      const int n = g.k1 - g.k0, h = g.item / a.chunks, chunk0 = (g.item - h * a.chunks) * p.tiles * 128;
+      const int rows = min(p.tiles * 128, a.rows - chunk0);
+      const int r = (p.split ? 0 : t * 128) + row;  // row of the chunk
+      const bool have = r < rows;
+      const long long qrow = ((long long)g.b * a.Hq + (long long)h * a.G) * a.T + chunk0 + (have ? r : 0);
+      const int tok_all = have ? (chunk0 + r) % a.T : 0;
+      const int tok = have && tok_all < s.count ? tok_all : -1;
+      const int steps = t < nstreams ? steps_of(t, n, rows) : 0;
+      float fq[4] = {0.f, 0.f, 0.f, 0.f};
+      if (t < p.tiles || p.split) {
+        const int hq = a.fq_heads > 1 ? h * a.G + (chunk0 + r) / a.T : 0;
+        const int pos = BIAS != 0 && tok >= 0 ? new_position(a, g.b, s, tok) : 0;
+        if (BIAS == 1 && tok >= 0) {
+          const float4 f = __ldg(static_cast<const float4 *>(a.fq) + (long long)hq * a.P + pos);
+          fq[0] = f.x, fq[1] = f.y, fq[2] = f.z, fq[3] = f.w;
+        }
+        if (t < p.tiles) {
+          // this row of the Q tile, and of the factor tile
+          const uint32_t qt = base + p.q + t * kTile;
+          const uint4 *q = reinterpret_cast<const uint4 *>(a.Q + qrow * a.d);
+#pragma unroll
+          for (int ch = 0; ch < DP / 8; ++ch) {
+            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+            if (have && ch * 8 < a.d) v = __ldg(q + ch);
+            if (E4M3)
+              sts16(qt + tile_at(row, ch), __byte_perm(v.x, v.y, 0x5410), __byte_perm(v.x, v.y, 0x7632),
+                    __byte_perm(v.z, v.w, 0x5410), __byte_perm(v.z, v.w, 0x7632));
+            else
+              sts16(qt + tile_at(row, ch), v.x, v.y, v.z, v.w);
+          }
+          if (BIAS == 2) {
+            const uint32_t ft = base + p.fq + t * fq_tile;
+            const float inv = 1.f / a.scale;
+            const uint4 *f = static_cast<const uint4 *>(a.fq) + ((long long)hq * a.P + pos) * (a.RP / 4);
+            bool over = false;
+            for (int i = 0; i < a.RP / 8; ++i) {  // eight ranks: 16 bytes of hi, 16 of lo
+              uint32_t hi[4] = {0u, 0u, 0u, 0u}, lo[4] = {0u, 0u, 0u, 0u};
+              if (tok >= 0) {
+                const uint4 u[2] = {__ldg(f + 2 * i), __ldg(f + 2 * i + 1)};
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                  const uint32_t hw = w == 0 ? u[0].x : (w == 1 ? u[0].y : (w == 2 ? u[1].x : u[1].y));
+                  const uint32_t lw = w == 0 ? u[0].z : (w == 1 ? u[0].w : (w == 2 ? u[1].z : u[1].w));
+                  const float2 h2 = __half22float2(*reinterpret_cast<const __half2 *>(&hw));
+                  const float2 l2 = __half22float2(*reinterpret_cast<const __half2 *>(&lw));
+                  float x0 = (h2.x + l2.x) * inv, x1 = (h2.y + l2.y) * inv;
+                  over |= !(fabsf(x0) <= 65504.f) || !(fabsf(x1) <= 65504.f);
+                  x0 = fminf(fmaxf(x0, -65504.f), 65504.f), x1 = fminf(fmaxf(x1, -65504.f), 65504.f);
+                  const __half2 hh = __floats2half2_rn(x0, x1);
+                  const float2 hf = __half22float2(hh);
+                  const __half2 ll = __floats2half2_rn(x0 - hf.x, x1 - hf.y);
+                  hi[w] = *reinterpret_cast<const uint32_t *>(&hh);
+                  lo[w] = *reinterpret_cast<const uint32_t *>(&ll);
+                }
+              }
+              sts16(ft + tile_at(row, i), hi[0], hi[1], hi[2], hi[3]);
+              sts16(ft + tile_at(row, p.rpb / 8 + i), lo[0], lo[1], lo[2], lo[3]);
+            }
+            if (over) atomicOr(a.flags, kFlagRange);
+          }
+          fence_proxy_async_smem();
+          mbar_arrive(&c.q_full);
+        }
+      }
+      const bool busy = __any_sync(0xffffffffu, tok >= 0);  // rows of this warp that want a result
+      float m = -INFINITY, l = 0.f;
+      int odd = 0;
+      for (int i = 0; i < steps; ++i) {
+        const int idx = p.split ? 2 * i + t : i;
+        const int j0 = (g.k0 + idx) * kTileKeys;
+        const long long tile = done + idx;
+        mbar_wait(&c.s_full[t], sphase & 1u, abort);
+        ++sphase;
+        tc_fence_after();
+        if (i > 0 && c.odd[(tile - (p.split ? 2 : 1)) & 7] == int(tile - (p.split ? 2 : 1)) + 1) odd = 1;
+        if (busy) {
+          const unsigned alive = c.alive[tile & 3];
+          const bool tail = j0 + kTileKeys > s.prefix || alive != 0xffu;
+          // the scores of columns 32 q .. 32 q + 31: biased (rank <= 4), masked
+          auto finish = [&](int q, uint32_t *x) {
+            if constexpr (BIAS == 1) {
+#pragma unroll
+              for (int k = 0; k < 32; k += 4) {
+                float y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int rr = 0; rr < 4; ++rr)
+                  if (rr < a.R) {
+                    const float4 f = *reinterpret_cast<const float4 *>(&planes[tile & 3][rr][32 * q + k]);
+                    y[0] = fmaf(f.x, fq[rr], y[0]), y[1] = fmaf(f.y, fq[rr], y[1]);
+                    y[2] = fmaf(f.z, fq[rr], y[2]), y[3] = fmaf(f.w, fq[rr], y[3]);
+                  }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[k + e] = __float_as_uint(fmaf(__uint_as_float(x[k + e]), a.scale, y[e]));
+              }
+            }
+            if (tail) {
+              uint32_t see = sees(a, s, g.b, tok, j0 + 32 * q);
+              if (!((alive >> (2 * q)) & 1u)) see &= 0xffff0000u;
+              if (!((alive >> (2 * q + 1)) & 1u)) see &= 0x0000ffffu;
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (!((see >> k) & 1u)) x[k] = 0xff800000u;
+            }
+          };
+          float top = -INFINITY;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t x[32];
+            tmem_ld32(s_tm + 32u * q, x);
+            tmem_ld_wait32(x);
+            finish(q, x);
+#pragma unroll
+            for (int k = 0; k < 32; k += 2) top = fmax3(top, __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
+          }
+          const bool raise = (top - m) * unit > kRaise;  // the first finite score too: m is -inf
+          if (__any_sync(0xffffffffu, raise)) {
+            const float alpha = raise ? ex2_approx((m - top) * unit) : 1.f;
+            if (raise) m = top;
+            l *= alpha;
+            if (i > 0) {
+#pragma unroll
+              for (int q = 0; q < DP / 32; ++q) {
+                uint32_t x[32];
+                tmem_ld32(o_tm + 32u * q, x);
+                tmem_ld_wait32(x);
+#pragma unroll
+                for (int k = 0; k < 32; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * alpha);
+                tmem_st32(o_tm + 32u * q, x);
+              }
+            }
+          }
+          const float mu = m == -INFINITY ? 0.f : m;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t x[32];
+            tmem_ld32(s_tm + 32u * q, x);
+            tmem_ld_wait32(x);
+            finish(q, x);
+            uint32_t w[16];
+            float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+            for (int k = 0; k < 32; k += 2) {
+              const float e0 = ex2_approx((__uint_as_float(x[k]) - mu) * unit);
+              const float e1 = ex2_approx((__uint_as_float(x[k + 1]) - mu) * unit);
+              sum0 += e0, sum1 += e1;
+              w[k / 2] = pack_bf16x2(e0, e1);
+            }
+            l += sum0 + sum1;
+            tmem_st16(s_tm + 16u * q, w);
+          }
+          tmem_st_wait();
+        }
+        tc_fence_before();
+        mbar_arrive(&c.p_full[t]);
+      }
+      // ---- the segment's end
+      if (steps > 0) {
+        mbar_wait(&c.o_final[t], ophase & 1u, abort);
+        ++ophase;
+        tc_fence_after();
+        const long long tile = done + (p.split ? 2 * (steps - 1) + t : steps - 1);
+        if (c.odd[tile & 7] == int(tile) + 1) odd = 1;
+      }
+      done += n;
+      float nat = BIAS == 1 || m == -INFINITY ? m : m * a.scale;  // the maximum in natural units
+      const bool whole = g.k0 == 0 && g.k1 == g.blocks;
+      float *mine = a.part + (2ll * blockIdx.x + (g.k0 == 0)) * kSlot;
+      if (!busy) nat = -INFINITY, l = 0.f;
+      // stream 1 of a split: its part to rows 128 .. 255 of the slot; stream 0 joins it
+      if (p.split && t == 1) {
+        const int at = 128 + row;
+        mine[DP * 256 + at] = nat, mine[(DP + 1) * 256 + at] = l;
+        if (steps > 0 && busy) {
+#pragma unroll
+          for (int q = 0; q < DP / 32; ++q) {
+            uint32_t x[32];
+            tmem_ld32(o_tm + 32u * q, x);
+            tmem_ld_wait32(x);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) mine[(32 * q + k) * 256 + at] = __uint_as_float(x[k]);
+          }
+        }
+      }
+      if (odd) c.seg_odd[seg & 1] = seg + 1;
+      named_bar_sync(1, 256);
+      if (t < p.tiles) {
+        float f0 = 1.f, f1 = 0.f;
+        if (p.split) {
+          const float m1 = mine[DP * 256 + 128 + row], l1 = mine[(DP + 1) * 256 + 128 + row];
+          const float top = fmaxf(nat, m1);
+          f0 = nat == -INFINITY ? 0.f : ex2_approx((nat - top) * kCacheLog2e);
+          f1 = m1 == -INFINITY ? 0.f : ex2_approx((m1 - top) * kCacheLog2e);
+          l = l * f0 + l1 * f1;
+          nat = top;
+        }
+        const bool none = tok < 0 || nat == -INFINITY;
+        if (have && whole) a.LSE[qrow] = none ? -INFINITY : nat + logf(l);
+        if (!whole) mine[DP * 256 + r] = nat, mine[(DP + 1) * 256 + r] = l;
+        const bool any_odd = c.seg_odd[seg & 1] == seg + 1;
+        const float inv = none ? 0.f : 1.f / l;
+        const int odd0 = max(g.k0 * kTileKeys, s.prefix / kTileKeys * kTileKeys), odd1 = min(s.len, g.k1 * kTileKeys);
+#pragma unroll
+        for (int q = 0; q < DP / 32; ++q) {
+          uint32_t x[32];
+#pragma unroll
+          for (int k = 0; k < 32; ++k) x[k] = 0u;
+          if (steps > 0 && busy) {  // uniform over the warp
+            tmem_ld32(o_tm + 32u * q, x);
+            tmem_ld_wait32(x);
+          }
+          if (p.split) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              float v = f0 == 0.f ? 0.f : __uint_as_float(x[k]) * f0;
+              if (f1 != 0.f) v = fmaf(mine[(32 * q + k) * 256 + 128 + row], f1, v);
+              x[k] = __float_as_uint(v);
+            }
+          }
+          if (any_odd && tok >= 0) {
+#pragma unroll 1
+            for (int k = 0; k < 32; ++k) {
+              const int dd = 32 * q + (E4M3 ? (k & ~3) + ((k & 1) << 1 | ((k >> 1) & 1)) : k);
+              if (dd < a.d) {
+                const float bad = odd_sum<E4M3>(a, s, g.b, h, tok, dd, odd0, odd1);
+                if (bad != 0.f)
+#pragma unroll
+                  for (int e = 0; e < 32; ++e)
+                    if (e == k) x[e] = __float_as_uint(__uint_as_float(x[e]) + bad);
+              }
+            }
+          }
+          if (whole) {
+            if (have) {
+              uint4 *o = reinterpret_cast<uint4 *>(a.O + qrow * a.d + 32 * q);
+#pragma unroll
+              for (int k = 0; k < 32; k += 8) {
+                float y[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  const int src = E4M3 ? (e & ~3) + ((e & 1) << 1 | ((e >> 1) & 1)) : e;
+                  y[e] = none ? 0.f : __uint_as_float(x[k + src]) * inv;
+                }
+                if (32 * q + k < a.d)
+                  o[k / 8] = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
+                                        pack_bf16x2(y[6], y[7]));
+              }
+            }
+          } else {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) mine[(32 * q + k) * 256 + r] = __uint_as_float(x[k]);
+          }
+        }
+      }
+      if (!whole) {
+        const int c0 = walk.owner(g.start), c1 = walk.owner(g.start + g.blocks - 1);
+        __threadfence();
+        named_bar_sync(1, 256);
+        if (threadIdx.x == 0) c.last = atomicAdd(a.counters + c0, 1u) == unsigned(c1 - c0);
+        named_bar_sync(1, 256);
+        if (c.last && t < p.tiles && have) {
+          __threadfence();
+          float top = -INFINITY;
+          for (int cc = c0; cc <= c1; ++cc) top = fmaxf(top, __ldcg(a.part + (2ll * cc + (cc == c0)) * kSlot + DP * 256 + r));
+          const bool none = tok < 0 || top == -INFINITY;
+          float sum = 0.f;
+          for (int cc = c0; cc <= c1; ++cc) {
+            const float *part = a.part + (2ll * cc + (cc == c0)) * kSlot;
+            const float mc = __ldcg(part + DP * 256 + r);
+            if (mc != -INFINITY) sum += __ldcg(part + (DP + 1) * 256 + r) * ex2_approx((mc - top) * kCacheLog2e);
+          }
+          a.LSE[qrow] = none ? -INFINITY : top + logf(sum);
+          const float inv = none ? 0.f : 1.f / sum;
+#pragma unroll 1
+          for (int k = 0; k < a.d; k += 8) {
+            float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            if (!none)
+              for (int cc = c0; cc <= c1; ++cc) {
+                const float *part = a.part + (2ll * cc + (cc == c0)) * kSlot;
+                const float mc = __ldcg(part + DP * 256 + r);
+                if (mc == -INFINITY) continue;
+                const float f = ex2_approx((mc - top) * kCacheLog2e) * inv;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  const int src = E4M3 ? (e & ~3) + ((e & 1) << 1 | ((e >> 1) & 1)) : e;
+                  y[e] = fmaf(__ldcg(part + (k + src) * 256 + r), f, y[e]);
+                }
+              }
+            *reinterpret_cast<uint4 *>(a.O + qrow * a.d + k) =
+                make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+          }
+        }
+        named_bar_sync(1, 256);
+        if (threadIdx.x == 0 && c.last) a.counters[c0] = 0u;  // for the next call
+      }
+      if (p.split) named_bar_sync(1, 256);  // stream 1's part has been read
+    }
+  } else if (warp < kIssuer) {
+    // ------------------------------------------------------------- loaders
+    // A tile's chunk of 16 bytes of a pool row becomes one (bf16) or two (e4m3) of a tile's chunks.
+    auto convert = [&](const uint4 &raw, uint32_t scale, uint4 &x, uint4 &y) {
+      x = raw;
+      if constexpr (E4M3) {
+        const RowScale rs = row_scale(scale);
+        e4m3_to_bf16(raw.x, rs, x.x, x.y), e4m3_to_bf16(raw.y, rs, x.z, x.w);
+        e4m3_to_bf16(raw.z, rs, y.x, y.y), e4m3_to_bf16(raw.w, rs, y.z, y.w);
+      }
+    };
+    auto store = [&](uint32_t dst, int row, int ch, const uint4 &x, const uint4 &y) {
+      if constexpr (E4M3) {
+        sts16(dst + tile_at(row, 2 * ch), x.x, x.y, x.z, x.w);
+        sts16(dst + tile_at(row, 2 * ch + 1), y.x, y.y, y.z, y.w);
+      } else {
+        sts16(dst + tile_at(row, ch), x.x, x.y, x.z, x.w);
+      }
+    };
+    long long tile = 0;
+    if (warp < 12) {
+      // K: loaded and converted before its slot is free, so that the tensor cores wait for the stores alone
+      const int l = threadIdx.x & 127;
+      while (walk.next(a, g)) {
+        const Seq &s = g.s;
+        const int h = g.item / a.chunks, hk = a.fk_heads > 1 ? h : 0;
+        for (int kt = g.k0; kt < g.k1; ++kt, ++tile) {
+          const TileRows rows{a, s, g.b, h, kt * kTileKeys, min(s.len, (kt + 1) * kTileKeys)};
+          const int slot = int(tile % p.ks);
+          const uint32_t dst = base + p.k + slot * kTile;
+          // chunk i of this thread: 16 bytes at ch of row row0 + i * (128 / CPR)
+          const int ch = l % CPR, row0 = l / CPR;
+          uint4 raw[CPR], more[E4M3 ? CPR : 1];
+          uint32_t sc[E4M3 ? CPR : 1];
+#pragma unroll
+          for (int i = 0; i < CPR; ++i) {
+            const int row = row0 + i * (128 / CPR), page = rows.page(row);
+            raw[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (E4M3) sc[E4M3 ? i : 0] = 127u;
+            if (page >= 0) {
+              const long long pr = rows.pool_row(page, row);
+              if (ch * 16 < a.d * ES)
+                raw[i] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(a.kp) + pr * (a.d * ES) + ch * 16));
+              if (E4M3) sc[E4M3 ? i : 0] = __ldg(a.ks + pr);
+            }
+          }
+          unsigned alive = 0u;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int j = rows.j0 + 16 * i;
+            if (j >= rows.jend || rows.page(16 * i) >= 0) alive |= 1u << i;  // behind the last key is the masks' affair
+          }
+          if (alive != 0xffu && l == 0) atomicOr(a.flags, kFlagRange);
+          auto position = [&](int row) {
+            const int j = rows.j0 + row;
+            if (j >= rows.jend) return 0;
+            if (j >= s.prefix) return new_position(a, g.b, s, j - s.prefix);
+            if (j < a.P) return j;
+            atomicOr(a.flags, kFlagRange);
+            return a.P - 1;
+          };
+          // (4 hi, 4 lo) groups of the keys' factors, eight loads at a time, the first eight ahead like K
+          constexpr int kBatch = 8;
+          const int groups = a.RP / 4, total = kTileKeys * groups;
+          const uint4 *fbase = static_cast<const uint4 *>(a.fk) + (BIAS == 2 ? (long long)hk * a.P * groups : 0ll);
+          uint4 f[BIAS == 2 ? kBatch : 1];
+          auto factors = [&](int at) {
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+              const int e = at + i * 128 + l, row = e / groups;
+              if (e < total) f[BIAS == 2 ? i : 0] = __ldg(fbase + (long long)position(row) * groups + (e - row * groups));
+            }
+          };
+          if constexpr (BIAS == 2) factors(0);
+          if constexpr (BIAS == 1) f[0] = __ldg(static_cast<const uint4 *>(a.fk) + (long long)hk * a.P + position(l));
+#pragma unroll
+          for (int i = 0; i < CPR; ++i) {
+            const uint4 was = raw[i];
+            convert(was, sc[E4M3 ? i : 0], raw[i], more[E4M3 ? i : 0]);
+          }
+          if (tile >= p.ks) mbar_wait(&c.k_empty[slot], uint32_t(tile / p.ks - 1) & 1u, abort);
+#pragma unroll
+          for (int i = 0; i < CPR; ++i) store(dst, row0 + i * (128 / CPR), ch, raw[i], more[E4M3 ? i : 0]);
+          if (l == 0) c.alive[tile & 3] = alive;
+          if constexpr (BIAS == 1) {
+            float(*pl)[kTileKeys] = planes[tile & 3];
+            pl[0][l] = __uint_as_float(f[0].x), pl[1][l] = __uint_as_float(f[0].y);
+            pl[2][l] = __uint_as_float(f[0].z), pl[3][l] = __uint_as_float(f[0].w);
+          }
+          if constexpr (BIAS == 2) {
+            const uint32_t ft = base + p.fk + slot * fk_tile;
+            for (int at = 0; at < total; at += kBatch * 128) {
+              if (at > 0) factors(at);
+#pragma unroll
+              for (int i = 0; i < kBatch; ++i) {
+                const int e = at + i * 128 + l, row = e / groups, q = e - row * groups;
+                if (e >= total) continue;
+                const uint32_t hi = ft + tile_at(row, q >> 1) + (q & 1) * 8;
+                const uint32_t lo = ft + tile_at(row, p.rpb / 8 + (q >> 1)) + (q & 1) * 8;
+                asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(hi), "r"(f[i].x), "r"(f[i].y) : "memory");
+                asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(lo), "r"(f[i].z), "r"(f[i].w) : "memory");
+              }
+            }
+          }
+          fence_proxy_async_smem();
+          mbar_arrive(&c.k_full[slot]);
+        }
+      }
+    } else {
+      const int l = threadIdx.x - 12 * 32;
+      constexpr int kMine = (128 * CPR + kVThreads - 1) / kVThreads;  // chunks of this thread
+      while (walk.next(a, g)) {
+        const Seq &s = g.s;
+        const int h = g.item / a.chunks;
+        for (int kt = g.k0; kt < g.k1; ++kt, ++tile) {
+          const TileRows rows{a, s, g.b, h, kt * kTileKeys, min(s.len, (kt + 1) * kTileKeys)};
+          const bool tail = (kt + 1) * kTileKeys > s.prefix;
+          const int slot = int(tile % p.vs);
+          const uint32_t dst = base + p.v + slot * kTile;
+          uint4 raw[kMine];
+          uint32_t sc[E4M3 ? kMine : 1];
+#pragma unroll
+          for (int i = 0; i < kMine; ++i) {
+            const int e = i * kVThreads + l, row = e / CPR, ch = e % CPR;
+            const int page = e < 128 * CPR ? rows.page(row) : -1;
+            raw[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (E4M3) sc[E4M3 ? i : 0] = 127u;
+            if (page >= 0) {
+              const long long pr = rows.pool_row(page, row);
+              if (ch * 16 < a.d * ES)
+                raw[i] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(a.vp) + pr * (a.d * ES) + ch * 16));
+              if (E4M3) sc[E4M3 ? i : 0] = __ldg(a.vs + pr);
+            }
+          }
+          if (tile >= p.vs) mbar_wait(&c.v_empty[slot], uint32_t(tile / p.vs - 1) & 1u, abort);
+          bool odd = false;
+#pragma unroll
+          for (int i = 0; i < kMine; ++i) {
+            const int e = i * kVThreads + l;
+            if (e >= 128 * CPR) continue;
+            uint4 out[2];
+            convert(raw[i], sc[E4M3 ? i : 0], out[0], out[1]);
+            if (tail) {
+              uint32_t *w = reinterpret_cast<uint32_t *>(out);
+#pragma unroll
+              for (int k = 0; k < (E4M3 ? 8 : 4); ++k) {
+                const uint32_t even = even_word<false>(w[k]);
+                odd |= even != w[k];
+                w[k] = even;
+              }
+            }
+            store(dst, e / CPR, e % CPR, out[0], out[1]);
+          }
+          if (odd) c.odd[tile & 7] = int(tile) + 1;
+          fence_proxy_async_smem();
+          mbar_arrive(&c.v_full[slot]);
+        }
+      }
+    }
+  } else {
+    // ---------------------------------------------------------- MMA issuer
+    constexpr uint32_t kQK = make_idesc_f16(true, true, 128, 128, false);
+    constexpr uint32_t kF = make_idesc_f16(false, false, 128, 128, false);
+    constexpr uint32_t kPV = make_idesc_f16(true, true, 128, DP, true);
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    long long done = 0;
+    uint32_t qphase = 0, pphase[2] = {0, 0};
+    while (walk.next(a, g)) {
+      const int n = g.k1 - g.k0, h = g.item / a.chunks;
+      const int rows = min(p.tiles * 128, a.rows - (g.item - h * a.chunks) * p.tiles * 128);
+      const int n0 = steps_of(0, n, rows), n1 = nstreams == 2 ? steps_of(1, n, rows) : 0;
+      mbar_wait(&c.q_full, qphase & 1u, abort);
+      ++qphase;
+      auto score = [&](int t, int i) {
+        const long long tile = done + (p.split ? 2 * i + t : i);
+        const int slot = int(tile % p.ks);
+        if (t == 0 || p.split) mbar_wait(&c.k_full[slot], uint32_t(tile / p.ks) & 1u, abort);
+        tc_fence_after();
+        const uint32_t d = tm + 128u * t;
+        const int rt = p.split ? 0 : t;
+        const uint64_t dq = desc_k(base + p.q + rt * kTile), dk = desc_k(base + p.k + slot * kTile);
+#pragma unroll
+        for (int kk = 0; kk < DP / 16; ++kk) mma_ss_elect(d, dq + step_k(kk), dk + step_k(kk), kQK, kk > 0 ? 1u : 0u);
+        if constexpr (BIAS == 2) {
+          const uint64_t df = desc_k(base + p.fq + rt * fq_tile), dg = desc_k(base + p.fk + slot * fk_tile);
+          const int low = p.rpb / 16;
+          for (int kk = 0; kk < a.RP / 16; ++kk) {
+            mma_ss_elect(d, df + step_k(kk), dg + step_k(kk), kF, 1u);
+            mma_ss_elect(d, df + step_k(low + kk), dg + step_k(kk), kF, 1u);
+            mma_ss_elect(d, df + step_k(kk), dg + step_k(low + kk), kF, 1u);
+          }
+        }
+        tc_commit_elect(&c.s_full[t]);
+        if (p.split || n1 == 0 || t == 1) tc_commit_elect(&c.k_empty[slot]);
+      };
+      auto product = [&](int t, int i, bool final) {
+        const long long tile = done + (p.split ? 2 * i + t : i);
+        const int slot = int(tile % p.vs);
+        mbar_wait(&c.v_full[slot], uint32_t(tile / p.vs) & 1u, abort);
+        mbar_wait(&c.p_full[t], pphase[t] & 1u, abort);
+        ++pphase[t];
+        tc_fence_after();
+        const uint32_t d = tm + 256u + 128u * t, pt = tm + 128u * t;
+        const uint64_t dv = desc_v(base + p.v + slot * kTile);
+#pragma unroll
+        for (int kk = 0; kk < kTileKeys / 16; ++kk)
+          mma_ts_elect(d, pt + uint32_t(kk * 8), dv + step_v(kk), kPV, i > 0 || kk > 0 ? 1u : 0u);
+        if (p.split || n1 == 0 || t == 1) tc_commit_elect(&c.v_empty[slot]);
+        if (final) tc_commit_elect(&c.o_final[t]);
+      };
+      for (int i = 0; i < n0; ++i) {
+        score(0, i);
+        if (i > 0 && i - 1 < n1) product(1, i - 1, i - 1 == n1 - 1);
+        if (i < n1) score(1, i);
+        product(0, i, i == n0 - 1);
+      }
+      if (n1 == n0 && n1 > 0) product(1, n1 - 1, true);
+      done += n;
+    }
+    tc_commit_elect(&c.drain);
+    if (!mbar_wait_for(&c.drain, 0, 1000000000ull)) c.abort = 1;
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kIssuer) {
+    tmem_relinquish();
+    tmem_dealloc(tmem, 512);
+  }
+  if (threadIdx.x == 0 && c.abort) atomicOr(a.flags, kFlagTimeout);
+}
+
+// The shared-memory plan, or smem = 0 where none fits.
+TilePlan make_plan(int d, int R, int rows) {
+  const int DP = d <= 64 ? 64 : 128;
+  const int RP = (R + 15) / 16 * 16;
+  const uint32_t tile = kTileKeys * DP * 2;
+  TilePlan best{};
+  // One or two row tiles, then K and V slots. One K slot costs less than one V slot: K is stored ready-made.
+  static const int kOptions[6][3] = {{2, 2, 2}, {2, 1, 2}, {2, 1, 1}, {1, 2, 2}, {1, 1, 2}, {1, 1, 1}};
+  for (const auto &o : kOptions) {
+    TilePlan p{};
+    p.tiles = o[0], p.ks = o[1], p.vs = o[2];
+    if (p.tiles == 2 && rows <= 128) continue;
+    p.rpb = R <= kCacheBiasExact ? 0 : (RP <= 32 ? 32 : (RP <= 64 ? 64 : 128));
+    const uint32_t f = kTileKeys * 4 * p.rpb;
+    p.q = 0;
+    p.fq = p.q + p.tiles * tile;
+    p.k = p.fq + p.tiles * f;
+    p.fk = p.k + p.ks * tile;
+    p.v = p.fk + p.ks * f;
+    p.planes = p.v + p.vs * tile;
+    p.ctrl = p.planes + (R > 0 && R <= kCacheBiasExact ? 4 * 4 * kTileKeys * 4 : 0);
+    p.smem = p.ctrl + uint32_t(sizeof(Ctrl)) + 1024;
+    p.split = p.tiles == 1 && p.ks == 2 && p.vs == 2;
+    if (p.smem <= 227u * 1024u) {
+      best = p;
+      break;
+    }
+  }
+  // more than half of the SM's shared memory: one CTA an SM, which takes all of the SM's TMEM
+  if (best.smem) best.smem = std::max(best.smem, 120u * 1024u);
+  return best;
+}
+
+template <int DP, bool E4M3>
+cudaError_t launch_tile(const CacheAttnArgs &a, const TilePlan &p, int grid, cudaStream_t st) {
+  void (*k)(const CacheAttnArgs, const TilePlan) =
+      a.R == 0 ? attn_cache_tile_kernel<DP, E4M3, 0>
+               : (a.R <= kCacheBiasExact ? attn_cache_tile_kernel<DP, E4M3, 1> : attn_cache_tile_kernel<DP, E4M3, 2>);
+  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(p.smem));
+  if (e != cudaSuccess) return e;
+  return launch_programmatic(k, dim3(unsigned(grid)), dim3(kThreads), size_t(p.smem), st, a, p);
+}
+
+}  // namespace
+
+bool cache_tile_fits(int d, int R, int rows) { return make_plan(d, R, rows).smem != 0; }
+
+size_t cache_tile_part_floats(int d, int sms) { return size_t(2) * sms * 256 * ((d <= 64 ? 64 : 128) + 2); }
+
+cudaError_t launch_attn_cache_tile(CacheAttnArgs a, int e4m3, int sms, cudaStream_t st) {
+  const TilePlan p = make_plan(a.d, a.R, a.rows);
+  if (!p.smem) return cudaErrorInvalidValue;
+  a.chunks = (a.rows + p.tiles * 128 - 1) / (p.tiles * 128);
+  const long long blocks = std::max<long long>(1, (((long long)a.max_pages << a.page_shift) + kTileKeys - 1) / kTileKeys);
+  const int grid = int(std::min<long long>((long long)a.B * a.H * a.chunks * blocks, sms));
+  if (a.d <= 64) return e4m3 ? launch_tile<64, true>(a, p, grid, st) : launch_tile<64, false>(a, p, grid, st);
+  return e4m3 ? launch_tile<128, true>(a, p, grid, st) : launch_tile<128, false>(a, p, grid, st);
+}
+
+}  // namespace fb

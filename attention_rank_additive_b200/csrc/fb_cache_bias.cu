@@ -109,6 +109,9 @@ bool sizes_ok(int B, int Hq, int H, int T, int d) {
          Hq <= (1 << 14) && B <= (1 << 20) && (long long)Hq * T <= (1 << 24);
 }
 
+// Query rows of an item (heads of a group times tokens) above which the 128-row tiles are used.
+constexpr int kTileRows = 16;
+
 }  // namespace
 }  // namespace fb
 
@@ -156,7 +159,8 @@ int fb_cache_bias_prepare(int Hq, int H, int P, int R, const float *phi_q, const
 
 size_t fb_attn_cache_workspace_bytes(int B, int Hq, int H, int T, int d) {
   if (!sizes_ok(B, Hq, H, T, d)) return 0;
-  const size_t part = cache_attn_part_floats(d, T, Hq / H, sm_count()) * 4;
+  size_t part = cache_attn_part_floats(d, T, Hq / H, sm_count()) * 4;
+  if (Hq / H * T > kTileRows) part = std::max(part, cache_tile_part_floats(d, sm_count()) * 4);
   return kCounterBytes + (part + 255) / 256 * 256;
 }
 
@@ -215,7 +219,9 @@ int fb_attn_cache_fwd(int cache_dt, int B, int Hq, int H, int T, int d, const vo
     a.fk = base + size_t(phi_q_heads) * P * row;
   }
   a.flags = flags;
-  const cudaError_t e = launch_attn_cache(a, cache_dt == FB_E4M3, sm_count(), static_cast<cudaStream_t>(stream));
+  const bool tiles = a.rows > kTileRows && cache_tile_fits(d, R, a.rows);
+  const cudaError_t e = (tiles ? launch_attn_cache_tile : launch_attn_cache)(a, cache_dt == FB_E4M3, sm_count(),
+                                                                            static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? FB_OK : FB_ERR_CUDA;
 }
 

@@ -572,8 +572,11 @@ int fb_cache_bias_prepare(int Hq, int H, int P, int R, const float *phi_q, const
  * do not reach it. Cache rows that the table does not lead to are not seen and
  * flag FB_ERR_RANGE.
  * Arithmetic: products of bf16 queries with bf16 or e4m3 keys are exact, sums
- * and the softmax are fp32; the probabilities are rounded once, to bf16 (bf16
- * cache) or fp16 (e4m3), for the product with V. Bitwise reproducible.
+ * and the softmax are fp32; the probabilities are rounded once for the product
+ * with V, to bf16, or to fp16 where an e4m3 cache meets at most 16 query rows of
+ * a key/value head (T Hq / H; more rows go through 128-row tiles, where a bias of
+ * rank 5 and up also passes fp16 as phi_q / scale and may flag FB_ERR_RANGE from
+ * 2^26 on). Bitwise reproducible.
  */
 size_t fb_attn_cache_workspace_bytes(int B, int Hq, int H, int T, int d);
 
