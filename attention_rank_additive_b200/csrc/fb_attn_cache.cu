@@ -152,7 +152,7 @@ __host__ __device__ __forceinline__ int stage_bytes(int d, bool e4m3, int bias, 
 }
 
 template <int D, bool E4M3, int NB, int BIAS>
-__global__ void __launch_bounds__(kWarps * 32, cta_per_sm(NB)) attn_cache_kernel(const CacheAttnArgs a, const int stages) {
+__global__ void __launch_bounds__(kWarps * 32, cta_per_sm(NB)) attn_cache_kernel(const __grid_constant__ CacheAttnArgs a, const int stages) {
   using L = Lay<D, E4M3>;
   constexpr int KS = D / 16, ROWS = 8 * NB, KM = groups_per_step(D, E4M3, NB);
   constexpr int BK = 16 * KM * kWarps;  // a block of keys: a step of each warp

@@ -17,13 +17,18 @@
 // runs: S_0(i), PV_1(i-1), S_1(i), PV_0(i). P overwrites the first half of S.
 //
 // 8-bit rows become bf16 in the loaders, exactly: a code's 3 bits of mantissa fit,
-// its exponent goes to bf16's with the row's power of two, so scores and values
-// need no further scaling. The order of d inside a group of four is (0, 2, 1, 3)
-// then, in Q, K, V and O alike, which saves a byte permutation per word.
+// and its exponent with the row's power of two as well, so scores and values
+// need no further scaling.
+//
+// The roles run side by side out of one instruction cache, so loops stay rolled
+// where they can: with all of them unrolled, warps waited for instructions ten
+// cycles of each twenty-four and grouped trees of 61 tokens took 972 us.
 //
 // The bias joins S in the same accumulator: phi_q / scale, split into fp16 parts
 // again, times the keys' prepared parts (three products). Ranks up to 4 are fp32
 // multiply-adds in the softmax.
+#include <cuda_fp8.h>
+
 #include <algorithm>
 
 #include "fb_attn_cache.cuh"
@@ -71,52 +76,33 @@ __device__ __forceinline__ uint32_t step_k(int kk) { return uint32_t((kk >> 2) *
 __device__ __forceinline__ uint32_t step_v(int kk) { return uint32_t(kk * 16 * 128) >> 4; }
 
 // Visibility of keys j0 .. j0 + 31 to new token t, a bit each (t < 0: none past the context).
-__device__ __forceinline__ uint32_t sees(const CacheAttnArgs &a, const Seq &s, int b, int t, int j0) {
+__device__ __noinline__ uint32_t sees(const CacheAttnArgs &a, int prefix, int count, int b, int t, int j0) {
   auto word = [&](int w) -> uint32_t {  // new tokens 32 w .. 32 w + 31
-    if (t < 0 || w * 32 >= s.count) return 0u;
+    if (t < 0 || w * 32 >= count) return 0u;
     uint32_t m;
     if (a.mask)
       m = a.mask[((long long)b * a.T + t) * a.mask_words + w];
     else
       m = t >= w * 32 + 31 ? 0xffffffffu : (t < w * 32 ? 0u : (2u << (t - w * 32)) - 1u);
-    const int n = s.count - w * 32;
+    const int n = count - w * 32;
     return n >= 32 ? m : m & ((1u << n) - 1u);
   };
-  const int u0 = j0 - s.prefix;
+  const int u0 = j0 - prefix;
   if (u0 <= -32) return 0xffffffffu;
   if (u0 < 0) return ((1u << -u0) - 1u) | (word(0) << -u0);
   return __funnelshift_r(word(u0 >> 5), u0 & 31 ? word((u0 >> 5) + 1) : 0u, u0 & 31);
 }
 
-// Four e4m3 codes as bf16 pairs (values 0, 2 and 1, 3) times 2^120 c1 c2: the code's bits are bf16's four places
-// lower, with an exponent bias 120 smaller (subnormals too).
-struct RowScale {
-  __nv_bfloat162 c1;
-  float c2;  // 1 but for rows of 2^8 and more
-};
-__device__ __forceinline__ RowScale row_scale(uint32_t byte) {
-  RowScale r;
-  const int e = int(byte) - 127 + 120, e1 = min(e, 127);
-  r.c1 = __float2bfloat162_rn(byte == 255u ? __uint_as_float(0x7fffffffu) : pow2i(e1));
-  r.c2 = pow2i(e - e1);
-  return r;
+template <bool E4M3>
+__device__ __noinline__ float odd_sum_of(const CacheAttnArgs &a, Seq s, int b, int h, int t, int dd, int j0, int j1) {
+  return odd_sum<E4M3>(a, s, b, h, t, dd, j0, j1);
 }
-__device__ __forceinline__ uint32_t scaled(uint32_t pair, const RowScale &r) {
-  __nv_bfloat162 v = __hmul2(*reinterpret_cast<__nv_bfloat162 *>(&pair), r.c1);
-  if (r.c2 != 1.f) v = __hmul2(v, __float2bfloat162_rn(r.c2));
-  return *reinterpret_cast<uint32_t *>(&v);
-}
-__device__ __forceinline__ void e4m3_to_bf16(uint32_t w, const RowScale &r, uint32_t &p02, uint32_t &p13) {
-  uint32_t e = ((w << 4) & 0x07f007f0u) | ((w << 8) & 0x80008000u);
-  uint32_t o = ((w >> 4) & 0x07f007f0u) | (w & 0x80008000u);
-  if (((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) {  // a NaN code
-    if ((w & 0x7fu) == 0x7fu) e |= 0x7fffu;
-    if ((w & 0x7f0000u) == 0x7f0000u) e |= 0x7fff0000u;
-    if ((w & 0x7f00u) == 0x7f00u) o |= 0x7fffu;
-    if ((w & 0x7f000000u) == 0x7f000000u) o |= 0x7fff0000u;
-  }
-  p02 = scaled(e, r);
-  p13 = scaled(o, r);
+
+// Two e4m3 codes (half `hi` of w) times a scale, as bf16; NaN codes stay NaN.
+__device__ __forceinline__ uint32_t e4m3_to_bf16(uint32_t w, bool hi, float scale) {
+  const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(hi ? w >> 16 : w & 0xffffu), __NV_E4M3);
+  const float2 f = __half22float2(__half2(r));
+  return pack_bf16x2(f.x * scale, f.y * scale);
 }
 
 __device__ __forceinline__ void sts16(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -140,7 +126,7 @@ struct TileRows {
 };
 
 template <int DP, bool E4M3, int BIAS>
-__global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const CacheAttnArgs a, const TilePlan p) {
+__global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const __grid_constant__ CacheAttnArgs a, const TilePlan p) {
   constexpr int ES = E4M3 ? 1 : 2;
   constexpr int CPR = DP * ES / 16;  // 16-byte chunks of a pool row (padded); also the chunks of a tile per loader thread
   constexpr uint32_t kTile = kTileKeys * DP * 2;
@@ -219,15 +205,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const Cach
           // this row of the Q tile, and of the factor tile
           const uint32_t qt = base + p.q + t * kTile;
           const uint4 *q = reinterpret_cast<const uint4 *>(a.Q + qrow * a.d);
-#pragma unroll
+#pragma unroll 8
           for (int ch = 0; ch < DP / 8; ++ch) {
             uint4 v = make_uint4(0u, 0u, 0u, 0u);
             if (have && ch * 8 < a.d) v = __ldg(q + ch);
-            if (E4M3)
-              sts16(qt + tile_at(row, ch), __byte_perm(v.x, v.y, 0x5410), __byte_perm(v.x, v.y, 0x7632),
-                    __byte_perm(v.z, v.w, 0x5410), __byte_perm(v.z, v.w, 0x7632));
-            else
-              sts16(qt + tile_at(row, ch), v.x, v.y, v.z, v.w);
+            sts16(qt + tile_at(row, ch), v.x, v.y, v.z, v.w);
           }
           if (BIAS == 2) {
             const uint32_t ft = base + p.fq + t * fq_tile;
@@ -295,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const Cach
               }
             }
             if (tail) {
-              uint32_t see = sees(a, s, g.b, tok, j0 + 32 * q);
+              uint32_t see = sees(a, s.prefix, s.count, g.b, tok, j0 + 32 * q);
               if (!((alive >> (2 * q)) & 1u)) see &= 0xffff0000u;
               if (!((alive >> (2 * q + 1)) & 1u)) see &= 0x0000ffffu;
 #pragma unroll
@@ -304,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const Cach
             }
           };
           float top = -INFINITY;
-#pragma unroll
+#pragma unroll 1
           for (int q = 0; q < 4; ++q) {
             uint32_t x[32];
             tmem_ld32(s_tm + 32u * q, x);
@@ -319,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const Cach
             if (raise) m = top;
             l *= alpha;
             if (i > 0) {
-#pragma unroll
+#pragma unroll 1
               for (int q = 0; q < DP / 32; ++q) {
                 uint32_t x[32];
                 tmem_ld32(o_tm + 32u * q, x);
@@ -331,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const Cach
             }
           }
           const float mu = m == -INFINITY ? 0.f : m;
-#pragma unroll
+#pragma unroll 1
           for (int q = 0; q < 4; ++q) {
             uint32_t x[32];
             tmem_ld32(s_tm + 32u * q, x);
@@ -372,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const Cach
         const int at = 128 + row;
         mine[DP * 256 + at] = nat, mine[(DP + 1) * 256 + at] = l;
         if (steps > 0 && busy) {
-#pragma unroll
+#pragma unroll 1
           for (int q = 0; q < DP / 32; ++q) {
             uint32_t x[32];
             tmem_ld32(o_tm + 32u * q, x);
@@ -400,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const Cach
         const bool any_odd = c.seg_odd[seg & 1] == seg + 1;
         const float inv = none ? 0.f : 1.f / l;
         const int odd0 = max(g.k0 * kTileKeys, s.prefix / kTileKeys * kTileKeys), odd1 = min(s.len, g.k1 * kTileKeys);
-#pragma unroll
+#pragma unroll 1
         for (int q = 0; q < DP / 32; ++q) {
           uint32_t x[32];
 #pragma unroll
@@ -418,17 +400,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const Cach
             }
           }
           if (any_odd && tok >= 0) {
-#pragma unroll 1
-            for (int k = 0; k < 32; ++k) {
-              const int dd = 32 * q + (E4M3 ? (k & ~3) + ((k & 1) << 1 | ((k >> 1) & 1)) : k);
-              if (dd < a.d) {
-                const float bad = odd_sum<E4M3>(a, s, g.b, h, tok, dd, odd0, odd1);
-                if (bad != 0.f)
 #pragma unroll
-                  for (int e = 0; e < 32; ++e)
-                    if (e == k) x[e] = __float_as_uint(__uint_as_float(x[e]) + bad);
-              }
-            }
+            for (int k = 0; k < 32; ++k)
+              if (32 * q + k < a.d)
+                x[k] = __float_as_uint(__uint_as_float(x[k]) + odd_sum_of<E4M3>(a, s, g.b, h, tok, 32 * q + k, odd0, odd1));
           }
           if (whole) {
             if (have) {
@@ -437,10 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const Cach
               for (int k = 0; k < 32; k += 8) {
                 float y[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  const int src = E4M3 ? (e & ~3) + ((e & 1) << 1 | ((e >> 1) & 1)) : e;
-                  y[e] = none ? 0.f : __uint_as_float(x[k + src]) * inv;
-                }
+                for (int e = 0; e < 8; ++e) y[e] = none ? 0.f : __uint_as_float(x[k + e]) * inv;
                 if (32 * q + k < a.d)
                   o[k / 8] = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
                                         pack_bf16x2(y[6], y[7]));
@@ -472,22 +444,27 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const Cach
           a.LSE[qrow] = none ? -INFINITY : top + logf(sum);
           const float inv = none ? 0.f : 1.f / sum;
 #pragma unroll 1
-          for (int k = 0; k < a.d; k += 8) {
-            float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+          for (int k = 0; k < a.d; k += 16) {  // sixteen loads in flight
+            float y[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) y[e] = 0.f;
             if (!none)
+#pragma unroll 1
               for (int cc = c0; cc <= c1; ++cc) {
                 const float *part = a.part + (2ll * cc + (cc == c0)) * kSlot;
                 const float mc = __ldcg(part + DP * 256 + r);
+                float v[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) v[e] = __ldcg(part + (k + e) * 256 + r);
                 if (mc == -INFINITY) continue;
                 const float f = ex2_approx((mc - top) * kCacheLog2e) * inv;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  const int src = E4M3 ? (e & ~3) + ((e & 1) << 1 | ((e >> 1) & 1)) : e;
-                  y[e] = fmaf(__ldcg(part + (k + src) * 256 + r), f, y[e]);
-                }
+                for (int e = 0; e < 16; ++e) y[e] = fmaf(v[e], f, y[e]);
               }
-            *reinterpret_cast<uint4 *>(a.O + qrow * a.d + k) =
-                make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+            uint4 *o = reinterpret_cast<uint4 *>(a.O + qrow * a.d + k);
+            o[0] = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+            o[1] = make_uint4(pack_bf16x2(y[8], y[9]), pack_bf16x2(y[10], y[11]), pack_bf16x2(y[12], y[13]),
+                              pack_bf16x2(y[14], y[15]));
           }
         }
         named_bar_sync(1, 256);
@@ -501,9 +478,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const Cach
     auto convert = [&](const uint4 &raw, uint32_t scale, uint4 &x, uint4 &y) {
       x = raw;
       if constexpr (E4M3) {
-        const RowScale rs = row_scale(scale);
-        e4m3_to_bf16(raw.x, rs, x.x, x.y), e4m3_to_bf16(raw.y, rs, x.z, x.w);
-        e4m3_to_bf16(raw.z, rs, y.x, y.y), e4m3_to_bf16(raw.w, rs, y.z, y.w);
+        // 2^(byte - 127); byte 255 is NaN, byte 0 (2^-127, which cache_write does not make) counts as 0
+        const float f = __uint_as_float(scale == 255u ? 0x7fffffffu : scale << 23);
+        x.x = e4m3_to_bf16(raw.x, false, f), x.y = e4m3_to_bf16(raw.x, true, f);
+        x.z = e4m3_to_bf16(raw.y, false, f), x.w = e4m3_to_bf16(raw.y, true, f);
+        y.x = e4m3_to_bf16(raw.z, false, f), y.y = e4m3_to_bf16(raw.z, true, f);
+        y.z = e4m3_to_bf16(raw.w, false, f), y.w = e4m3_to_bf16(raw.w, true, f);
       }
     };
     auto store = [&](uint32_t dst, int row, int ch, const uint4 &x, const uint4 &y) {
@@ -705,13 +685,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const Cach
         if (p.split || n1 == 0 || t == 1) tc_commit_elect(&c.v_empty[slot]);
         if (final) tc_commit_elect(&c.o_final[t]);
       };
-      for (int i = 0; i < n0; ++i) {
-        score(0, i);
-        if (i > 0 && i - 1 < n1) product(1, i - 1, i - 1 == n1 - 1);
-        if (i < n1) score(1, i);
-        product(0, i, i == n0 - 1);
+      // S_0(0), S_1(0), PV_0(0), S_0(1), PV_1(0), S_1(1), PV_0(1), ...: one place in the code for each
+#pragma unroll 1
+      for (int half = 0; half <= 2 * n0; ++half) {
+        const int t = half & 1, i = half >> 1, pt = 1 - t, pi = t ? i : i - 1;
+        if (i < (t ? n1 : n0)) score(t, i);
+        const int pn = pt ? n1 : n0;
+        if (pi >= 0 && pi < pn) product(pt, pi, pi == pn - 1);
       }
-      if (n1 == n0 && n1 > 0) product(1, n1 - 1, true);
       done += n;
     }
     tc_commit_elect(&c.drain);
