@@ -67,10 +67,13 @@ struct Ctrl {
 __device__ __forceinline__ uint32_t tile_at(int row, int ch) {
   return uint32_t(ch >> 3) * (kTileKeys * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4);
 }
-__device__ __forceinline__ uint64_t desc_k(uint32_t base) { return make_smem_desc(base, 16, 1024, swizzle_code(128)); }
-__device__ __forceinline__ uint64_t desc_v(uint32_t base) {
-  return make_smem_desc(base, kTileKeys * 128, 1024, swizzle_code(128));
+// Matrix descriptors of a K-major tile and of V: only the start address in the low word is not a constant.
+__device__ __forceinline__ uint64_t desc(uint32_t start, uint32_t lbo) {
+  constexpr uint32_t high = (1024u >> 4) | (1u << 14) | (swizzle_code(128) << 29);
+  return (uint64_t(high) << 32) | ((lbo >> 4) << 16) | start;
 }
+__device__ __forceinline__ uint64_t desc_k(uint32_t start) { return desc(start, 16); }
+__device__ __forceinline__ uint64_t desc_v(uint32_t start) { return desc(start, kTileKeys * 128); }
 // Start-address offsets (16-byte units) of 16-column step kk of a K-major tile, and of 16-key step kk of V.
 __device__ __forceinline__ uint32_t step_k(int kk) { return uint32_t((kk >> 2) * (kTileKeys * 128) + (kk & 3) * 32) >> 4; }
 __device__ __forceinline__ uint32_t step_v(int kk) { return uint32_t(kk * 16 * 128) >> 4; }
@@ -105,23 +108,46 @@ __device__ __forceinline__ uint32_t e4m3_to_bf16(uint32_t w, bool hi, float scal
   return pack_bf16x2(f.x * scale, f.y * scale);
 }
 
+// Takes the non-finite values out of N words of bf16 pairs; whether there were any.
+template <int N>
+__device__ __forceinline__ bool clear_odd(uint32_t *w) {
+  bool odd = false;
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const uint32_t even = even_word<false>(w[k]);
+    odd |= even != w[k];
+    w[k] = even;
+  }
+  return odd;
+}
+
 __device__ __forceinline__ void sts16(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   st_shared_v4(at, a, b, c, d);
 }
 
-// The page rows of a 128-key tile as one loader thread sees them.
-struct TileRows {
-  const CacheAttnArgs &a;
-  const Seq &s;
-  int b, h, j0, jend;
-  __device__ __forceinline__ int page(int row) const {
-    const int j = j0 + row;
-    if (j >= jend) return -1;
-    const int p = __ldg(a.table + (long long)b * a.max_pages + (j >> a.page_shift));
-    return p >= 0 && p < a.num_pages ? p : -1;
+// The pages of a segment's 128-key tiles, for a loader warp: lane i (< 8) holds the page of 16-key group i, fetched
+// one tile ahead, so that no load of a row waits for its page number.
+struct Pages {
+  int now, next;
+  __device__ __forceinline__ int fetch(const CacheAttnArgs &a, int b, int j, int len, int lane) const {
+    j += 16 * lane;
+    return lane < 8 && j < len ? __ldg(a.table + (long long)b * a.max_pages + (j >> a.page_shift)) : 0;
   }
-  __device__ __forceinline__ long long pool_row(int page, int row) const {
-    return (((long long)page * a.H + h) << a.page_shift) + ((j0 + row) & ((1 << a.page_shift) - 1));
+  __device__ __forceinline__ void start(const CacheAttnArgs &a, int b, int j, int len, int lane) {
+    next = fetch(a, b, j, len, lane);
+  }
+  // Moves on to the tile at j; bit i of the result: group i has a page or lies behind the last key.
+  __device__ __forceinline__ unsigned step(const CacheAttnArgs &a, int b, int j, int len, int lane) {
+    now = next;
+    next = fetch(a, b, j + kTileKeys, len, lane);
+    const bool ok = now >= 0 && now < a.num_pages;
+    if (!ok) now = 0;
+    return __ballot_sync(0xffffffffu, ok) & 0xffu;
+  }
+  // Pool row of the tile's row `row`.
+  __device__ __forceinline__ long long pool_row(const CacheAttnArgs &a, int h, int j, int row) const {
+    const int page = __shfl_sync(0xffffffffu, now, row >> 4);
+    return (((long long)page * a.H + h) << a.page_shift) + ((j + row) & ((1 << a.page_shift) - 1));
   }
 };
 
@@ -179,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const __gr
     const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
     const uint32_t s_tm = tmem + lane_base + 128u * t, o_tm = tmem + lane_base + 256u + 128u * t;
     const float unit = BIAS == 1 ? kCacheLog2e : a.scale * kCacheLog2e;  // of the maximum, in log2
-    long long done = 0;    // key tiles of the segments before
+    unsigned done = 0;  // key tiles of the segments before
     uint32_t sphase = 0, ophase = 0;
     int seg = 0;
     constexpr int kSlot = 256 * (DP + 2);
@@ -251,8 +277,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const __gr
       for (int i = 0; i < steps; ++i) {
         const int idx = p.split ? 2 * i + t : i;
         const int j0 = (g.k0 + idx) * kTileKeys;
-        const long long tile = done + idx;
-        mbar_wait(&c.s_full[t], sphase & 1u, abort);
+        const unsigned tile = done + unsigned(idx);
+        mbar_wait_long(&c.s_full[t], sphase & 1u, abort);
         ++sphase;
         tc_fence_after();
         if (i > 0 && c.odd[(tile - (p.split ? 2 : 1)) & 7] == int(tile - (p.split ? 2 : 1)) + 1) odd = 1;
@@ -338,10 +364,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const __gr
       }
       // ---- the segment's end
       if (steps > 0) {
-        mbar_wait(&c.o_final[t], ophase & 1u, abort);
+        mbar_wait_long(&c.o_final[t], ophase & 1u, abort);
         ++ophase;
         tc_fence_after();
-        const long long tile = done + (p.split ? 2 * (steps - 1) + t : steps - 1);
+        const unsigned tile = done + unsigned(p.split ? 2 * (steps - 1) + t : steps - 1);
         if (c.odd[tile & 7] == int(tile) + 1) odd = 1;
       }
       done += n;
@@ -494,70 +520,84 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const __gr
         sts16(dst + tile_at(row, ch), x.x, x.y, x.z, x.w);
       }
     };
-    long long tile = 0;
+    const int rb = a.d * ES;  // bytes of a pool row
+    unsigned tile = 0;
+    Pages pages;
     if (warp < 12) {
       // K: loaded and converted before its slot is free, so that the tensor cores wait for the stores alone
       const int l = threadIdx.x & 127;
+      // chunk i of this thread: 16 bytes at ch of row row0 + i * (128 / CPR)
+      const int ch = l % CPR, row0 = l / CPR;
+      const bool inside = ch * 16 < rb;
+      const uint32_t at0 = tile_at(row0, E4M3 ? 2 * ch : ch), at1 = tile_at(row0, 2 * ch + 1);
       while (walk.next(a, g)) {
         const Seq &s = g.s;
         const int h = g.item / a.chunks, hk = a.fk_heads > 1 ? h : 0;
+        pages.start(a, g.b, g.k0 * kTileKeys, s.len, lane);
         for (int kt = g.k0; kt < g.k1; ++kt, ++tile) {
-          const TileRows rows{a, s, g.b, h, kt * kTileKeys, min(s.len, (kt + 1) * kTileKeys)};
-          const int slot = int(tile % p.ks);
+          const int j0 = kt * kTileKeys;
+          const unsigned alive = pages.step(a, g.b, j0, s.len, lane);
+          const int slot = p.ks == 2 ? int(tile & 1u) : 0;
           const uint32_t dst = base + p.k + slot * kTile;
-          // chunk i of this thread: 16 bytes at ch of row row0 + i * (128 / CPR)
-          const int ch = l % CPR, row0 = l / CPR;
           uint4 raw[CPR], more[E4M3 ? CPR : 1];
           uint32_t sc[E4M3 ? CPR : 1];
 #pragma unroll
-          for (int i = 0; i < CPR; ++i) {
-            const int row = row0 + i * (128 / CPR), page = rows.page(row);
-            raw[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (E4M3) sc[E4M3 ? i : 0] = 127u;
-            if (page >= 0) {
-              const long long pr = rows.pool_row(page, row);
-              if (ch * 16 < a.d * ES)
-                raw[i] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(a.kp) + pr * (a.d * ES) + ch * 16));
-              if (E4M3) sc[E4M3 ? i : 0] = __ldg(a.ks + pr);
-            }
-          }
-          unsigned alive = 0u;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int j = rows.j0 + 16 * i;
-            if (j >= rows.jend || rows.page(16 * i) >= 0) alive |= 1u << i;  // behind the last key is the masks' affair
+          for (int i = 0; i < CPR; ++i) {  // rows behind the last key read what lies there and are cleared below
+            const long long pr = pages.pool_row(a, h, j0, row0 + i * (128 / CPR));
+            raw[i] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(a.kp) + pr * rb + (inside ? ch * 16 : 0)));
+            if (E4M3) sc[E4M3 ? i : 0] = __ldg(a.ks + pr);
           }
           if (alive != 0xffu && l == 0) atomicOr(a.flags, kFlagRange);
+          // (4 hi, 4 lo) groups of the keys' factors, eight loads at a time, the first eight ahead like K
+          constexpr int kBatch = 8;
+          const int groups = a.RP / 4, total = kTileKeys * groups;
+          const bool plain = j0 + kTileKeys <= min(s.prefix, a.P);  // positions are j0, j0 + 1, ...
           auto position = [&](int row) {
-            const int j = rows.j0 + row;
-            if (j >= rows.jend) return 0;
+            const int j = j0 + row;
+            if (plain) return j;
+            if (j >= s.len) return 0;
             if (j >= s.prefix) return new_position(a, g.b, s, j - s.prefix);
             if (j < a.P) return j;
             atomicOr(a.flags, kFlagRange);
             return a.P - 1;
           };
-          // (4 hi, 4 lo) groups of the keys' factors, eight loads at a time, the first eight ahead like K
-          constexpr int kBatch = 8;
-          const int groups = a.RP / 4, total = kTileKeys * groups;
           const uint4 *fbase = static_cast<const uint4 *>(a.fk) + (BIAS == 2 ? (long long)hk * a.P * groups : 0ll);
           uint4 f[BIAS == 2 ? kBatch : 1];
           auto factors = [&](int at) {
+            if (plain) {
+              const uint4 *x = fbase + (long long)j0 * groups + at + l;
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-              const int e = at + i * 128 + l, row = e / groups;
-              if (e < total) f[BIAS == 2 ? i : 0] = __ldg(fbase + (long long)position(row) * groups + (e - row * groups));
+              for (int i = 0; i < kBatch; ++i)
+                if (at + i * 128 < total) f[BIAS == 2 ? i : 0] = __ldg(x + i * 128);
+            } else {
+#pragma unroll 1
+              for (int i = 0; i < kBatch; ++i) {
+                const int e = at + i * 128 + l, row = e / groups;
+                uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                if (e < total) v = __ldg(fbase + (long long)position(row) * groups + (e - row * groups));
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k)
+                  if (k == i) f[BIAS == 2 ? k : 0] = v;
+              }
             }
           };
           if constexpr (BIAS == 2) factors(0);
           if constexpr (BIAS == 1) f[0] = __ldg(static_cast<const uint4 *>(a.fk) + (long long)hk * a.P + position(l));
+          const int left = s.len - j0;  // keys from here on
 #pragma unroll
           for (int i = 0; i < CPR; ++i) {
-            const uint4 was = raw[i];
+            const int row = row0 + i * (128 / CPR);
+            uint4 was = raw[i];
+            if (!inside || row >= left || !((alive >> (row >> 4)) & 1u)) was = make_uint4(0u, 0u, 0u, 0u);
             convert(was, sc[E4M3 ? i : 0], raw[i], more[E4M3 ? i : 0]);
           }
-          if (tile >= p.ks) mbar_wait(&c.k_empty[slot], uint32_t(tile / p.ks - 1) & 1u, abort);
+          if (tile >= unsigned(p.ks)) mbar_wait_long(&c.k_empty[slot], (p.ks == 2 ? (tile >> 1) - 1 : tile - 1) & 1u, abort);
 #pragma unroll
-          for (int i = 0; i < CPR; ++i) store(dst, row0 + i * (128 / CPR), ch, raw[i], more[E4M3 ? i : 0]);
+          for (int i = 0; i < CPR; ++i) {
+            const uint32_t to = dst + i * (128 / CPR) * 128;  // whole groups of eight rows on: the swizzle is the same
+            sts16(to + at0, raw[i].x, raw[i].y, raw[i].z, raw[i].w);
+            if constexpr (E4M3) sts16(to + at1, more[i].x, more[i].y, more[i].z, more[i].w);
+          }
           if (l == 0) c.alive[tile & 3] = alive;
           if constexpr (BIAS == 1) {
             float(*pl)[kTileKeys] = planes[tile & 3];
@@ -566,16 +606,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const __gr
           }
           if constexpr (BIAS == 2) {
             const uint32_t ft = base + p.fk + slot * fk_tile;
+#pragma unroll 1
             for (int at = 0; at < total; at += kBatch * 128) {
               if (at > 0) factors(at);
 #pragma unroll
               for (int i = 0; i < kBatch; ++i) {
                 const int e = at + i * 128 + l, row = e / groups, q = e - row * groups;
-                if (e >= total) continue;
-                const uint32_t hi = ft + tile_at(row, q >> 1) + (q & 1) * 8;
-                const uint32_t lo = ft + tile_at(row, p.rpb / 8 + (q >> 1)) + (q & 1) * 8;
-                asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(hi), "r"(f[i].x), "r"(f[i].y) : "memory");
-                asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(lo), "r"(f[i].z), "r"(f[i].w) : "memory");
+                if (at + i * 128 >= total) break;
+                const uint32_t hi = tile_at(row, q >> 1) + (q & 1) * 8;
+                // the lo columns: four chunks on in the same 64 columns, or the blocks behind the hi ones
+                const uint32_t lo = p.rpb == 32 ? hi ^ 64u : hi + (p.rpb >> 6) * (kTileKeys * 128);
+                asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(ft + hi), "r"(f[i].x), "r"(f[i].y) : "memory");
+                asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(ft + lo), "r"(f[i].z), "r"(f[i].w) : "memory");
               }
             }
           }
@@ -585,48 +627,38 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const __gr
       }
     } else {
       const int l = threadIdx.x - 12 * 32;
-      constexpr int kMine = (128 * CPR + kVThreads - 1) / kVThreads;  // chunks of this thread
+      // chunk i of this thread: 16 bytes at ch of row row0 + i * kStep; the last ones of some threads do not exist
+      constexpr int kStep = kVThreads / CPR, kMine = (128 + kStep - 1) / kStep;
+      const int ch = l % CPR, row0 = l / CPR;
+      const bool inside = ch * 16 < rb;
       while (walk.next(a, g)) {
         const Seq &s = g.s;
         const int h = g.item / a.chunks;
+        pages.start(a, g.b, g.k0 * kTileKeys, s.len, lane);
         for (int kt = g.k0; kt < g.k1; ++kt, ++tile) {
-          const TileRows rows{a, s, g.b, h, kt * kTileKeys, min(s.len, (kt + 1) * kTileKeys)};
-          const bool tail = (kt + 1) * kTileKeys > s.prefix;
-          const int slot = int(tile % p.vs);
+          const int j0 = kt * kTileKeys, left = s.len - j0;
+          const bool tail = j0 + kTileKeys > s.prefix;
+          const unsigned alive = pages.step(a, g.b, j0, s.len, lane);
+          const int slot = p.vs == 2 ? int(tile & 1u) : 0;
           const uint32_t dst = base + p.v + slot * kTile;
           uint4 raw[kMine];
           uint32_t sc[E4M3 ? kMine : 1];
 #pragma unroll
           for (int i = 0; i < kMine; ++i) {
-            const int e = i * kVThreads + l, row = e / CPR, ch = e % CPR;
-            const int page = e < 128 * CPR ? rows.page(row) : -1;
-            raw[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (E4M3) sc[E4M3 ? i : 0] = 127u;
-            if (page >= 0) {
-              const long long pr = rows.pool_row(page, row);
-              if (ch * 16 < a.d * ES)
-                raw[i] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(a.vp) + pr * (a.d * ES) + ch * 16));
-              if (E4M3) sc[E4M3 ? i : 0] = __ldg(a.vs + pr);
-            }
+            const long long pr = pages.pool_row(a, h, j0, min(row0 + i * kStep, 127));
+            raw[i] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(a.vp) + pr * rb + (inside ? ch * 16 : 0)));
+            if (E4M3) sc[E4M3 ? i : 0] = __ldg(a.vs + pr);
           }
-          if (tile >= p.vs) mbar_wait(&c.v_empty[slot], uint32_t(tile / p.vs - 1) & 1u, abort);
+          if (tile >= unsigned(p.vs)) mbar_wait_long(&c.v_empty[slot], (p.vs == 2 ? (tile >> 1) - 1 : tile - 1) & 1u, abort);
           bool odd = false;
 #pragma unroll
           for (int i = 0; i < kMine; ++i) {
-            const int e = i * kVThreads + l;
-            if (e >= 128 * CPR) continue;
-            uint4 out[2];
-            convert(raw[i], sc[E4M3 ? i : 0], out[0], out[1]);
-            if (tail) {
-              uint32_t *w = reinterpret_cast<uint32_t *>(out);
-#pragma unroll
-              for (int k = 0; k < (E4M3 ? 8 : 4); ++k) {
-                const uint32_t even = even_word<false>(w[k]);
-                odd |= even != w[k];
-                w[k] = even;
-              }
-            }
-            store(dst, e / CPR, e % CPR, out[0], out[1]);
+            const int row = row0 + i * kStep;
+            uint4 was = raw[i], out[2];
+            if (!inside || row >= left || !((alive >> ((row >> 4) & 7)) & 1u)) was = make_uint4(0u, 0u, 0u, 0u);
+            convert(was, sc[E4M3 ? i : 0], out[0], out[1]);
+            if (tail) odd |= clear_odd<E4M3 ? 8 : 4>(reinterpret_cast<uint32_t *>(out));
+            if (row < 128) store(dst, row, ch, out[0], out[1]);
           }
           if (odd) c.odd[tile & 7] = int(tile) + 1;
           fence_proxy_async_smem();
@@ -640,48 +672,53 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const __gr
     constexpr uint32_t kF = make_idesc_f16(false, false, 128, 128, false);
     constexpr uint32_t kPV = make_idesc_f16(true, true, 128, DP, true);
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-    long long done = 0;
+    unsigned done = 0;
     uint32_t qphase = 0, pphase[2] = {0, 0};
     while (walk.next(a, g)) {
       const int n = g.k1 - g.k0, h = g.item / a.chunks;
       const int rows = min(p.tiles * 128, a.rows - (g.item - h * a.chunks) * p.tiles * 128);
       const int n0 = steps_of(0, n, rows), n1 = nstreams == 2 ? steps_of(1, n, rows) : 0;
-      mbar_wait(&c.q_full, qphase & 1u, abort);
+      mbar_wait_long(&c.q_full, qphase & 1u, abort);
       ++qphase;
+      // addresses are made the same for the warp by a shuffle, which lets them stay in uniform registers
+      auto uniform = [&](uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); };
       auto score = [&](int t, int i) {
-        const long long tile = done + (p.split ? 2 * i + t : i);
-        const int slot = int(tile % p.ks);
-        if (t == 0 || p.split) mbar_wait(&c.k_full[slot], uint32_t(tile / p.ks) & 1u, abort);
+        const unsigned tile = done + unsigned(p.split ? 2 * i + t : i);
+        const int slot = p.ks == 2 ? int(tile & 1u) : 0;
+        if (t == 0 || p.split) mbar_wait_long(&c.k_full[slot], (p.ks == 2 ? tile >> 1 : tile) & 1u, abort);
         tc_fence_after();
-        const uint32_t d = tm + 128u * t;
+        const uint32_t d = uniform(tm + 128u * t);
         const int rt = p.split ? 0 : t;
-        const uint64_t dq = desc_k(base + p.q + rt * kTile), dk = desc_k(base + p.k + slot * kTile);
+        const uint32_t q = uniform((base + p.q + rt * kTile) >> 4), k = uniform((base + p.k + slot * kTile) >> 4);
 #pragma unroll
-        for (int kk = 0; kk < DP / 16; ++kk) mma_ss_elect(d, dq + step_k(kk), dk + step_k(kk), kQK, kk > 0 ? 1u : 0u);
+        for (int kk = 0; kk < DP / 16; ++kk)
+          mma_ss_elect(d, desc_k(q + step_k(kk)), desc_k(k + step_k(kk)), kQK, kk > 0 ? 1u : 0u);
         if constexpr (BIAS == 2) {
-          const uint64_t df = desc_k(base + p.fq + rt * fq_tile), dg = desc_k(base + p.fk + slot * fk_tile);
+          const uint32_t fq = uniform((base + p.fq + rt * fq_tile) >> 4), fk = uniform((base + p.fk + slot * fk_tile) >> 4);
           const int low = p.rpb / 16;
+#pragma unroll 2
           for (int kk = 0; kk < a.RP / 16; ++kk) {
-            mma_ss_elect(d, df + step_k(kk), dg + step_k(kk), kF, 1u);
-            mma_ss_elect(d, df + step_k(low + kk), dg + step_k(kk), kF, 1u);
-            mma_ss_elect(d, df + step_k(kk), dg + step_k(low + kk), kF, 1u);
+            const uint32_t hi = uniform(step_k(kk)), lo = uniform(step_k(low + kk));
+            mma_ss_elect(d, desc_k(fq + hi), desc_k(fk + hi), kF, 1u);
+            mma_ss_elect(d, desc_k(fq + lo), desc_k(fk + hi), kF, 1u);
+            mma_ss_elect(d, desc_k(fq + hi), desc_k(fk + lo), kF, 1u);
           }
         }
         tc_commit_elect(&c.s_full[t]);
         if (p.split || n1 == 0 || t == 1) tc_commit_elect(&c.k_empty[slot]);
       };
       auto product = [&](int t, int i, bool final) {
-        const long long tile = done + (p.split ? 2 * i + t : i);
-        const int slot = int(tile % p.vs);
-        mbar_wait(&c.v_full[slot], uint32_t(tile / p.vs) & 1u, abort);
-        mbar_wait(&c.p_full[t], pphase[t] & 1u, abort);
+        const unsigned tile = done + unsigned(p.split ? 2 * i + t : i);
+        const int slot = p.vs == 2 ? int(tile & 1u) : 0;
+        mbar_wait_long(&c.v_full[slot], (p.vs == 2 ? tile >> 1 : tile) & 1u, abort);
+        mbar_wait_long(&c.p_full[t], pphase[t] & 1u, abort);
         ++pphase[t];
         tc_fence_after();
-        const uint32_t d = tm + 256u + 128u * t, pt = tm + 128u * t;
-        const uint64_t dv = desc_v(base + p.v + slot * kTile);
+        const uint32_t d = uniform(tm + 256u + 128u * t), pt = uniform(tm + 128u * t);
+        const uint32_t v = uniform((base + p.v + slot * kTile) >> 4), more = uniform(i > 0 ? 1u : 0u);
 #pragma unroll
         for (int kk = 0; kk < kTileKeys / 16; ++kk)
-          mma_ts_elect(d, pt + uint32_t(kk * 8), dv + step_v(kk), kPV, i > 0 || kk > 0 ? 1u : 0u);
+          mma_ts_elect(d, pt + uint32_t(kk * 8), desc_v(v + step_v(kk)), kPV, kk > 0 ? 1u : more);
         if (p.split || n1 == 0 || t == 1) tc_commit_elect(&c.v_empty[slot]);
         if (final) tc_commit_elect(&c.o_final[t]);
       };
