@@ -14,15 +14,7 @@ constexpr float kCacheLog2e = 1.4426950408889634f;
 // 2^e for an integer e, clamped to the normal range.
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float(uint32_t(min(max(e, -126), 127) + 127) << 23); }
 
-// Copy N words to shared memory, or zeros where !in (the address is then not read).
-template <int N>
-__device__ __forceinline__ void copy_words(uint32_t dst, const void *src, bool in) {
-  const int bytes = in ? 4 * N : 0;
-  if constexpr (N == 4)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(4 * N), "r"(bytes) : "memory");
-}
+// Asynchronous copy of N words (2 or 4) to shared memory.
 template <int N>
 __device__ __forceinline__ void copy_whole(uint32_t dst, const void *src) {
   if constexpr (N == 4)
@@ -30,7 +22,7 @@ __device__ __forceinline__ void copy_whole(uint32_t dst, const void *src) {
   else
     asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(4 * N) : "memory");
 }
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copies_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 struct Seq {
   int prefix, count, len;
 };

@@ -5,11 +5,11 @@
 //
 // A CTA (one per SM) holds one or two tiles of 128 query rows of an item and
 // walks over its run of 128-key tiles:
-//   warps 0-3, 4-7  softmax of stream 0 and 1: a thread per row (TMEM lane)
-//   warps 8-11      K loader: codes or bf16 from the pages to a swizzled bf16
+//   warp 0          MMA issuer: S = Q K^T (+ phi_q phi_k^T), O += P V
+//   warps 1-3       V loader
+//   warps 4-7       K loader: codes or bf16 from the pages to a swizzled bf16
 //                   tile, and the keys' bias factors
-//   warps 12-14     V loader
-//   warp 15         MMA issuer: S = Q K^T (+ phi_q phi_k^T), O += P V
+//   warps 8-11, 12-15  softmax of stream 0 and 1: a thread per row (TMEM lane)
 // Stream t is row tile t (both walk over the same keys), or, when an item has
 // 128 rows or fewer, every second key tile of the one row tile: the streams
 // then end with a maximum, sum and O each and are joined like two CTAs' parts.
@@ -38,14 +38,15 @@ namespace {
 
 constexpr int kThreads = 16 * 32;  // four warps a scheduler: 128 registers a thread
 constexpr int kVThreads = 96;
-constexpr int kIssuer = 15;
+constexpr int kIssuer = 0, kVWarp = 1, kKWarp = 4, kSoftmaxWarp = 8;
 constexpr int kTileKeys = 128;
 constexpr float kRaise = 8.f;  // log2 units: O is rescaled when the maximum grows by more
 
 struct TilePlan {
   int tiles;  // row tiles of an item's chunk: 1 or 2
   int split;  // one row tile, its key tiles dealt to two streams
-  int ks, vs; // K and V slots
+  int ks, vs;  // K and V slots
+  int fs;      // slots of the keys' factors
   int rpb;    // bias: columns reserved for the hi and for the lo parts (32, 64, 128), or 0
   uint32_t q, fq, k, fk, v, planes, ctrl;  // shared memory offsets from the 1024-byte aligned base
   uint32_t smem;
@@ -151,6 +152,13 @@ struct Pages {
   }
 };
 
+__device__ __noinline__ void wait_long(uint64_t *bar, uint32_t parity, volatile int *abort) {
+  mbar_wait_long(bar, parity, abort);
+}
+__device__ __forceinline__ void wait_for(uint64_t *bar, uint32_t parity, volatile int *abort) {
+  if (!mbar_try_wait(bar, parity)) wait_long(bar, parity, abort);
+}
+
 template <int DP, bool E4M3, int BIAS>
 __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const __grid_constant__ CacheAttnArgs a, const TilePlan p) {
   constexpr int ES = E4M3 ? 1 : 2;
@@ -199,9 +207,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const __gr
 
   if (blockIdx.x >= walk.ctas) {
     // no work: only the teardown below
-  } else if (warp < 8) {
+  } else if (warp >= kSoftmaxWarp) {
     // ------------------------------------------------------------- softmax
-    const int t = warp >> 2, row = threadIdx.x & 127;
+    const int t = (warp - kSoftmaxWarp) >> 2, row = threadIdx.x & 127;
     const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
     const uint32_t s_tm = tmem + lane_base + 128u * t, o_tm = tmem + lane_base + 256u + 128u * t;
     const float unit = BIAS == 1 ? kCacheLog2e : a.scale * kCacheLog2e;  // of the maximum, in log2
@@ -242,6 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const __gr
             const float inv = 1.f / a.scale;
             const uint4 *f = static_cast<const uint4 *>(a.fq) + ((long long)hq * a.P + pos) * (a.RP / 4);
             bool over = false;
+#pragma unroll 2
             for (int i = 0; i < a.RP / 8; ++i) {  // eight ranks: 16 bytes of hi, 16 of lo
               uint32_t hi[4] = {0u, 0u, 0u, 0u}, lo[4] = {0u, 0u, 0u, 0u};
               if (tok >= 0) {
@@ -278,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const __gr
         const int idx = p.split ? 2 * i + t : i;
         const int j0 = (g.k0 + idx) * kTileKeys;
         const unsigned tile = done + unsigned(idx);
-        mbar_wait_long(&c.s_full[t], sphase & 1u, abort);
+        wait_for(&c.s_full[t], sphase & 1u, abort);
         ++sphase;
         tc_fence_after();
         if (i > 0 && c.odd[(tile - (p.split ? 2 : 1)) & 7] == int(tile - (p.split ? 2 : 1)) + 1) odd = 1;
@@ -311,18 +320,47 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const __gr
                 if (!((see >> k) & 1u)) x[k] = 0xff800000u;
             }
           };
-          float top = -INFINITY;
-#pragma unroll 1
-          for (int q = 0; q < 4; ++q) {
-            uint32_t x[32];
-            tmem_ld32(s_tm + 32u * q, x);
-            tmem_ld_wait32(x);
-            finish(q, x);
+          // One pass over S with the maximum so far: P stays in registers until every row of the warp is known to keep
+          // within 2^8 of it. Else (the first tile of a segment, and a few after it) the maxima are raised, O is
+          // rescaled and the pass is repeated.
+          uint32_t w[4][16];
+          float sum = 0.f;
+          auto pass = [&]() {
+            const float mu = m == -INFINITY ? 0.f : m;
+            const float shift = -mu * unit;
+            const uint64_t unit2 = f2_pack(unit, unit), shift2 = f2_pack(shift, shift), mu2 = f2_pack(mu, mu);
+            uint64_t acc = 0;
+            float top = -INFINITY;
 #pragma unroll
-            for (int k = 0; k < 32; k += 2) top = fmax3(top, __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
-          }
-          const bool raise = (top - m) * unit > kRaise;  // the first finite score too: m is -inf
-          if (__any_sync(0xffffffffu, raise)) {
+            for (int q = 0; q < 4; ++q) {
+              uint32_t x[32];
+              tmem_ld32(s_tm + 32u * q, x);
+              tmem_ld_wait32(x);
+              finish(q, x);
+#pragma unroll
+              for (int k = 0; k < 32; k += 2) top = fmax3(top, __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
+#pragma unroll
+              for (int k = 0; k < 32; k += 2) {
+                const uint64_t x2 = f2_pack(__uint_as_float(x[k]), __uint_as_float(x[k + 1]));
+                // rank <= 4: the difference first, which holds at scores of the type's lowest value too
+                const uint64_t y2 = BIAS == 1 ? f2_fma(f2_sub(x2, mu2), unit2, 0) : f2_fma(x2, unit2, shift2);
+                float y0, y1;
+                f2_unpack(y2, y0, y1);
+                const float e0 = ex2_approx(y0), e1 = ex2_approx(y1);
+                acc = f2_add(acc, f2_pack(e0, e1));
+                w[q][k / 2] = pack_bf16x2(e0, e1);
+              }
+            }
+            float a0, a1;
+            f2_unpack(acc, a0, a1);
+            sum = a0 + a1;
+            return top;
+          };
+#pragma unroll 1
+          for (int again = 0; again < 2; ++again) {
+            const float top = pass();
+            const bool raise = (top - m) * unit > kRaise;  // the first finite score too: m is -inf
+            if (!__any_sync(0xffffffffu, raise)) break;
             const float alpha = raise ? ex2_approx((m - top) * unit) : 1.f;
             if (raise) m = top;
             l *= alpha;
@@ -338,25 +376,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const __gr
               }
             }
           }
-          const float mu = m == -INFINITY ? 0.f : m;
-#pragma unroll 1
-          for (int q = 0; q < 4; ++q) {
-            uint32_t x[32];
-            tmem_ld32(s_tm + 32u * q, x);
-            tmem_ld_wait32(x);
-            finish(q, x);
-            uint32_t w[16];
-            float sum0 = 0.f, sum1 = 0.f;
+          l += sum;
 #pragma unroll
-            for (int k = 0; k < 32; k += 2) {
-              const float e0 = ex2_approx((__uint_as_float(x[k]) - mu) * unit);
-              const float e1 = ex2_approx((__uint_as_float(x[k + 1]) - mu) * unit);
-              sum0 += e0, sum1 += e1;
-              w[k / 2] = pack_bf16x2(e0, e1);
-            }
-            l += sum0 + sum1;
-            tmem_st16(s_tm + 16u * q, w);
-          }
+          for (int q = 0; q < 4; ++q) tmem_st16(s_tm + 16u * q, w[q]);
           tmem_st_wait();
         }
         tc_fence_before();
@@ -364,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const __gr
       }
       // ---- the segment's end
       if (steps > 0) {
-        mbar_wait_long(&c.o_final[t], ophase & 1u, abort);
+        wait_for(&c.o_final[t], ophase & 1u, abort);
         ++ophase;
         tc_fence_after();
         const unsigned tile = done + unsigned(p.split ? 2 * (steps - 1) + t : steps - 1);
@@ -454,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const __gr
         const int c0 = walk.owner(g.start), c1 = walk.owner(g.start + g.blocks - 1);
         __threadfence();
         named_bar_sync(1, 256);
-        if (threadIdx.x == 0) c.last = atomicAdd(a.counters + c0, 1u) == unsigned(c1 - c0);
+        if (threadIdx.x == kSoftmaxWarp * 32) c.last = atomicAdd(a.counters + c0, 1u) == unsigned(c1 - c0);
         named_bar_sync(1, 256);
         if (c.last && t < p.tiles && have) {
           __threadfence();
@@ -470,35 +492,37 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const __gr
           a.LSE[qrow] = none ? -INFINITY : top + logf(sum);
           const float inv = none ? 0.f : 1.f / sum;
 #pragma unroll 1
-          for (int k = 0; k < a.d; k += 16) {  // sixteen loads in flight
-            float y[16];
+          for (int k = 0; k < a.d; k += 32) {  // 32 loads in flight; the columns past a head dim of 16 n exist in the slot
+            float y[32];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) y[e] = 0.f;
+            for (int e = 0; e < 32; ++e) y[e] = 0.f;
             if (!none)
 #pragma unroll 1
               for (int cc = c0; cc <= c1; ++cc) {
                 const float *part = a.part + (2ll * cc + (cc == c0)) * kSlot;
                 const float mc = __ldcg(part + DP * 256 + r);
-                float v[16];
+                float v[32];
 #pragma unroll
-                for (int e = 0; e < 16; ++e) v[e] = __ldcg(part + (k + e) * 256 + r);
+                for (int e = 0; e < 32; ++e) v[e] = __ldcg(part + (k + e) * 256 + r);
                 if (mc == -INFINITY) continue;
                 const float f = ex2_approx((mc - top) * kCacheLog2e) * inv;
 #pragma unroll
-                for (int e = 0; e < 16; ++e) y[e] = fmaf(v[e], f, y[e]);
+                for (int e = 0; e < 32; ++e) y[e] = fmaf(v[e], f, y[e]);
               }
             uint4 *o = reinterpret_cast<uint4 *>(a.O + qrow * a.d + k);
-            o[0] = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
-            o[1] = make_uint4(pack_bf16x2(y[8], y[9]), pack_bf16x2(y[10], y[11]), pack_bf16x2(y[12], y[13]),
-                              pack_bf16x2(y[14], y[15]));
+#pragma unroll
+            for (int e = 0; e < 32; e += 8)
+              if (k + e < a.d)
+                o[e / 8] = make_uint4(pack_bf16x2(y[e], y[e + 1]), pack_bf16x2(y[e + 2], y[e + 3]),
+                                      pack_bf16x2(y[e + 4], y[e + 5]), pack_bf16x2(y[e + 6], y[e + 7]));
           }
         }
         named_bar_sync(1, 256);
-        if (threadIdx.x == 0 && c.last) a.counters[c0] = 0u;  // for the next call
+        if (threadIdx.x == kSoftmaxWarp * 32 && c.last) a.counters[c0] = 0u;  // for the next call
       }
       if (p.split) named_bar_sync(1, 256);  // stream 1's part has been read
     }
-  } else if (warp < kIssuer) {
+  } else if (warp != kIssuer) {
     // ------------------------------------------------------------- loaders
     // A tile's chunk of 16 bytes of a pool row becomes one (bf16) or two (e4m3) of a tile's chunks.
     auto convert = [&](const uint4 &raw, uint32_t scale, uint4 &x, uint4 &y) {
@@ -523,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const __gr
     const int rb = a.d * ES;  // bytes of a pool row
     unsigned tile = 0;
     Pages pages;
-    if (warp < 12) {
+    if (warp >= kKWarp) {
       // K: loaded and converted before its slot is free, so that the tensor cores wait for the stores alone
       const int l = threadIdx.x & 127;
       // chunk i of this thread: 16 bytes at ch of row row0 + i * (128 / CPR)
@@ -539,6 +563,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const __gr
           const unsigned alive = pages.step(a, g.b, j0, s.len, lane);
           const int slot = p.ks == 2 ? int(tile & 1u) : 0;
           const uint32_t dst = base + p.k + slot * kTile;
+          auto wait_empty = [&]() {
+            if (tile >= unsigned(p.ks))
+              wait_for(&c.k_empty[slot], (p.ks == 2 ? (tile >> 1) - 1 : tile - 1) & 1u, abort);
+          };
+          const bool early = p.ks == 2 || p.fs == 1;
+          if (early) wait_empty();
           uint4 raw[CPR], more[E4M3 ? CPR : 1];
           uint32_t sc[E4M3 ? CPR : 1];
 #pragma unroll
@@ -548,9 +578,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const __gr
             if (E4M3) sc[E4M3 ? i : 0] = __ldg(a.ks + pr);
           }
           if (alive != 0xffu && l == 0) atomicOr(a.flags, kFlagRange);
-          // (4 hi, 4 lo) groups of the keys' factors, eight loads at a time, the first eight ahead like K
-          constexpr int kBatch = 8;
-          const int groups = a.RP / 4, total = kTileKeys * groups;
           const bool plain = j0 + kTileKeys <= min(s.prefix, a.P);  // positions are j0, j0 + 1, ...
           auto position = [&](int row) {
             const int j = j0 + row;
@@ -561,28 +588,34 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const __gr
             atomicOr(a.flags, kFlagRange);
             return a.P - 1;
           };
-          const uint4 *fbase = static_cast<const uint4 *>(a.fk) + (BIAS == 2 ? (long long)hk * a.P * groups : 0ll);
-          uint4 f[BIAS == 2 ? kBatch : 1];
-          auto factors = [&](int at) {
-            if (plain) {
-              const uint4 *x = fbase + (long long)j0 * groups + at + l;
-#pragma unroll
-              for (int i = 0; i < kBatch; ++i)
-                if (at + i * 128 < total) f[BIAS == 2 ? i : 0] = __ldg(x + i * 128);
+          uint4 f;
+          if constexpr (BIAS == 1) f = __ldg(static_cast<const uint4 *>(a.fk) + (long long)hk * a.P + position(l));
+          if constexpr (BIAS == 2) {
+            // The keys' factors, (4 hi, 4 lo) groups of 16 bytes, go to the hi and lo columns of one of two tiles by
+            // asynchronous copies of 8 bytes. Its last reader, tile - 2's S, is done: with two K slots the wait above
+            // was for it, with one the last turn's (a single slot's, tile - 1's S, was waited for above).
+            const uint32_t ft = base + p.fk + (p.fs == 2 ? tile & 1u : 0u) * fk_tile;
+            const int groups = a.RP / 4, total = kTileKeys * groups;
+            const uint4 *fbase = static_cast<const uint4 *>(a.fk) + (long long)hk * a.P * groups;
+            // lo columns: four chunks on in the same 64 columns, or in the blocks behind the hi ones
+            auto copy = [&](const uint4 *src, uint32_t hi) {
+              const uint32_t lo = p.rpb == 32 ? hi ^ 64u : hi + (p.rpb >> 6) * (kTileKeys * 128);
+              copy_whole<2>(ft + hi, src);
+              copy_whole<2>(ft + lo, reinterpret_cast<const uint2 *>(src) + 1);
+            };
+            if (plain && 128 % groups == 0) {  // 128 threads are whole rows: a step is 128 / groups rows on
+              const int row = l / groups, q = l % groups, rows = 128 / groups;
+              const uint4 *src = fbase + (long long)j0 * groups + l;
+#pragma unroll 4
+              for (int i = 0; i < groups; ++i) copy(src + i * 128, tile_at(row + i * rows, q >> 1) + (q & 1) * 8);
             } else {
 #pragma unroll 1
-              for (int i = 0; i < kBatch; ++i) {
-                const int e = at + i * 128 + l, row = e / groups;
-                uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                if (e < total) v = __ldg(fbase + (long long)position(row) * groups + (e - row * groups));
-#pragma unroll
-                for (int k = 0; k < kBatch; ++k)
-                  if (k == i) f[BIAS == 2 ? k : 0] = v;
+              for (int e = l; e < total; e += 128) {
+                const int row = e / groups, q = e - row * groups;
+                copy(fbase + (long long)position(row) * groups + q, tile_at(row, q >> 1) + (q & 1) * 8);
               }
             }
-          };
-          if constexpr (BIAS == 2) factors(0);
-          if constexpr (BIAS == 1) f[0] = __ldg(static_cast<const uint4 *>(a.fk) + (long long)hk * a.P + position(l));
+          }
           const int left = s.len - j0;  // keys from here on
 #pragma unroll
           for (int i = 0; i < CPR; ++i) {
@@ -591,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const __gr
             if (!inside || row >= left || !((alive >> (row >> 4)) & 1u)) was = make_uint4(0u, 0u, 0u, 0u);
             convert(was, sc[E4M3 ? i : 0], raw[i], more[E4M3 ? i : 0]);
           }
-          if (tile >= unsigned(p.ks)) mbar_wait_long(&c.k_empty[slot], (p.ks == 2 ? (tile >> 1) - 1 : tile - 1) & 1u, abort);
+          if (!early) wait_empty();
 #pragma unroll
           for (int i = 0; i < CPR; ++i) {
             const uint32_t to = dst + i * (128 / CPR) * 128;  // whole groups of eight rows on: the swizzle is the same
@@ -601,34 +634,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const __gr
           if (l == 0) c.alive[tile & 3] = alive;
           if constexpr (BIAS == 1) {
             float(*pl)[kTileKeys] = planes[tile & 3];
-            pl[0][l] = __uint_as_float(f[0].x), pl[1][l] = __uint_as_float(f[0].y);
-            pl[2][l] = __uint_as_float(f[0].z), pl[3][l] = __uint_as_float(f[0].w);
+            pl[0][l] = __uint_as_float(f.x), pl[1][l] = __uint_as_float(f.y);
+            pl[2][l] = __uint_as_float(f.z), pl[3][l] = __uint_as_float(f.w);
           }
-          if constexpr (BIAS == 2) {
-            const uint32_t ft = base + p.fk + slot * fk_tile;
-#pragma unroll 1
-            for (int at = 0; at < total; at += kBatch * 128) {
-              if (at > 0) factors(at);
-#pragma unroll
-              for (int i = 0; i < kBatch; ++i) {
-                const int e = at + i * 128 + l, row = e / groups, q = e - row * groups;
-                if (at + i * 128 >= total) break;
-                const uint32_t hi = tile_at(row, q >> 1) + (q & 1) * 8;
-                // the lo columns: four chunks on in the same 64 columns, or the blocks behind the hi ones
-                const uint32_t lo = p.rpb == 32 ? hi ^ 64u : hi + (p.rpb >> 6) * (kTileKeys * 128);
-                asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(ft + hi), "r"(f[i].x), "r"(f[i].y) : "memory");
-                asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(ft + lo), "r"(f[i].z), "r"(f[i].w) : "memory");
-              }
-            }
-          }
+          if constexpr (BIAS == 2) copies_wait_all();
           fence_proxy_async_smem();
           mbar_arrive(&c.k_full[slot]);
         }
       }
     } else {
-      const int l = threadIdx.x - 12 * 32;
+      const int l = threadIdx.x - kVWarp * 32;
       // chunk i of this thread: 16 bytes at ch of row row0 + i * kStep; the last ones of some threads do not exist
       constexpr int kStep = kVThreads / CPR, kMine = (128 + kStep - 1) / kStep;
+      constexpr int kPart = CPR == 16 ? 6 : (CPR == 8 ? 4 : 3), kParts = (kMine + kPart - 1) / kPart;
       const int ch = l % CPR, row0 = l / CPR;
       const bool inside = ch * 16 < rb;
       while (walk.next(a, g)) {
@@ -641,24 +659,37 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const __gr
           const unsigned alive = pages.step(a, g.b, j0, s.len, lane);
           const int slot = p.vs == 2 ? int(tile & 1u) : 0;
           const uint32_t dst = base + p.v + slot * kTile;
-          uint4 raw[kMine];
-          uint32_t sc[E4M3 ? kMine : 1];
+          // three or four chunks at a time, the next ones' loads under way meanwhile
+          uint4 raw[2][kPart];
+          uint32_t sc[2][E4M3 ? kPart : 1];
+          auto load = [&](int part, uint4 *x, uint32_t *scale) {
 #pragma unroll
-          for (int i = 0; i < kMine; ++i) {
-            const long long pr = pages.pool_row(a, h, j0, min(row0 + i * kStep, 127));
-            raw[i] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(a.vp) + pr * rb + (inside ? ch * 16 : 0)));
-            if (E4M3) sc[E4M3 ? i : 0] = __ldg(a.vs + pr);
-          }
-          if (tile >= unsigned(p.vs)) mbar_wait_long(&c.v_empty[slot], (p.vs == 2 ? (tile >> 1) - 1 : tile - 1) & 1u, abort);
+            for (int i = 0; i < kPart; ++i) {
+              const long long pr = pages.pool_row(a, h, j0, min(row0 + (part * kPart + i) * kStep, 127));
+              x[i] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(a.vp) + pr * rb + (inside ? ch * 16 : 0)));
+              if (E4M3) scale[E4M3 ? i : 0] = __ldg(a.vs + pr);
+            }
+          };
+          load(0, raw[0], sc[0]);
+          if (tile >= unsigned(p.vs)) wait_for(&c.v_empty[slot], (p.vs == 2 ? (tile >> 1) - 1 : tile - 1) & 1u, abort);
           bool odd = false;
+#pragma unroll 1
+          for (int part = 0; part < kParts; ++part) {
+            load(min(part + 1, kParts - 1), raw[1], sc[1]);
 #pragma unroll
-          for (int i = 0; i < kMine; ++i) {
-            const int row = row0 + i * kStep;
-            uint4 was = raw[i], out[2];
-            if (!inside || row >= left || !((alive >> ((row >> 4) & 7)) & 1u)) was = make_uint4(0u, 0u, 0u, 0u);
-            convert(was, sc[E4M3 ? i : 0], out[0], out[1]);
-            if (tail) odd |= clear_odd<E4M3 ? 8 : 4>(reinterpret_cast<uint32_t *>(out));
-            if (row < 128) store(dst, row, ch, out[0], out[1]);
+            for (int i = 0; i < kPart; ++i) {
+              const int row = row0 + (part * kPart + i) * kStep;
+              uint4 was = raw[0][i], out[2];
+              if (!inside || row >= left || !((alive >> ((row >> 4) & 7)) & 1u)) was = make_uint4(0u, 0u, 0u, 0u);
+              convert(was, sc[0][E4M3 ? i : 0], out[0], out[1]);
+              if (tail) odd |= clear_odd<E4M3 ? 8 : 4>(reinterpret_cast<uint32_t *>(out));
+              if (row < 128) store(dst, row, ch, out[0], out[1]);
+            }
+#pragma unroll
+            for (int i = 0; i < kPart; ++i) {
+              raw[0][i] = raw[1][i];
+              if (E4M3) sc[0][E4M3 ? i : 0] = sc[1][E4M3 ? i : 0];
+            }
           }
           if (odd) c.odd[tile & 7] = int(tile) + 1;
           fence_proxy_async_smem();
@@ -668,59 +699,58 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const __gr
     }
   } else {
     // ---------------------------------------------------------- MMA issuer
+    // One lane issues: its instructions need no election and no predicates.
     constexpr uint32_t kQK = make_idesc_f16(true, true, 128, 128, false);
     constexpr uint32_t kF = make_idesc_f16(false, false, 128, 128, false);
     constexpr uint32_t kPV = make_idesc_f16(true, true, 128, DP, true);
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     unsigned done = 0;
     uint32_t qphase = 0, pphase[2] = {0, 0};
-    while (walk.next(a, g)) {
+    while (lane == 0 && walk.next(a, g)) {
       const int n = g.k1 - g.k0, h = g.item / a.chunks;
       const int rows = min(p.tiles * 128, a.rows - (g.item - h * a.chunks) * p.tiles * 128);
       const int n0 = steps_of(0, n, rows), n1 = nstreams == 2 ? steps_of(1, n, rows) : 0;
-      mbar_wait_long(&c.q_full, qphase & 1u, abort);
+      wait_for(&c.q_full, qphase & 1u, abort);
       ++qphase;
-      // addresses are made the same for the warp by a shuffle, which lets them stay in uniform registers
-      auto uniform = [&](uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); };
       auto score = [&](int t, int i) {
         const unsigned tile = done + unsigned(p.split ? 2 * i + t : i);
         const int slot = p.ks == 2 ? int(tile & 1u) : 0;
-        if (t == 0 || p.split) mbar_wait_long(&c.k_full[slot], (p.ks == 2 ? tile >> 1 : tile) & 1u, abort);
+        if (t == 0 || p.split) wait_for(&c.k_full[slot], (p.ks == 2 ? tile >> 1 : tile) & 1u, abort);
         tc_fence_after();
-        const uint32_t d = uniform(tm + 128u * t);
+        const uint32_t d = (tm + 128u * t);
         const int rt = p.split ? 0 : t;
-        const uint32_t q = uniform((base + p.q + rt * kTile) >> 4), k = uniform((base + p.k + slot * kTile) >> 4);
-#pragma unroll
+        const uint32_t q = (base + p.q + rt * kTile) >> 4, k = (base + p.k + slot * kTile) >> 4;
+#pragma unroll 1
         for (int kk = 0; kk < DP / 16; ++kk)
-          mma_ss_elect(d, desc_k(q + step_k(kk)), desc_k(k + step_k(kk)), kQK, kk > 0 ? 1u : 0u);
+          mma_ss_one(d, desc_k(q + step_k(kk)), desc_k(k + step_k(kk)), kQK, kk > 0 ? 1u : 0u);
         if constexpr (BIAS == 2) {
-          const uint32_t fq = uniform((base + p.fq + rt * fq_tile) >> 4), fk = uniform((base + p.fk + slot * fk_tile) >> 4);
+          const uint32_t fq = (base + p.fq + rt * fq_tile) >> 4, fk = (base + p.fk + (p.fs == 2 ? tile & 1u : 0u) * fk_tile) >> 4;
           const int low = p.rpb / 16;
-#pragma unroll 2
+#pragma unroll 1
           for (int kk = 0; kk < a.RP / 16; ++kk) {
-            const uint32_t hi = uniform(step_k(kk)), lo = uniform(step_k(low + kk));
-            mma_ss_elect(d, desc_k(fq + hi), desc_k(fk + hi), kF, 1u);
-            mma_ss_elect(d, desc_k(fq + lo), desc_k(fk + hi), kF, 1u);
-            mma_ss_elect(d, desc_k(fq + hi), desc_k(fk + lo), kF, 1u);
+            const uint32_t hi = (step_k(kk)), lo = (step_k(low + kk));
+            mma_ss_one(d, desc_k(fq + hi), desc_k(fk + hi), kF, 1u);
+            mma_ss_one(d, desc_k(fq + lo), desc_k(fk + hi), kF, 1u);
+            mma_ss_one(d, desc_k(fq + hi), desc_k(fk + lo), kF, 1u);
           }
         }
-        tc_commit_elect(&c.s_full[t]);
-        if (p.split || n1 == 0 || t == 1) tc_commit_elect(&c.k_empty[slot]);
+        tc_commit(&c.s_full[t]);
+        if (p.split || n1 == 0 || t == 1) tc_commit(&c.k_empty[slot]);
       };
       auto product = [&](int t, int i, bool final) {
         const unsigned tile = done + unsigned(p.split ? 2 * i + t : i);
         const int slot = p.vs == 2 ? int(tile & 1u) : 0;
-        mbar_wait_long(&c.v_full[slot], (p.vs == 2 ? tile >> 1 : tile) & 1u, abort);
-        mbar_wait_long(&c.p_full[t], pphase[t] & 1u, abort);
+        wait_for(&c.v_full[slot], (p.vs == 2 ? tile >> 1 : tile) & 1u, abort);
+        wait_for(&c.p_full[t], pphase[t] & 1u, abort);
         ++pphase[t];
         tc_fence_after();
-        const uint32_t d = uniform(tm + 256u + 128u * t), pt = uniform(tm + 128u * t);
-        const uint32_t v = uniform((base + p.v + slot * kTile) >> 4), more = uniform(i > 0 ? 1u : 0u);
-#pragma unroll
+        const uint32_t d = (tm + 256u + 128u * t), pt = (tm + 128u * t);
+        const uint32_t v = ((base + p.v + slot * kTile) >> 4), more = (i > 0 ? 1u : 0u);
+#pragma unroll 1
         for (int kk = 0; kk < kTileKeys / 16; ++kk)
-          mma_ts_elect(d, pt + uint32_t(kk * 8), desc_v(v + step_v(kk)), kPV, kk > 0 ? 1u : more);
-        if (p.split || n1 == 0 || t == 1) tc_commit_elect(&c.v_empty[slot]);
-        if (final) tc_commit_elect(&c.o_final[t]);
+          mma_ts_one(d, pt + uint32_t(kk * 8), desc_v(v + step_v(kk)), kPV, kk > 0 ? 1u : more);
+        if (p.split || n1 == 0 || t == 1) tc_commit(&c.v_empty[slot]);
+        if (final) tc_commit(&c.o_final[t]);
       };
       // S_0(0), S_1(0), PV_0(0), S_0(1), PV_1(0), S_1(1), PV_0(1), ...: one place in the code for each
 #pragma unroll 1
@@ -732,8 +762,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const __gr
       }
       done += n;
     }
-    tc_commit_elect(&c.drain);
-    if (!mbar_wait_for(&c.drain, 0, 1000000000ull)) c.abort = 1;
+    if (lane == 0) {
+      tc_commit(&c.drain);
+      if (!mbar_wait_for(&c.drain, 0, 1000000000ull)) c.abort = 1;
+    }
   }
   __syncwarp();
   tc_fence_before();
@@ -752,11 +784,12 @@ TilePlan make_plan(int d, int R, int rows) {
   const int RP = (R + 15) / 16 * 16;
   const uint32_t tile = kTileKeys * DP * 2;
   TilePlan best{};
-  // One or two row tiles, then K and V slots. One K slot costs less than one V slot: K is stored ready-made.
-  static const int kOptions[6][3] = {{2, 2, 2}, {2, 1, 2}, {2, 1, 1}, {1, 2, 2}, {1, 1, 2}, {1, 1, 1}};
+  // One or two row tiles, then K, V and factor slots. One K slot costs less than one V slot: K is stored ready-made.
+  static const int kOptions[8][4] = {{2, 2, 2, 2}, {2, 1, 2, 2}, {2, 1, 1, 2}, {2, 1, 1, 1},
+                                     {1, 2, 2, 2}, {1, 1, 2, 2}, {1, 1, 2, 1}, {1, 1, 1, 1}};
   for (const auto &o : kOptions) {
     TilePlan p{};
-    p.tiles = o[0], p.ks = o[1], p.vs = o[2];
+    p.tiles = o[0], p.ks = o[1], p.vs = o[2], p.fs = o[3];
     if (p.tiles == 2 && rows <= 128) continue;
     p.rpb = R <= kCacheBiasExact ? 0 : (RP <= 32 ? 32 : (RP <= 64 ? 64 : 128));
     const uint32_t f = kTileKeys * 4 * p.rpb;
@@ -764,7 +797,7 @@ TilePlan make_plan(int d, int R, int rows) {
     p.fq = p.q + p.tiles * tile;
     p.k = p.fq + p.tiles * f;
     p.fk = p.k + p.ks * tile;
-    p.v = p.fk + p.ks * f;
+    p.v = p.fk + p.fs * f;
     p.planes = p.v + p.vs * tile;
     p.ctrl = p.planes + (R > 0 && R <= kCacheBiasExact ? 4 * 4 * kTileKeys * 4 : 0);
     p.smem = p.ctrl + uint32_t(sizeof(Ctrl)) + 1024;
