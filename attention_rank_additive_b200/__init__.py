@@ -16,6 +16,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 
 __all__ = [
     "FB_OK", "FB_ERR_INVALID_ARG", "FB_ERR_UNSUPPORTED", "FB_ERR_RANGE", "FB_ERR_WORKSPACE", "FB_ERR_CUDA",
@@ -29,8 +30,8 @@ __all__ = [
     "PreparedBias", "attn_dense_bias", "factors_sandwich", "factors_alibi", "svd_factors",
     "attn_flops", "FB_E4M3", "fb_rope_fwd", "fb_rope_bwd", "fb_rope_turns_host", "fb_rope_frequencies_host",
     "fb_cache_write", "fb_cache_read", "fb_cache_bias_bytes", "fb_cache_bias_prepare",
-    "fb_attn_cache_workspace_bytes", "fb_attn_cache_fwd", "Rope", "rope", "rope_bwd", "PagedCache", "cache_write",
-    "cache_read", "CacheBias", "cache_workspace", "attn_cache",
+    "fb_attn_cache_workspace_bytes", "fb_attn_cache_fwd", "fb_call", "Rope", "rope", "rope_bwd", "PagedCache",
+    "cache_write", "cache_read", "CacheBias", "cache_workspace", "attn_cache",
 ]
 
 FB_OK, FB_ERR_INVALID_ARG, FB_ERR_UNSUPPORTED, FB_ERR_RANGE, FB_ERR_WORKSPACE, FB_ERR_CUDA, FB_ERR_TIMEOUT = range(7)
@@ -48,7 +49,7 @@ EXPORTED = (
     "fb_svd_factors_device", "fb_attn_neural_workspace_bytes", "fb_attn_neural_fwd", "fb_attn_bwd_workspace_bytes",
     "fb_attn_bwd", "fb_attn_neural_bwd_workspace_bytes", "fb_attn_neural_bwd", "fb_rope_fwd", "fb_rope_bwd",
     "fb_rope_turns_host", "fb_rope_frequencies_host", "fb_cache_write", "fb_cache_read", "fb_cache_bias_bytes",
-    "fb_cache_bias_prepare", "fb_attn_cache_workspace_bytes", "fb_attn_cache_fwd",
+    "fb_cache_bias_prepare", "fb_attn_cache_workspace_bytes", "fb_attn_cache_fwd", "fb_call",
 )
 
 
@@ -135,6 +136,7 @@ def lib() -> ctypes.CDLL:
         L.fb_attn_cache_fwd.argtypes = [i32, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, i32, i32, vp, i32, vp, vp, vp,
                                         i32, vp, i32, i32, i32, i32, vp, f32, vp, vp, vp, sz, vp]
         L.fb_attn_cache_fwd.restype = i32
+        L.fb_call.argtypes, L.fb_call.restype = [i32, ctypes.c_char_p, i32], i32
         L.fb_check_device_error.argtypes, L.fb_check_device_error.restype = [vp], i32
         L.fb_selftest_wait_timeout.argtypes, L.fb_selftest_wait_timeout.restype = [i32, vp], i32
         _lib = L
@@ -421,6 +423,11 @@ def fb_attn_cache_fwd(cache_dt, B, Hq, H, T, d, Q, k_pages, v_pages, k_scale, v_
                                    workspace_bytes, stream)
 
 
+def fb_call(entry, words, count) -> int:
+    """words: the arguments packed by the struct module, 8 bytes each (a bytes object)."""
+    return lib().fb_call(entry, words, count)
+
+
 def fb_check_device_error(stream) -> int:
     return lib().fb_check_device_error(stream)
 
@@ -625,43 +632,48 @@ def attn_flops(B: int, H: int, N: int, d: int, R: int, causal: bool) -> float:
 
 # ------------------------------------------------- serving: rotary positions, paged cache, attention over it
 
-class _On:
-    """The tensors' device as the current one while a call launches."""
+class _Entry:
+    """One entry of fb_call. Called with the device and the arguments but the stream, which is the device's current one;
+    the device is made the current one for the call where it is not."""
 
-    __slots__ = ("old", "new")
+    def __init__(self, entry: int, where: str, words: str):
+        self.entry, self.where, self.count = entry, where, len(words) + 1
+        self.pack = struct.Struct("=" + words + "q").pack
 
-    def __init__(self, new: int, old: int):
-        self.new, self.old = new, old
-
-    def __enter__(self):
+    def __call__(self, index: int, *args):
         import torch
-        torch.cuda.set_device(self.new)
+        words = self.pack(*args, torch._C._cuda_getCurrentRawStream(index))
+        L = _lib or lib()
+        now = torch.cuda.current_device()
+        if now == index:
+            status = L.fb_call(self.entry, words, self.count)
+        else:
+            with torch.cuda.device(index):
+                status = L.fb_call(self.entry, words, self.count)
+        if status != FB_OK:
+            raise FlashBiasError(status, self.where)
 
-    def __exit__(self, *exc):
-        import torch
-        torch.cuda.set_device(self.old)
+
+_rope_fwd = _Entry(0, "fb_rope_fwd", 7 * "q" + "d" + 20 * "q")
+_rope_bwd = _Entry(1, "fb_rope_bwd", 7 * "q" + "d" + 20 * "q")
+_cache_write = _Entry(2, "fb_cache_write", 24 * "q")
+_cache_read = _Entry(3, "fb_cache_read", 18 * "q")
+_attn_cache = _Entry(4, "fb_attn_cache_fwd", 25 * "q" + "d" + 4 * "q")
 
 
-def _launch(call, where: str, index: int, *args):
-    """call(*args, the current stream of device `index`), with that device current."""
+def _code(dtype):
+    """FB_BF16, FB_F32, or None."""
     import torch
-    now = torch.cuda.current_device()
-    if now == index:
-        status = call(*args, torch._C._cuda_getCurrentRawStream(index))
-    else:
-        with _On(index, now):
-            status = call(*args, torch._C._cuda_getCurrentRawStream(index))
-    if status != FB_OK:
-        raise FlashBiasError(status, where)
+    return FB_BF16 if dtype is torch.bfloat16 else (FB_F32 if dtype is torch.float32 else None)
 
 
-def _ints(t, shape, device, what: str) -> int:
-    """Pointer of a contiguous int32 tensor of this shape on this device (0 for None)."""
+def _ints(t, shape, index: int, what: str) -> int:
+    """Pointer of a contiguous int32 tensor of this shape on CUDA device `index` (0 for None)."""
     import torch
     if t is None:
         return 0
-    if t.dtype != torch.int32 or t.shape != shape or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{what}: a contiguous int32 tensor {tuple(shape)} on {device}")
+    if t.dtype is not torch.int32 or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{what}: a contiguous int32 tensor {tuple(shape)} on cuda:{index}")
     return t.data_ptr()
 
 
@@ -689,6 +701,7 @@ class Rope:
         # 2^-64 turns as two's complement: torch's uint64 has few operations
         signed = [t - (1 << 64) if t >> 63 else t for t in turns]
         self.turns = torch.tensor(signed, dtype=torch.int64, device=device)
+        self.index, self.pointer = self.turns.get_device(), self.turns.data_ptr()
 
     @classmethod
     def scaled(cls, rot: int, base=10000.0, scaling="none", by=1.0, trained=4096.0, fast=32.0, slow=1.0,
@@ -702,40 +715,55 @@ class Rope:
         return cls(freq, interleaved, out.value if factor is None else factor, device)
 
 
-def _rope(call, where, q, k, rope, positions, out):
+def _side(x, what: str):
+    """Heads, pointer and strides of a [B, H, N, d] tensor with d contiguous."""
+    if x.dim() != 4:
+        raise ValueError(f"{what}: a tensor [B, H, N, d]")
+    sb, sh, sn, sd = x.stride()
+    if sd != 1 and x.shape[3] > 1:
+        raise ValueError(f"{what}: the last dimension contiguous")
+    return x.data_ptr(), sb, sh, sn
+
+
+def _rope(call, q, k, rope, positions, out):
     import torch
-    if not (q.dim() == 4 and q.is_cuda and q.stride(3) == 1):
-        raise ValueError(f"{where}: q a CUDA tensor [B, H, N, d], d contiguous")
     B, Hq, N, d = q.shape
-    dev, dt = q.device, _dtype_code(q)
-    if not (rope.turns.device == dev):
-        raise ValueError(f"{where}: the Rope is on another device")
-    qo, ko = out if out is not None else (torch.empty_like(q), None if k is None else torch.empty_like(k))
-    if not (qo.shape == q.shape and qo.dtype == q.dtype and qo.device == dev and qo.stride(3) == 1):
-        raise ValueError(f"{where}: out like q")
-    if k is None:
-        side_k = (0, 0, 0, 0, 0, 0, 0, 0, 0)
+    index, dt = q.get_device(), _code(q.dtype)
+    if dt is None or index < 0:
+        raise ValueError(f"{call.where}: q a bfloat16 or float32 CUDA tensor [B, H, N, d]")
+    if rope.index != index:
+        raise ValueError(f"{call.where}: the Rope is on another device")
+    if out is None:
+        qo, ko = torch.empty_like(q), None if k is None else torch.empty_like(k)
     else:
-        if not (k.dim() == 4 and k.shape[0] == B and k.shape[2:] == q.shape[2:]
-                and k.dtype == q.dtype and k.device == dev and k.stride(3) == 1):
-            raise ValueError(f"{where}: k [B, Hk, N, d] like q")
-        if not (ko.shape == k.shape and ko.dtype == k.dtype and ko.device == dev and ko.stride(3) == 1):
-            raise ValueError(f"{where}: out like k")
-        side_k = (k.shape[1], k.data_ptr(), *k.stride()[:3], ko.data_ptr(), *ko.stride()[:3])
-    if out is not None:
-        for t in out:
-            if not (t is None or all(s > 0 or n <= 1 for s, n in zip(t.stride(), t.shape))):
-                raise ValueError(f"{where}: out with places of its own for every value")
-    pos, pos_bs = 0, 0
+        qo, ko = out
+        for x, y in ((q, qo), (k, ko)):
+            if (x is None) != (y is None) or x is not None and not (
+                    y.shape == x.shape and y.dtype is x.dtype and y.get_device() == index
+                    and all(s > 0 or n <= 1 for s, n in zip(y.stride(), y.shape))):
+                raise ValueError(f"{call.where}: out like q and k, with a place of its own for every value")
+    qp, qb, qh, qn = _side(q, "q")
+    op, ob, oh, on = _side(qo, "q's output")
+    if k is None:
+        Hk = kp = kb = kh = kn = rp = rb = rh = rn = 0
+    else:
+        Bk, Hk, Nk, dk = k.shape
+        if Bk != B or Nk != N or dk != d or k.dtype is not q.dtype or k.get_device() != index:
+            raise ValueError(f"{call.where}: k [B, Hk, N, d] like q")
+        kp, kb, kh, kn = _side(k, "k")
+        rp, rb, rh, rn = _side(ko, "k's output")
+    pos = pos_bs = 0
     if positions is not None:
-        if not (positions.dtype == torch.int32 and positions.device == dev and positions.shape[-1] == N
+        shape = positions.shape
+        if not (positions.dtype is torch.int32 and positions.get_device() == index and shape[-1] == N
                 and (N == 1 or positions.stride(-1) == 1)
-                and (positions.dim() == 1 or (positions.dim() == 2 and positions.shape[0] in (1, B)))):
-            raise ValueError(f"{where}: positions int32 [N], [1, N] or [B, N] on {dev}, contiguous along N")
+                and (len(shape) == 1 or len(shape) == 2 and shape[0] in (1, B))):
+            raise ValueError(f"{call.where}: positions int32 [N], [1, N] or [B, N] on q's device, contiguous along N")
         pos = positions.data_ptr()
-        pos_bs = positions.stride(0) if positions.dim() == 2 and positions.shape[0] == B and B > 1 else 0
-    _launch(call, where, dev.index, dt, B, N, d, rope.rot, rope.interleaved, rope.turns.data_ptr(), rope.factor, pos,
-            pos_bs, Hq, q.data_ptr(), *q.stride()[:3], qo.data_ptr(), *qo.stride()[:3], *side_k)
+        if len(shape) == 2 and shape[0] > 1:
+            pos_bs = positions.stride(0)
+    call(index, dt, B, N, d, rope.rot, rope.interleaved, rope.pointer, rope.factor, pos, pos_bs, Hq, qp, qb, qh, qn, op,
+         ob, oh, on, Hk, kp, kb, kh, kn, rp, rb, rh, rn)
     return qo, ko
 
 
@@ -746,12 +774,12 @@ def rope(q, k, rope, positions=None, out=None):
     dimensions (d contiguous); k may be None. positions: int32 [N], [1, N] or
     [B, N], or None for 0 .. N - 1. out: (q, k) to write to, which may be the
     inputs themselves."""
-    return _rope(lib().fb_rope_fwd, "fb_rope_fwd", q, k, rope, positions, out)
+    return _rope(_rope_fwd, q, k, rope, positions, out)
 
 
 def rope_bwd(dq, dk, rope, positions=None, out=None):
     """Gradients of rope's inputs from those of its outputs (fb_rope_bwd); arguments as for rope."""
-    return _rope(lib().fb_rope_bwd, "fb_rope_bwd", dq, dk, rope, positions, out)
+    return _rope(_rope_bwd, dq, dk, rope, positions, out)
 
 
 class PagedCache:
@@ -775,7 +803,7 @@ class PagedCache:
                         and s.device == k.device and s.is_contiguous()):
                     raise ValueError("PagedCache: scales float8_e8m0fnu or uint8 [pages, H, page]")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.device = k.device
+        self.device, self.index = k.device, k.get_device()
         self.num_pages, self.heads, self.page, self.d = k.shape
 
     @classmethod
@@ -790,15 +818,17 @@ class PagedCache:
             torch.float8_e8m0fnu) for _ in range(2)])
 
     def _pointers(self):
-        e4m3 = self.dt == FB_E4M3
-        return (self.k.data_ptr(), self.v.data_ptr(), self.k_scale.data_ptr() if e4m3 else 0,
-                self.v_scale.data_ptr() if e4m3 else 0, self.num_pages, self.page)
+        # afresh at each call: the tensors are the user's, who may have resized or moved them
+        if self.dt == FB_BF16:
+            return self.k.data_ptr(), self.v.data_ptr(), 0, 0, self.num_pages, self.page
+        return (self.k.data_ptr(), self.v.data_ptr(), self.k_scale.data_ptr(), self.v_scale.data_ptr(), self.num_pages,
+                self.page)
 
     def _table(self, table, B):
         import torch
-        if not (table.dtype == torch.int32 and table.dim() == 2 and table.shape[0] == B
-                and table.device == self.device and table.is_contiguous()):
-            raise ValueError(f"block table: a contiguous int32 tensor [{B}, pages] on {self.device}")
+        if not (table.dtype is torch.int32 and table.dim() == 2 and table.shape[0] == B
+                and table.get_device() == self.index and table.is_contiguous()):
+            raise ValueError(f"block table: a contiguous int32 tensor [{B}, pages] on cuda:{self.index}")
         return table.data_ptr(), table.shape[1]
 
 
@@ -807,20 +837,19 @@ def cache_write(cache: PagedCache, k, v, table, starts, counts=None):
     k, v [B, H, N, d] (bf16 or fp32, any order of the first three dimensions)
     becomes token starts[b] + n of sequence b. table: int32 [B, max_pages];
     starts, counts: int32 [B] (counts None: every row)."""
-    if not (k.dim() == 4 and k.device == cache.device and k.stride(3) == 1 and v.shape == k.shape
-            and v.dtype == k.dtype and v.device == k.device and v.stride(3) == 1):
-        raise ValueError(f"cache_write: k, v [B, H, N, d] on {cache.device}, d contiguous")
     B, H, N, d = k.shape
-    if not (H == cache.heads and d == cache.d):
-        raise ValueError(f"cache_write: {cache.heads} heads of {cache.d}")
+    index, dt = cache.index, _code(k.dtype)
+    if (H != cache.heads or d != cache.d or dt is None or k.get_device() != index or v.shape != k.shape
+            or v.dtype is not k.dtype or v.get_device() != index):
+        raise ValueError(f"cache_write: k, v bfloat16 or float32 [B, {cache.heads}, N, {cache.d}] on cuda:{index}")
+    if starts is None:
+        raise ValueError("cache_write: starts")
+    kx, kb, kh, kn = _side(k, "k")
+    vx, vb, vh, vn = _side(v, "v")
     tab, width = cache._table(table, B)
     kp, vp, ks, vs, pages, page = cache._pointers()
-    if not (starts is not None):
-        raise ValueError("cache_write: starts")
-    dev = cache.device
-    _launch(lib().fb_cache_write, "fb_cache_write", dev.index, _dtype_code(k), cache.dt, B, H, N, d, k.data_ptr(),
-            *k.stride()[:3], v.data_ptr(), *v.stride()[:3], kp, vp, ks, vs, pages, page, tab, width,
-            _ints(starts, (B,), dev, "starts"), _ints(counts, (B,), dev, "counts"))
+    _cache_write(index, dt, cache.dt, B, H, N, d, kx, kb, kh, kn, vx, vb, vh, vn, kp, vp, ks, vs, pages, page, tab,
+                 width, _ints(starts, (B,), index, "starts"), _ints(counts, (B,), index, "counts"))
 
 
 def cache_read(cache: PagedCache, table, starts, counts, tokens: int, dtype=None, out=None):
@@ -828,21 +857,24 @@ def cache_read(cache: PagedCache, table, starts, counts, tokens: int, dtype=None
     [B, H, tokens, d] (fb_cache_read), rows past counts[b] zero; dtype bfloat16
     (the default) or float32. starts None: from 0; counts None: all tokens."""
     import torch
-    B, dev = table.shape[0], cache.device
+    B, index = table.shape[0], cache.index
     tab, width = cache._table(table, B)
     shape = (B, cache.heads, tokens, cache.d)
     if out is None:
         dtype = torch.bfloat16 if dtype is None else dtype
-        k, v = torch.empty(shape, dtype=dtype, device=dev), torch.empty(shape, dtype=dtype, device=dev)
+        k = torch.empty(shape, dtype=dtype, device=cache.device)
+        v = torch.empty_like(k)
     else:
         k, v = out
-        if not (all(t.shape == shape and t.device == dev and t.is_contiguous() and t.dtype == k.dtype for t in (k, v))
-                and dtype in (None, k.dtype)):
+        if not (all(t.shape == shape and t.get_device() == index and t.is_contiguous() and t.dtype is k.dtype
+                    for t in (k, v)) and dtype in (None, k.dtype)):
             raise ValueError(f"cache_read: out two contiguous tensors {shape}")
+    dt = _code(k.dtype)
+    if dt is None:
+        raise ValueError("cache_read: dtype bfloat16 or float32")
     kp, vp, ks, vs, pages, page = cache._pointers()
-    _launch(lib().fb_cache_read, "fb_cache_read", dev.index, _dtype_code(k), cache.dt, B, cache.heads, tokens, cache.d,
-            kp, vp, ks, vs, pages, page, tab, width, _ints(starts, (B,), dev, "starts"),
-            _ints(counts, (B,), dev, "counts"), k.data_ptr(), v.data_ptr())
+    _cache_read(index, dt, cache.dt, B, cache.heads, tokens, cache.d, kp, vp, ks, vs, pages, page, tab, width,
+                _ints(starts, (B,), index, "starts"), _ints(counts, (B,), index, "counts"), k.data_ptr(), v.data_ptr())
     return k, v
 
 
@@ -866,8 +898,12 @@ class CacheBias:
         self.k_heads = phi_k.shape[0]
         nb = fb_cache_bias_bytes(self.q_heads, self.k_heads, self.P, self.R)
         self.prepared = torch.empty(max(nb, 1), device=self.device, dtype=torch.uint8)
-        _launch(lib().fb_cache_bias_prepare, "fb_cache_bias_prepare", self.device.index, self.q_heads, self.k_heads,
-                self.P, self.R, phi_q.data_ptr(), phi_k.data_ptr(), self.prepared.data_ptr(), nb)
+        with torch.cuda.device(self.device):
+            _check(fb_cache_bias_prepare(self.q_heads, self.k_heads, self.P, self.R, phi_q.data_ptr(), phi_k.data_ptr(),
+                                         self.prepared.data_ptr(), nb, _stream(self.device)), "fb_cache_bias_prepare")
+        self.index = phi_q.get_device()
+        # the five words that a call takes
+        self.words = self.R, self.P, self.q_heads, self.k_heads, self.prepared.data_ptr()
 
 
 def cache_workspace(B: int, Hq: int, H: int, T: int, d: int, device="cuda"):
@@ -892,39 +928,37 @@ def attn_cache(q, cache: PagedCache, table, prefix, counts=None, tree_mask=None,
     workspace: of cache_workspace (None: allocated here, at the cost of a
     memset)."""
     import torch
-    dev = cache.device
-    if not (q.dim() == 4 and q.dtype == torch.bfloat16 and q.device == dev and q.is_contiguous()):
-        raise ValueError(f"attn_cache: q a contiguous bfloat16 tensor [B, Hq, T, d] on {dev}")
     B, Hq, T, d = q.shape
-    H = cache.heads
-    if not (d == cache.d):
-        raise ValueError(f"attn_cache: head dim {cache.d}")
+    index, H = cache.index, cache.heads
+    if q.dtype is not torch.bfloat16 or q.get_device() != index or d != cache.d or not q.is_contiguous():
+        raise ValueError(f"attn_cache: q a contiguous bfloat16 tensor [B, Hq, T, {cache.d}] on cuda:{index}")
     tab, width = cache._table(table, B)
-    words, mask = 0, 0
+    mask = words = 0
     if tree_mask is not None:
         words = tree_mask.shape[-1]
-        mask = _ints(tree_mask, (B, T, words), dev, "tree_mask")
-    R, P, fq, fk, pb = 0, 0, 0, 0, 0
+        mask = _ints(tree_mask, (B, T, words), index, "tree_mask")
+    R = P = fq = fk = pb = 0
     if bias is not None:
-        if not (bias.device == dev):
+        if bias.index != index:
             raise ValueError("attn_cache: the bias is on another device")
-        R, P, fq, fk, pb = bias.R, bias.P, bias.q_heads, bias.k_heads, bias.prepared.data_ptr()
-    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    o = torch.empty_like(q) if out is None else out
-    l = torch.empty((B, Hq, T), device=dev, dtype=torch.float32) if lse is None else lse
-    if not (out is None or (o.shape == q.shape and o.dtype == q.dtype and o.device == dev and o.is_contiguous())):
+        R, P, fq, fk, pb = bias.words
+    if out is None:
+        out = torch.empty_like(q)
+    elif not (out.shape == q.shape and out.dtype is q.dtype and out.get_device() == index and out.is_contiguous()):
         raise ValueError("attn_cache: out like q")
-    if not (lse is None or (l.shape == (B, Hq, T) and l.dtype == torch.float32 and l.device == dev
-                            and l.is_contiguous())):
+    if lse is None:
+        lse = torch.empty((B, Hq, T), device=cache.device, dtype=torch.float32)
+    elif not (lse.shape == (B, Hq, T) and lse.dtype is torch.float32 and lse.get_device() == index
+              and lse.is_contiguous()):
         raise ValueError("attn_cache: lse a contiguous float32 tensor [B, Hq, T]")
-    kp, vp, ks, vs, pages, page = cache._pointers()
     if workspace is None:
         nb = fb_attn_cache_workspace_bytes(B, Hq, H, T, d)
-        workspace = torch.zeros(max(nb, 1), device=dev, dtype=torch.uint8)
-    if workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError("attn_cache: workspace of cache_workspace")
-    _launch(lib().fb_attn_cache_fwd, "fb_attn_cache_fwd", dev.index, cache.dt, B, Hq, H, T, d, q.data_ptr(), kp, vp, ks,
-            vs, pages, page, tab, width, _ints(prefix, (B,), dev, "prefix"), _ints(counts, (B,), dev, "counts"), mask,
-            words, _ints(depths, (B, T), dev, "depths"), R, P, fq, fk, pb, scale, o.data_ptr(), l.data_ptr(),
-            workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    return o, l
+        workspace = torch.zeros(max(nb, 1), device=cache.device, dtype=torch.uint8)
+    if workspace.dtype is not torch.uint8 or workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError("attn_cache: a workspace of cache_workspace")
+    kp, vp, ks, vs, pages, page = cache._pointers()
+    _attn_cache(index, cache.dt, B, Hq, H, T, d, q.data_ptr(), kp, vp, ks, vs, pages, page, tab, width,
+                _ints(prefix, (B,), index, "prefix"), _ints(counts, (B,), index, "counts"), mask, words,
+                _ints(depths, (B, T), index, "depths"), R, P, fq, fk, pb, d ** -0.5 if scale is None else scale,
+                out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel())
+    return out, lse

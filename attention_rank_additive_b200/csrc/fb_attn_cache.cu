@@ -744,7 +744,8 @@ cudaError_t launch_bias(const CacheAttnArgs &a, int sms, cudaStream_t st) {
   }
   stages = std::max(2, stages);
   const int smem = fixed + std::max(join, stages * stage);
-  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<unsigned long long> done{0};
+  const cudaError_t e = allow_all_shared_memory(reinterpret_cast<const void *>(k), done);
   if (e != cudaSuccess) return e;
   const long long blocks = std::max<long long>(1, (((long long)a.max_pages << a.page_shift) + keys - 1) / keys);
   const int grid = int(std::min<long long>((long long)a.B * a.H * a.chunks * blocks, (long long)sms * ctas));

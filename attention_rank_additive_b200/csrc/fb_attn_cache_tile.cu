@@ -808,14 +808,19 @@ TilePlan make_plan(int d, int R, int rows) {
   return best;
 }
 
-template <int DP, bool E4M3>
-cudaError_t launch_tile(const CacheAttnArgs &a, const TilePlan &p, int grid, cudaStream_t st) {
-  void (*k)(const CacheAttnArgs, const TilePlan) =
-      a.R == 0 ? attn_cache_tile_kernel<DP, E4M3, 0>
-               : (a.R <= kCacheBiasExact ? attn_cache_tile_kernel<DP, E4M3, 1> : attn_cache_tile_kernel<DP, E4M3, 2>);
-  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(p.smem));
+template <int DP, bool E4M3, int BIAS>
+cudaError_t launch_bias(const CacheAttnArgs &a, const TilePlan &p, int grid, cudaStream_t st) {
+  auto *k = attn_cache_tile_kernel<DP, E4M3, BIAS>;
+  static std::atomic<unsigned long long> done{0};
+  const cudaError_t e = allow_all_shared_memory(reinterpret_cast<const void *>(k), done);
   if (e != cudaSuccess) return e;
   return launch_programmatic(k, dim3(unsigned(grid)), dim3(kThreads), size_t(p.smem), st, a, p);
+}
+
+template <int DP, bool E4M3>
+cudaError_t launch_tile(const CacheAttnArgs &a, const TilePlan &p, int grid, cudaStream_t st) {
+  if (a.R == 0) return launch_bias<DP, E4M3, 0>(a, p, grid, st);
+  return a.R <= kCacheBiasExact ? launch_bias<DP, E4M3, 1>(a, p, grid, st) : launch_bias<DP, E4M3, 2>(a, p, grid, st);
 }
 
 }  // namespace

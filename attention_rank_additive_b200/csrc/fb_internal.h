@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/flashbias.h"
 
 namespace fb {
@@ -185,6 +187,18 @@ cudaError_t launch_programmatic(void (*kern)(KArgs...), dim3 grid, dim3 block, s
 
 // Whether the cache's kernels take this head dim and page size.
 bool cache_dims_ok(int d, int page_size);
+
+// Lets a kernel ask for all of an SM's shared memory, once per device (`done`: a bit each).
+inline cudaError_t allow_all_shared_memory(const void *kernel, std::atomic<unsigned long long> &done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 
 // Per-device flag word (allocated once per device as a module global).
 int *device_flags();

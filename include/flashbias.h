@@ -590,6 +590,23 @@ int fb_attn_cache_fwd(int cache_dt, int B, int Hq, int H, int T, int d, const vo
                       void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * The entry points of a decode step with their arguments as 8-byte words, for
+ * bindings that pay for each argument: `words` holds `count` arguments in the
+ * order of the function's parameters (integers sign-extended, pointers as they
+ * are, floats as doubles). Another count is FB_ERR_INVALID_ARG, another entry
+ * FB_ERR_UNSUPPORTED; otherwise the status of the call.
+ */
+typedef enum {
+  FB_CALL_ROPE_FWD = 0,     /* 29 words */
+  FB_CALL_ROPE_BWD = 1,     /* 29 */
+  FB_CALL_CACHE_WRITE = 2,  /* 25 */
+  FB_CALL_CACHE_READ = 3,   /* 19 */
+  FB_CALL_ATTN_CACHE_FWD = 4 /* 31 */
+} fb_entry;
+
+int fb_call(int entry, const uint64_t *words, int count);
+
+/*
  * Synchronises `stream`, then reads and clears the library's device flag:
  * FB_ERR_TIMEOUT if a kernel's bounded wait ran out, FB_ERR_RANGE if a factor
  * overflowed fp16 in the preparation step or a cache call met a token, length
