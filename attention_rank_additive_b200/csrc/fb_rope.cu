@@ -147,10 +147,11 @@ cudaError_t launch_v(RopeArgs a, int interleaved, cudaStream_t st) {
   a.units = a.turn_units + copy_units;
   const long long tokens_units = (long long)a.B * a.N * a.units;
   const int H = a.heads[0] + a.heads[1];
-  // Heads per thread: as many as leave four waves of threads on 148 SMs, at most 8 (the sines and cosines
-  // then cost less than the loads); a single token gets one head per thread.
-  long long hpt = tokens_units * H / (148ll * 2048 * 4);
-  a.hpt = int(hpt < 1 ? 1 : (hpt > 8 ? 8 : hpt));
+  // Heads per thread, which share one set of sines and cosines (320 instructions for V = 8): as many as leave 148
+  // SMs 1024 threads each, at most 16; a single token gets one head per thread. With four full waves of threads asked
+  // for instead, a prompt of 8 x 2048 tokens and 24 heads got one head each and took 31 us.
+  long long hpt = tokens_units * H / (148ll * 1024);
+  a.hpt = int(hpt < 1 ? 1 : (hpt > 16 ? 16 : hpt));
   if (a.hpt > H) a.hpt = H;
   a.hgroups = (H + a.hpt - 1) / a.hpt;
   if (tokens_units > 0xffffff00ll || a.hgroups > 65535) return cudaErrorInvalidValue;
