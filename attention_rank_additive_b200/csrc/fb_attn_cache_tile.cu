@@ -4,11 +4,11 @@
 // products bound the time, so they run as 128 x 128 tiles.
 //
 // A CTA (one per SM) holds one or two tiles of 128 query rows of an item and
-// walks over its run of 128-key tiles:
+// walks over its run of 96-key tiles (two of K, V and factors fit beside the queries
+// at the largest head dim and ranks up to 32; of 128 keys only one K would):
 //   warp 0          MMA issuer: S = Q K^T (+ phi_q phi_k^T), O += P V
-//   warps 1-3       V loader
-//   warps 4-7       K loader: codes or bf16 from the pages to a swizzled bf16
-//                   tile, and the keys' bias factors
+//   warps 1-3, 4-7  V and K loader: codes or bf16 from the pages to swizzled bf16
+//                   tiles; the K loader also the factors and the query tiles
 //   warps 8-11, 12-15  softmax of stream 0 and 1: a thread per row (TMEM lane)
 // Stream t is row tile t (both walk over the same keys), or, when an item has
 // 128 rows or fewer, every second key tile of the one row tile: the streams
@@ -20,9 +20,10 @@
 // and its exponent with the row's power of two as well, so scores and values
 // need no further scaling.
 //
-// The roles run side by side out of one instruction cache, so loops stay rolled
-// where they can: with all of them unrolled, warps waited for instructions ten
-// cycles of each twenty-four and grouped trees of 61 tokens took 972 us.
+// The roles run side by side out of one instruction cache, which decides more than
+// the instructions do: loops stay rolled, K and V share the loaders' loop, and
+// what is rare is out of line. Grouped trees of 61 tokens took 972 us with
+// everything unrolled, the instruction cache behind the SM 69 % busy even at 237 us.
 //
 // The bias joins S in the same accumulator: phi_q / scale, split into fp16 parts
 // again, times the keys' prepared parts (three products). Ranks up to 4 are fp32
@@ -39,14 +40,13 @@ namespace {
 constexpr int kThreads = 16 * 32;  // four warps a scheduler: 128 registers a thread
 constexpr int kVThreads = 96;
 constexpr int kIssuer = 0, kVWarp = 1, kKWarp = 4, kSoftmaxWarp = 8;
-constexpr int kTileKeys = 128;
+constexpr int kTileKeys = 96, kGroups = kTileKeys / 16;
 constexpr float kRaise = 8.f;  // log2 units: O is rescaled when the maximum grows by more
 
 struct TilePlan {
   int tiles;  // row tiles of an item's chunk: 1 or 2
   int split;  // one row tile, its key tiles dealt to two streams
-  int ks, vs;  // K and V slots
-  int fs;      // slots of the keys' factors
+  int ks, vs;  // slots of K and its factors, and of V
   int rpb;    // bias: columns reserved for the hi and for the lo parts (32, 64, 128), or 0
   uint32_t q, fq, k, fk, v, planes, ctrl;  // shared memory offsets from the 1024-byte aligned base
   uint32_t smem;
@@ -64,19 +64,24 @@ struct Ctrl {
   int abort, last;
 };
 
-// 16-byte chunk `ch` of row `row` in a tile of 128-byte rows, swizzled; columns past 64 go to the next 128-row block.
+// 16-byte chunk `ch` of row `row` in a tile of 128-byte rows, swizzled; columns past 64 go to the next block of ROWS rows.
+template <int ROWS>
 __device__ __forceinline__ uint32_t tile_at(int row, int ch) {
-  return uint32_t(ch >> 3) * (kTileKeys * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4);
+  return uint32_t(ch >> 3) * (ROWS * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4);
 }
-// Matrix descriptors of a K-major tile and of V: only the start address in the low word is not a constant.
-__device__ __forceinline__ uint64_t desc(uint32_t start, uint32_t lbo) {
+// Low word of the matrix descriptor of a K-major tile, and of V, at shared memory address `at`; the start address is its
+// lowest field, so that a step is added to it. The high word is a constant.
+__device__ __forceinline__ uint32_t low_k(uint32_t at) { return (at >> 4) | (16u >> 4) << 16; }
+__device__ __forceinline__ uint32_t low_v(uint32_t at) { return (at >> 4) | uint32_t(kTileKeys * 128 >> 4) << 16; }
+__device__ __forceinline__ uint64_t desc(uint32_t low) {
   constexpr uint32_t high = (1024u >> 4) | (1u << 14) | (swizzle_code(128) << 29);
-  return (uint64_t(high) << 32) | ((lbo >> 4) << 16) | start;
+  return (uint64_t(high) << 32) | low;
 }
-__device__ __forceinline__ uint64_t desc_k(uint32_t start) { return desc(start, 16); }
-__device__ __forceinline__ uint64_t desc_v(uint32_t start) { return desc(start, kTileKeys * 128); }
-// Start-address offsets (16-byte units) of 16-column step kk of a K-major tile, and of 16-key step kk of V.
-__device__ __forceinline__ uint32_t step_k(int kk) { return uint32_t((kk >> 2) * (kTileKeys * 128) + (kk & 3) * 32) >> 4; }
+// Start-address offsets (16-byte units) of 16-column step kk of a K-major tile of ROWS rows, and of 16-key step kk of V.
+template <int ROWS>
+__device__ __forceinline__ uint32_t step_k(int kk) {
+  return uint32_t((kk >> 2) * (ROWS * 128) + (kk & 3) * 32) >> 4;
+}
 __device__ __forceinline__ uint32_t step_v(int kk) { return uint32_t(kk * 16 * 128) >> 4; }
 
 // Visibility of keys j0 .. j0 + 31 to new token t, a bit each (t < 0: none past the context).
@@ -126,31 +131,40 @@ __device__ __forceinline__ void sts16(uint32_t at, uint32_t a, uint32_t b, uint3
   st_shared_v4(at, a, b, c, d);
 }
 
-// The pages of a segment's 128-key tiles, for a loader warp: lane i (< 8) holds the page of 16-key group i, fetched
-// one tile ahead, so that no load of a row waits for its page number.
+// The pages of a segment's key tiles, for a loader warp: lane i (< kGroups) holds the page of 16-key group i, fetched
+// a tile ahead, so that no load of a row waits for its page number.
 struct Pages {
   int now, next;
   __device__ __forceinline__ int fetch(const CacheAttnArgs &a, int b, int j, int len, int lane) const {
     j += 16 * lane;
-    return lane < 8 && j < len ? __ldg(a.table + (long long)b * a.max_pages + (j >> a.page_shift)) : 0;
+    return lane < kGroups && j < len ? __ldg(a.table + (long long)b * a.max_pages + (j >> a.page_shift)) : 0;
   }
-  __device__ __forceinline__ void start(const CacheAttnArgs &a, int b, int j, int len, int lane) {
-    next = fetch(a, b, j, len, lane);
-  }
-  // Moves on to the tile at j; bit i of the result: group i has a page or lies behind the last key.
-  __device__ __forceinline__ unsigned step(const CacheAttnArgs &a, int b, int j, int len, int lane) {
-    now = next;
-    next = fetch(a, b, j + kTileKeys, len, lane);
-    const bool ok = now >= 0 && now < a.num_pages;
-    if (!ok) now = 0;
-    return __ballot_sync(0xffffffffu, ok) & 0xffu;
-  }
-  // Pool row of the tile's row `row`.
-  __device__ __forceinline__ long long pool_row(const CacheAttnArgs &a, int h, int j, int row) const {
-    const int page = __shfl_sync(0xffffffffu, now, row >> 4);
-    return (((long long)page * a.H + h) << a.page_shift) + ((j + row) & ((1 << a.page_shift) - 1));
+  // Bit i: group i of the present tile has a page or lies behind the last key.
+  __device__ __forceinline__ unsigned alive(const CacheAttnArgs &a) const {
+    return __ballot_sync(0xffffffffu, now >= 0 && now < a.num_pages) & ((1u << kGroups) - 1u);
   }
 };
+// Pool row of the tile's row `row`, given the lanes' pages (one outside the pool counts as page 0: it is cleared).
+__device__ __forceinline__ long long pool_row(const CacheAttnArgs &a, int pages, int h, int j, int row) {
+  const int page = __shfl_sync(0xffffffffu, pages >= 0 && pages < a.num_pages ? pages : 0, row >> 4);
+  return (((long long)page * a.H + h) << a.page_shift) + ((j + row) & ((1 << a.page_shift) - 1));
+}
+
+struct Chunks {
+  uint4 x, y;
+};
+// The chunks without their non-finite values; `odd` where there were any.
+__device__ __noinline__ Chunks clear_odd(Chunks c, int *odd, int stamp) {
+  uint32_t w[8] = {c.x.x, c.x.y, c.x.z, c.x.w, c.y.x, c.y.y, c.y.z, c.y.w};
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const uint32_t even = even_word<false>(w[k]);
+    if (even != w[k]) *odd = stamp;
+    w[k] = even;
+  }
+  c.x = make_uint4(w[0], w[1], w[2], w[3]), c.y = make_uint4(w[4], w[5], w[6], w[7]);
+  return c;
+}
 
 __device__ __noinline__ void wait_long(uint64_t *bar, uint32_t parity, volatile int *abort) {
   mbar_wait_long(bar, parity, abort);
@@ -163,7 +177,7 @@ template <int DP, bool E4M3, int BIAS>
 __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const __grid_constant__ CacheAttnArgs a, const TilePlan p) {
   constexpr int ES = E4M3 ? 1 : 2;
   constexpr int CPR = DP * ES / 16;  // 16-byte chunks of a pool row (padded); also the chunks of a tile per loader thread
-  constexpr uint32_t kTile = kTileKeys * DP * 2;
+  constexpr uint32_t kTile = kTileKeys * DP * 2, kQTile = 128 * DP * 2;
   extern __shared__ __align__(16) uint8_t smem_dyn[];
   uint8_t *sm = smem_dyn + ((1024u - (smem_u32(smem_dyn) & 1023u)) & 1023u);
   Ctrl &c = *reinterpret_cast<Ctrl *>(sm + p.ctrl);
@@ -171,10 +185,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const __gr
   const uint32_t base = smem_u32(sm);
   // [tile & 3][rank][key]: the keys' factors, ranks up to 4
   float(*planes)[4][kTileKeys] = reinterpret_cast<float(*)[4][kTileKeys]>(sm + p.planes);
-  const uint32_t fq_tile = kTileKeys * 4 * p.rpb, fk_tile = fq_tile;
+  const uint32_t fq_tile = 128 * 4 * p.rpb, fk_tile = kTileKeys * 4 * p.rpb;
 
   if (threadIdx.x == 0) {
-    mbar_init(&c.q_full, p.tiles * 128);
+    mbar_init(&c.q_full, 128);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&c.k_full[i], 128), mbar_init(&c.v_full[i], kVThreads);
       mbar_init(&c.k_empty[i], 1), mbar_init(&c.v_empty[i], 1);
@@ -228,57 +242,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const __gr
       const int tok = have && tok_all < s.count ? tok_all : -1;
       const int steps = t < nstreams ? steps_of(t, n, rows) : 0;
       float fq[4] = {0.f, 0.f, 0.f, 0.f};
-      if (t < p.tiles || p.split) {
+      if (BIAS == 1 && tok >= 0) {
         const int hq = a.fq_heads > 1 ? h * a.G + (chunk0 + r) / a.T : 0;
-        const int pos = BIAS != 0 && tok >= 0 ? new_position(a, g.b, s, tok) : 0;
-        if (BIAS == 1 && tok >= 0) {
-          const float4 f = __ldg(static_cast<const float4 *>(a.fq) + (long long)hq * a.P + pos);
-          fq[0] = f.x, fq[1] = f.y, fq[2] = f.z, fq[3] = f.w;
-        }
-        if (t < p.tiles) {
-          // this row of the Q tile, and of the factor tile
-          const uint32_t qt = base + p.q + t * kTile;
-          const uint4 *q = reinterpret_cast<const uint4 *>(a.Q + qrow * a.d);
-#pragma unroll 8
-          for (int ch = 0; ch < DP / 8; ++ch) {
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (have && ch * 8 < a.d) v = __ldg(q + ch);
-            sts16(qt + tile_at(row, ch), v.x, v.y, v.z, v.w);
-          }
-          if (BIAS == 2) {
-            const uint32_t ft = base + p.fq + t * fq_tile;
-            const float inv = 1.f / a.scale;
-            const uint4 *f = static_cast<const uint4 *>(a.fq) + ((long long)hq * a.P + pos) * (a.RP / 4);
-            bool over = false;
-#pragma unroll 2
-            for (int i = 0; i < a.RP / 8; ++i) {  // eight ranks: 16 bytes of hi, 16 of lo
-              uint32_t hi[4] = {0u, 0u, 0u, 0u}, lo[4] = {0u, 0u, 0u, 0u};
-              if (tok >= 0) {
-                const uint4 u[2] = {__ldg(f + 2 * i), __ldg(f + 2 * i + 1)};
-#pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                  const uint32_t hw = w == 0 ? u[0].x : (w == 1 ? u[0].y : (w == 2 ? u[1].x : u[1].y));
-                  const uint32_t lw = w == 0 ? u[0].z : (w == 1 ? u[0].w : (w == 2 ? u[1].z : u[1].w));
-                  const float2 h2 = __half22float2(*reinterpret_cast<const __half2 *>(&hw));
-                  const float2 l2 = __half22float2(*reinterpret_cast<const __half2 *>(&lw));
-                  float x0 = (h2.x + l2.x) * inv, x1 = (h2.y + l2.y) * inv;
-                  over |= !(fabsf(x0) <= 65504.f) || !(fabsf(x1) <= 65504.f);
-                  x0 = fminf(fmaxf(x0, -65504.f), 65504.f), x1 = fminf(fmaxf(x1, -65504.f), 65504.f);
-                  const __half2 hh = __floats2half2_rn(x0, x1);
-                  const float2 hf = __half22float2(hh);
-                  const __half2 ll = __floats2half2_rn(x0 - hf.x, x1 - hf.y);
-                  hi[w] = *reinterpret_cast<const uint32_t *>(&hh);
-                  lo[w] = *reinterpret_cast<const uint32_t *>(&ll);
-                }
-              }
-              sts16(ft + tile_at(row, i), hi[0], hi[1], hi[2], hi[3]);
-              sts16(ft + tile_at(row, p.rpb / 8 + i), lo[0], lo[1], lo[2], lo[3]);
-            }
-            if (over) atomicOr(a.flags, kFlagRange);
-          }
-          fence_proxy_async_smem();
-          mbar_arrive(&c.q_full);
-        }
+        const float4 f = __ldg(static_cast<const float4 *>(a.fq) + (long long)hq * a.P + new_position(a, g.b, s, tok));
+        fq[0] = f.x, fq[1] = f.y, fq[2] = f.z, fq[3] = f.w;
       }
       const bool busy = __any_sync(0xffffffffu, tok >= 0);  // rows of this warp that want a result
       float m = -INFINITY, l = 0.f;
@@ -293,7 +260,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const __gr
         if (i > 0 && c.odd[(tile - (p.split ? 2 : 1)) & 7] == int(tile - (p.split ? 2 : 1)) + 1) odd = 1;
         if (busy) {
           const unsigned alive = c.alive[tile & 3];
-          const bool tail = j0 + kTileKeys > s.prefix || alive != 0xffu;
+          const bool tail = j0 + kTileKeys > s.prefix || alive != (1u << kGroups) - 1u;
+          // which keys this row sees, found before its scores take the registers
+          constexpr int kParts = kTileKeys / 32;
+          uint32_t see[kParts];
+          if (__builtin_expect(tail, 0)) {
+#pragma unroll
+            for (int q = 0; q < kParts; ++q) {
+              see[q] = sees(a, s.prefix, s.count, g.b, tok, j0 + 32 * q);
+              if (!((alive >> (2 * q)) & 1u)) see[q] &= 0xffff0000u;
+              if (!((alive >> (2 * q + 1)) & 1u)) see[q] &= 0x0000ffffu;
+            }
+          }
           // the scores of columns 32 q .. 32 q + 31: biased (rank <= 4), masked
           auto finish = [&](int q, uint32_t *x) {
             if constexpr (BIAS == 1) {
@@ -311,20 +289,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const __gr
                 for (int e = 0; e < 4; ++e) x[k + e] = __float_as_uint(fmaf(__uint_as_float(x[k + e]), a.scale, y[e]));
               }
             }
-            if (tail) {
-              uint32_t see = sees(a, s.prefix, s.count, g.b, tok, j0 + 32 * q);
-              if (!((alive >> (2 * q)) & 1u)) see &= 0xffff0000u;
-              if (!((alive >> (2 * q + 1)) & 1u)) see &= 0x0000ffffu;
+            if (__builtin_expect(tail, 0)) {
+              const uint32_t mine = q == 0 ? see[0] : (q == 1 ? see[1] : see[2]);
 #pragma unroll
               for (int k = 0; k < 32; ++k)
-                if (!((see >> k) & 1u)) x[k] = 0xff800000u;
+                if (!((mine >> k) & 1u)) x[k] = 0xff800000u;
             }
           };
-          // Two passes over S in rolled loops of 32 columns. (One pass that keeps P in registers until the maximum is
-          // known reads S once but needs four copies of the loop's body: 352 against 300 us for grouped trees.)
+          // Two passes over S in rolled loops of 32 columns. (One pass, with all scores or all of P in registers, reads S
+          // once but needs a copy of the loop's body per 32 columns: 300 to 350 us for grouped trees.)
           float top = -INFINITY;
 #pragma unroll 1
-          for (int q = 0; q < 4; ++q) {
+          for (int q = 0; q < kParts; ++q) {
             uint32_t x[32];
             tmem_ld32(s_tm + 32u * q, x);
             tmem_ld_wait32(x);
@@ -339,13 +315,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const __gr
             l *= alpha;
             if (i > 0) {
 #pragma unroll 1
-              for (int q = 0; q < DP / 32; ++q) {
-                uint32_t x[32];
-                tmem_ld32(o_tm + 32u * q, x);
-                tmem_ld_wait32(x);
+              for (int q = 0; q < DP / 16; ++q) {
+                uint32_t y[16];
+                tmem_ld16(o_tm + 16u * q, y);
+                tmem_ld_wait16(y);
 #pragma unroll
-                for (int k = 0; k < 32; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * alpha);
-                tmem_st32(o_tm + 32u * q, x);
+                for (int k = 0; k < 16; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * alpha);
+                tmem_st16(o_tm + 16u * q, y);
               }
             }
           }
@@ -353,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const __gr
           const uint64_t unit2 = f2_pack(unit, unit), shift2 = f2_pack(shift, shift), mu2 = f2_pack(mu, mu);
           uint64_t acc = 0;
 #pragma unroll 1
-          for (int q = 0; q < 4; ++q) {
+          for (int q = 0; q < kParts; ++q) {
             uint32_t x[32], w[16];
             tmem_ld32(s_tm + 32u * q, x);
             tmem_ld_wait32(x);
@@ -519,244 +495,256 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const __gr
     }
   } else if (warp != kIssuer) {
     // ------------------------------------------------------------- loaders
-    // A tile's chunk of 16 bytes of a pool row becomes one (bf16) or two (e4m3) of a tile's chunks.
-    auto convert = [&](const uint4 &raw, uint32_t scale, uint4 &x, uint4 &y) {
-      x = raw;
-      if constexpr (E4M3) {
-        // 2^(byte - 127); byte 255 is NaN, byte 0 (2^-127, which cache_write does not make) counts as 0
-        const float f = __uint_as_float(scale == 255u ? 0x7fffffffu : scale << 23);
-        x.x = e4m3_to_bf16(raw.x, false, f), x.y = e4m3_to_bf16(raw.x, true, f);
-        x.z = e4m3_to_bf16(raw.y, false, f), x.w = e4m3_to_bf16(raw.y, true, f);
-        y.x = e4m3_to_bf16(raw.z, false, f), y.y = e4m3_to_bf16(raw.z, true, f);
-        y.z = e4m3_to_bf16(raw.w, false, f), y.w = e4m3_to_bf16(raw.w, true, f);
-      }
-    };
-    auto store = [&](uint32_t dst, int row, int ch, const uint4 &x, const uint4 &y) {
-      if constexpr (E4M3) {
-        sts16(dst + tile_at(row, 2 * ch), x.x, x.y, x.z, x.w);
-        sts16(dst + tile_at(row, 2 * ch + 1), y.x, y.y, y.z, y.w);
-      } else {
-        sts16(dst + tile_at(row, ch), x.x, x.y, x.z, x.w);
-      }
-    };
+    const bool is_v = warp < kKWarp;
+    const int l = is_v ? threadIdx.x - kVWarp * 32 : threadIdx.x - kKWarp * 32, threads = is_v ? kVThreads : 128;
+    const uint8_t *pool = static_cast<const uint8_t *>(is_v ? a.vp : a.kp), *scales = is_v ? a.vs : a.ks;
+    const int slots = is_v ? p.vs : p.ks;
+    const uint32_t dst0 = base + (is_v ? p.v : p.k);
+    uint64_t *full = is_v ? c.v_full : c.k_full, *empty = is_v ? c.v_empty : c.k_empty;
+    // This thread's chunks, 16 bytes of a pool row each, which become one (bf16) or two (e4m3) of the tile's: at ch of
+    // rows row0, row0 + stride, ... A chunk's registers take the next tile's load as soon as it is stored.
+    const int ch = threadIdx.x % CPR, row0 = l / CPR, stride = threads / CPR, mine = kTileKeys / stride;
+    static_assert(kTileKeys * CPR / kVThreads == CPR, "chunks of a V loader thread; a K loader thread has fewer");
     const int rb = a.d * ES;  // bytes of a pool row
+    const bool inside = ch * 16 < rb;
+    const int at = inside ? ch * 16 : 0;
     unsigned tile = 0;
     Pages pages;
-    if (warp >= kKWarp) {
-      // K: loaded and converted before its slot is free, so that the tensor cores wait for the stores alone
-      const int l = threadIdx.x & 127;
-      // chunk i of this thread: 16 bytes at ch of row row0 + i * (128 / CPR)
-      const int ch = l % CPR, row0 = l / CPR;
-      const bool inside = ch * 16 < rb;
-      const uint32_t at0 = tile_at(row0, E4M3 ? 2 * ch : ch), at1 = tile_at(row0, 2 * ch + 1);
-      while (walk.next(a, g)) {
-        const Seq &s = g.s;
-        const int h = g.item / a.chunks, hk = a.fk_heads > 1 ? h : 0;
-        pages.start(a, g.b, g.k0 * kTileKeys, s.len, lane);
-        for (int kt = g.k0; kt < g.k1; ++kt, ++tile) {
-          const int j0 = kt * kTileKeys;
-          const unsigned alive = pages.step(a, g.b, j0, s.len, lane);
-          const int slot = p.ks == 2 ? int(tile & 1u) : 0;
-          const uint32_t dst = base + p.k + slot * kTile;
-          auto wait_empty = [&]() {
-            if (tile >= unsigned(p.ks))
-              wait_for(&c.k_empty[slot], (p.ks == 2 ? (tile >> 1) - 1 : tile - 1) & 1u, abort);
-          };
-          const bool early = p.ks == 2 || p.fs == 1;
-          if (early) wait_empty();
-          uint4 raw[CPR], more[E4M3 ? CPR : 1];
-          uint32_t sc[E4M3 ? CPR : 1];
+    while (walk.next(a, g)) {
+      const Seq &s = g.s;
+      const int h = g.item / a.chunks;
+      pages.now = pages.fetch(a, g.b, g.k0 * kTileKeys, s.len, lane);
+      pages.next = pages.fetch(a, g.b, (g.k0 + 1) * kTileKeys, s.len, lane);
+      if (!is_v) {
+        // ---- the query tiles, a thread per row, and their factors; their last readers are the S of all tiles so far
+        for (unsigned n = 1; n <= unsigned(slots) && n <= tile; ++n)
+          wait_for(&empty[(tile - n) % slots], ((tile - n) / slots) & 1u, abort);
+        const int chunk0 = (g.item - h * a.chunks) * p.tiles * 128, rows = min(p.tiles * 128, a.rows - chunk0);
+        const float inv = 1.f / a.scale;
+#pragma unroll 1
+        for (int t = 0; t < p.tiles; ++t) {
+          const int r = t * 128 + l, tok_all = (chunk0 + r) % a.T;
+          const bool have = r < rows;
+          const uint32_t qt = base + p.q + t * kQTile;
+          const uint4 *q = reinterpret_cast<const uint4 *>(
+              a.Q + (((long long)g.b * a.Hq + (long long)h * a.G) * a.T + chunk0 + (have ? r : 0)) * a.d);
+#pragma unroll 1
+          for (int c0 = 0; c0 < DP / 8; c0 += 8) {
+            uint4 v[8];
 #pragma unroll
-          for (int i = 0; i < CPR; ++i) {  // rows behind the last key read what lies there and are cleared below
-            const long long pr = pages.pool_row(a, h, j0, row0 + i * (128 / CPR));
-            raw[i] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(a.kp) + pr * rb + (inside ? ch * 16 : 0)));
-            if (E4M3) sc[E4M3 ? i : 0] = __ldg(a.ks + pr);
+            for (int i = 0; i < 8; ++i) {
+              v[i] = make_uint4(0u, 0u, 0u, 0u);
+              if (have && (c0 + i) * 8 < a.d) v[i] = __ldg(q + c0 + i);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sts16(qt + tile_at<128>(l, c0 + i), v[i].x, v[i].y, v[i].z, v[i].w);
           }
-          if (alive != 0xffu && l == 0) atomicOr(a.flags, kFlagRange);
-          const bool plain = j0 + kTileKeys <= min(s.prefix, a.P);  // positions are j0, j0 + 1, ...
-          auto position = [&](int row) {
-            const int j = j0 + row;
-            if (plain) return j;
-            if (j >= s.len) return 0;
-            if (j >= s.prefix) return new_position(a, g.b, s, j - s.prefix);
-            if (j < a.P) return j;
-            atomicOr(a.flags, kFlagRange);
-            return a.P - 1;
-          };
-          uint4 f;
-          if constexpr (BIAS == 1) f = __ldg(static_cast<const uint4 *>(a.fk) + (long long)hk * a.P + position(l));
           if constexpr (BIAS == 2) {
-            // The keys' factors, (4 hi, 4 lo) groups of 16 bytes, go to the hi and lo columns of one of two tiles by
-            // asynchronous copies of 8 bytes. Its last reader, tile - 2's S, is done: with two K slots the wait above
-            // was for it, with one the last turn's (a single slot's, tile - 1's S, was waited for above).
-            const uint32_t ft = base + p.fk + (p.fs == 2 ? tile & 1u : 0u) * fk_tile;
-            const int groups = a.RP / 4, total = kTileKeys * groups;
-            const uint4 *fbase = static_cast<const uint4 *>(a.fk) + (long long)hk * a.P * groups;
-            // lo columns: four chunks on in the same 64 columns, or in the blocks behind the hi ones
-            auto copy = [&](const uint4 *src, uint32_t hi) {
-              const uint32_t lo = p.rpb == 32 ? hi ^ 64u : hi + (p.rpb >> 6) * (kTileKeys * 128);
-              copy_whole<2>(ft + hi, src);
-              copy_whole<2>(ft + lo, reinterpret_cast<const uint2 *>(src) + 1);
+            const uint32_t ft = base + p.fq + t * fq_tile;
+            const bool real = have && tok_all < s.count;
+            const int hq = a.fq_heads > 1 && have ? h * a.G + (chunk0 + r) / a.T : 0;
+            const uint4 *f = static_cast<const uint4 *>(a.fq) +
+                             ((long long)hq * a.P + (real ? new_position(a, g.b, s, tok_all) : 0)) * (a.RP / 4);
+            bool over = false;
+#pragma unroll 1
+            for (int i = 0; i < a.RP / 8; i += 2) {  // sixteen ranks; eight are 16 bytes of hi and 16 of lo
+              uint4 u[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) u[k] = real ? __ldg(f + 2 * i + k) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const uint32_t hw[4] = {u[2 * k].x, u[2 * k].y, u[2 * k + 1].x, u[2 * k + 1].y};
+                const uint32_t lw[4] = {u[2 * k].z, u[2 * k].w, u[2 * k + 1].z, u[2 * k + 1].w};
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                  const float2 h2 = __half22float2(*reinterpret_cast<const __half2 *>(&hw[w]));
+                  const float2 l2 = __half22float2(*reinterpret_cast<const __half2 *>(&lw[w]));
+                  float x0 = (h2.x + l2.x) * inv, x1 = (h2.y + l2.y) * inv;
+                  over |= !(fabsf(x0) <= 65504.f) || !(fabsf(x1) <= 65504.f);
+                  x0 = fminf(fmaxf(x0, -65504.f), 65504.f), x1 = fminf(fmaxf(x1, -65504.f), 65504.f);
+                  const __half2 hh = __floats2half2_rn(x0, x1);
+                  const float2 hf = __half22float2(hh);
+                  const __half2 ll = __floats2half2_rn(x0 - hf.x, x1 - hf.y);
+                  hi[w] = *reinterpret_cast<const uint32_t *>(&hh);
+                  lo[w] = *reinterpret_cast<const uint32_t *>(&ll);
+                }
+                sts16(ft + tile_at<128>(l, i + k), hi[0], hi[1], hi[2], hi[3]);
+                sts16(ft + tile_at<128>(l, p.rpb / 8 + i + k), lo[0], lo[1], lo[2], lo[3]);
+              }
+            }
+            if (over) atomicOr(a.flags, kFlagRange);
+          }
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(&c.q_full);
+      }
+      uint4 raw[CPR];
+      uint32_t sc[E4M3 ? CPR : 1];
+      auto load = [&](int i, int pg, int j) {  // rows behind the last key read what lies there and are cleared below
+        const long long pr = pool_row(a, pg, h, j, row0 + i * stride);
+        raw[i] = __ldg(reinterpret_cast<const uint4 *>(pool + pr * rb + at));
+        if (E4M3) sc[E4M3 ? i : 0] = __ldg(scales + pr);
+      };
+#pragma unroll
+      for (int i = 0; i < CPR; ++i)
+        if (i < mine) load(i, pages.now, g.k0 * kTileKeys);
+      for (int kt = g.k0; kt < g.k1; ++kt, ++tile) {
+        const int j0 = kt * kTileKeys, left = s.len - j0;
+        const bool tail = j0 + kTileKeys > s.prefix;
+        const unsigned alive = pages.alive(a);
+        const int slot = slots == 2 ? int(tile & 1u) : 0;
+        const uint32_t dst = dst0 + slot * kTile;
+        if (tile >= unsigned(slots)) wait_for(&empty[slot], (slots == 2 ? (tile >> 1) - 1 : tile - 1) & 1u, abort);
+        if (!is_v) {
+          if (l == 0) c.alive[tile & 3] = alive;
+          if (alive != (1u << kGroups) - 1u && l == 0) atomicOr(a.flags, kFlagRange);
+          if constexpr (BIAS != 0) {
+            const int hk = a.fk_heads > 1 ? h : 0;
+            const bool plain = j0 + kTileKeys <= min(s.prefix, a.P);  // positions are j0, j0 + 1, ...
+            auto position = [&](int row) {
+              const int j = j0 + row;
+              if (plain) return j;
+              if (j >= s.len) return 0;
+              if (j >= s.prefix) return new_position(a, g.b, s, j - s.prefix);
+              if (j < a.P) return j;
+              atomicOr(a.flags, kFlagRange);
+              return a.P - 1;
             };
-            if (plain && 128 % groups == 0) {  // 128 threads are whole rows: a step is 128 / groups rows on
-              const int row = l / groups, q = l % groups, rows = 128 / groups;
-              const uint4 *src = fbase + (long long)j0 * groups + l;
-#pragma unroll 4
-              for (int i = 0; i < groups; ++i) copy(src + i * 128, tile_at(row + i * rows, q >> 1) + (q & 1) * 8);
+            if constexpr (BIAS == 1) {
+              if (l < kTileKeys) {
+                const float4 f = __ldg(static_cast<const float4 *>(a.fk) + (long long)hk * a.P + position(l));
+                float(*pl)[kTileKeys] = planes[tile & 3];
+                pl[0][l] = f.x, pl[1][l] = f.y, pl[2][l] = f.z, pl[3][l] = f.w;
+              }
             } else {
+              // The keys' factors, (4 hi, 4 lo) groups of 16 bytes, go to the hi and lo columns of the slot's factor tile
+              // by asynchronous copies of 8 bytes.
+              const uint32_t ft = base + p.fk + slot * fk_tile;
+              const int groups = a.RP / 4, total = kTileKeys * groups;
+              const uint4 *fbase = static_cast<const uint4 *>(a.fk) + (long long)hk * a.P * groups;
+              int row = l / groups, q = l - row * groups;
+              const int rstep = 128 / groups, qstep = 128 - rstep * groups;
 #pragma unroll 1
               for (int e = l; e < total; e += 128) {
-                const int row = e / groups, q = e - row * groups;
-                copy(fbase + (long long)position(row) * groups + q, tile_at(row, q >> 1) + (q & 1) * 8);
+                const uint4 *src = fbase + (long long)position(row) * groups + q;
+                const uint32_t hi = tile_at<kTileKeys>(row, q >> 1) + (q & 1) * 8;
+                // lo columns: four chunks on in the same 64 columns, or in the blocks behind the hi ones
+                const uint32_t lo = p.rpb == 32 ? hi ^ 64u : hi + (p.rpb >> 6) * (kTileKeys * 128);
+                copy_whole<2>(ft + hi, src);
+                copy_whole<2>(ft + lo, reinterpret_cast<const uint2 *>(src) + 1);
+                row += rstep, q += qstep;
+                if (q >= groups) q -= groups, ++row;
               }
             }
           }
-          const int left = s.len - j0;  // keys from here on
-#pragma unroll
-          for (int i = 0; i < CPR; ++i) {
-            const int row = row0 + i * (128 / CPR);
-            uint4 was = raw[i];
-            if (!inside || row >= left || !((alive >> (row >> 4)) & 1u)) was = make_uint4(0u, 0u, 0u, 0u);
-            convert(was, sc[E4M3 ? i : 0], raw[i], more[E4M3 ? i : 0]);
-          }
-          if (!early) wait_empty();
-#pragma unroll
-          for (int i = 0; i < CPR; ++i) {
-            const uint32_t to = dst + i * (128 / CPR) * 128;  // whole groups of eight rows on: the swizzle is the same
-            sts16(to + at0, raw[i].x, raw[i].y, raw[i].z, raw[i].w);
-            if constexpr (E4M3) sts16(to + at1, more[i].x, more[i].y, more[i].z, more[i].w);
-          }
-          if (l == 0) c.alive[tile & 3] = alive;
-          if constexpr (BIAS == 1) {
-            float(*pl)[kTileKeys] = planes[tile & 3];
-            pl[0][l] = __uint_as_float(f.x), pl[1][l] = __uint_as_float(f.y);
-            pl[2][l] = __uint_as_float(f.z), pl[3][l] = __uint_as_float(f.w);
-          }
-          if constexpr (BIAS == 2) copies_wait_all();
-          fence_proxy_async_smem();
-          mbar_arrive(&c.k_full[slot]);
         }
-      }
-    } else {
-      const int l = threadIdx.x - kVWarp * 32;
-      // chunk i of this thread: 16 bytes at ch of row row0 + i * kStep; the last ones of some threads do not exist
-      constexpr int kStep = kVThreads / CPR, kMine = (128 + kStep - 1) / kStep;
-      constexpr int kPart = CPR == 16 ? 6 : (CPR == 8 ? 4 : 3), kParts = (kMine + kPart - 1) / kPart;
-      const int ch = l % CPR, row0 = l / CPR;
-      const bool inside = ch * 16 < rb;
-      while (walk.next(a, g)) {
-        const Seq &s = g.s;
-        const int h = g.item / a.chunks;
-        pages.start(a, g.b, g.k0 * kTileKeys, s.len, lane);
-        for (int kt = g.k0; kt < g.k1; ++kt, ++tile) {
-          const int j0 = kt * kTileKeys, left = s.len - j0;
-          const bool tail = j0 + kTileKeys > s.prefix;
-          const unsigned alive = pages.step(a, g.b, j0, s.len, lane);
-          const int slot = p.vs == 2 ? int(tile & 1u) : 0;
-          const uint32_t dst = base + p.v + slot * kTile;
-          // three or four chunks at a time, the next ones' loads under way meanwhile
-          uint4 raw[2][kPart];
-          uint32_t sc[2][E4M3 ? kPart : 1];
-          auto load = [&](int part, uint4 *x, uint32_t *scale) {
+        const bool more = kt + 1 < g.k1;
 #pragma unroll
-            for (int i = 0; i < kPart; ++i) {
-              const long long pr = pages.pool_row(a, h, j0, min(row0 + (part * kPart + i) * kStep, 127));
-              x[i] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(a.vp) + pr * rb + (inside ? ch * 16 : 0)));
-              if (E4M3) scale[E4M3 ? i : 0] = __ldg(a.vs + pr);
-            }
-          };
-          load(0, raw[0], sc[0]);
-          if (tile >= unsigned(p.vs)) wait_for(&c.v_empty[slot], (p.vs == 2 ? (tile >> 1) - 1 : tile - 1) & 1u, abort);
-          bool odd = false;
-#pragma unroll 1
-          for (int part = 0; part < kParts; ++part) {
-            load(min(part + 1, kParts - 1), raw[1], sc[1]);
-#pragma unroll
-            for (int i = 0; i < kPart; ++i) {
-              const int row = row0 + (part * kPart + i) * kStep;
-              uint4 was = raw[0][i], out[2];
-              if (!inside || row >= left || !((alive >> ((row >> 4) & 7)) & 1u)) was = make_uint4(0u, 0u, 0u, 0u);
-              convert(was, sc[0][E4M3 ? i : 0], out[0], out[1]);
-              if (tail) odd |= clear_odd<E4M3 ? 8 : 4>(reinterpret_cast<uint32_t *>(out));
-              if (row < 128) store(dst, row, ch, out[0], out[1]);
-            }
-#pragma unroll
-            for (int i = 0; i < kPart; ++i) {
-              raw[0][i] = raw[1][i];
-              if (E4M3) sc[0][E4M3 ? i : 0] = sc[1][E4M3 ? i : 0];
-            }
+        for (int i = 0; i < CPR; ++i) {
+          if (i >= mine) break;
+          const int row = row0 + i * stride;
+          const uint4 was = raw[i];
+          Chunks out;
+          out.x = out.y = was;
+          if constexpr (E4M3) {
+            // 2^(byte - 127); byte 255 is NaN, byte 0 (2^-127, which cache_write does not make) counts as 0
+            const uint32_t byte = sc[E4M3 ? i : 0];
+            const float f = __uint_as_float(byte == 255u ? 0x7fffffffu : byte << 23);
+            out.x = make_uint4(e4m3_to_bf16(was.x, false, f), e4m3_to_bf16(was.x, true, f),
+                               e4m3_to_bf16(was.y, false, f), e4m3_to_bf16(was.y, true, f));
+            out.y = make_uint4(e4m3_to_bf16(was.z, false, f), e4m3_to_bf16(was.z, true, f),
+                               e4m3_to_bf16(was.w, false, f), e4m3_to_bf16(was.w, true, f));
           }
-          if (odd) c.odd[tile & 7] = int(tile) + 1;
-          fence_proxy_async_smem();
-          mbar_arrive(&c.v_full[slot]);
+          if (more) load(i, pages.next, j0 + kTileKeys);
+          if (!inside || row >= left || !((alive >> (row >> 4)) & 1u)) out.x = out.y = make_uint4(0u, 0u, 0u, 0u);
+          if (__builtin_expect(is_v && tail, 0)) out = clear_odd(out, &c.odd[tile & 7], int(tile) + 1);
+          const uint32_t to = dst + tile_at<kTileKeys>(row, E4M3 ? 2 * ch : ch);
+          sts16(to, out.x.x, out.x.y, out.x.z, out.x.w);
+          if constexpr (E4M3) sts16(to ^ 16u, out.y.x, out.y.y, out.y.z, out.y.w);  // the next chunk, an odd one
         }
+        pages.now = pages.next;
+        pages.next = pages.fetch(a, g.b, j0 + 2 * kTileKeys, s.len, lane);
+        if (BIAS == 2 && !is_v) copies_wait_all();
+        fence_proxy_async_smem();
+        mbar_arrive(&full[slot]);
       }
     }
   } else {
     // ---------------------------------------------------------- MMA issuer
-    // One lane issues: its instructions need no election and no predicates.
-    constexpr uint32_t kQK = make_idesc_f16(true, true, 128, 128, false);
-    constexpr uint32_t kF = make_idesc_f16(false, false, 128, 128, false);
+    // One lane issues. The tensor cores take 48 clocks a product and wait for whatever it does between two: a loop that
+    // finds each step's addresses anew took 133, without anything else running, so four steps at a time are unrolled,
+    // with immediate offsets, and the slots are counters that run on. Both streams share one copy of the code.
+    constexpr uint32_t kQK = make_idesc_f16(true, true, 128, kTileKeys, false);
+    constexpr uint32_t kF = make_idesc_f16(false, false, 128, kTileKeys, false);
     constexpr uint32_t kPV = make_idesc_f16(true, true, 128, DP, true);
-    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-    unsigned done = 0;
-    uint32_t qphase = 0, pphase[2] = {0, 0};
+    const uint32_t q0 = low_k(base + p.q), fq0 = low_k(base + p.fq), k0 = low_k(base + p.k), fk0 = low_k(base + p.fk);
+    const uint32_t v0 = low_v(base + p.v);
+    const uint32_t fq_low = BIAS == 2 ? step_k<128>(p.rpb / 16) : 0u, fk_low = BIAS == 2 ? step_k<kTileKeys>(p.rpb / 16) : 0u;
+    const bool split = p.split, ks2 = p.ks == 2, vs2 = p.vs == 2;
+    const int factor_steps = BIAS == 2 ? a.RP / 16 : 0;
+    unsigned ktile = 0, vtile = 0;  // tiles whose K and V the products to come read
+    uint32_t qphase = 0, pphase = 0;  // bit t of pphase: stream t's
     while (lane == 0 && walk.next(a, g)) {
       const int n = g.k1 - g.k0, h = g.item / a.chunks;
       const int rows = min(p.tiles * 128, a.rows - (g.item - h * a.chunks) * p.tiles * 128);
       const int n0 = steps_of(0, n, rows), n1 = nstreams == 2 ? steps_of(1, n, rows) : 0;
+      const bool alone = split || n1 == 0;  // a tile is one stream's
       wait_for(&c.q_full, qphase & 1u, abort);
       ++qphase;
-      auto score = [&](int t, int i) {
-        const unsigned tile = done + unsigned(p.split ? 2 * i + t : i);
-        const int slot = p.ks == 2 ? int(tile & 1u) : 0;
-        if (t == 0 || p.split) wait_for(&c.k_full[slot], (p.ks == 2 ? tile >> 1 : tile) & 1u, abort);
+      auto score = [&](uint32_t t) {
+        const uint32_t slot = ks2 ? ktile & 1u : 0u;
+        if (t == 0 || split) wait_for(&c.k_full[slot], (ks2 ? ktile >> 1 : ktile) & 1u, abort);
         tc_fence_after();
-        const uint32_t d = (tm + 128u * t);
-        const int rt = p.split ? 0 : t;
-        const uint32_t q = (base + p.q + rt * kTile) >> 4, k = (base + p.k + slot * kTile) >> 4;
+        const uint32_t d = tmem + 128u * t, row_tile = t == 1 && !split ? 1u : 0u;
+        uint32_t k = k0 + slot * (kTile >> 4), q = q0 + row_tile * (kQTile >> 4);
 #pragma unroll 1
-        for (int kk = 0; kk < DP / 16; ++kk)
-          mma_ss_one(d, desc_k(q + step_k(kk)), desc_k(k + step_k(kk)), kQK, kk > 0 ? 1u : 0u);
+        for (uint32_t more = 0; more < DP / 64; ++more) {  // 64 columns, four products
+          mma_ss_one(d, desc(q), desc(k), kQK, more);
+#pragma unroll
+          for (int kk = 1; kk < 4; ++kk) mma_ss_one(d, desc(q + 2 * kk), desc(k + 2 * kk), kQK, 1u);
+          q += 128 * 128 >> 4, k += kTileKeys * 128 >> 4;
+        }
         if constexpr (BIAS == 2) {
-          const uint32_t fq = (base + p.fq + rt * fq_tile) >> 4;
-          const uint32_t fk = (base + p.fk + (p.fs == 2 ? tile & 1u : 0u) * fk_tile) >> 4;
-          const uint32_t fql = fq + step_k(p.rpb / 16), fkl = fk + step_k(p.rpb / 16);
+          uint32_t fq = fq0 + row_tile * (fq_tile >> 4), fk = fk0 + slot * (fk_tile >> 4);
 #pragma unroll 1
-          for (int kk = 0; kk < a.RP / 16; ++kk) {
-            const uint32_t step = step_k(kk);
-            mma_ss_one(d, desc_k(fq + step), desc_k(fk + step), kF, 1u);
-            mma_ss_one(d, desc_k(fql + step), desc_k(fk + step), kF, 1u);
-            mma_ss_one(d, desc_k(fq + step), desc_k(fkl + step), kF, 1u);
+          for (int kk = 0; kk < factor_steps; ++kk) {
+            mma_ss_one(d, desc(fq), desc(fk), kF, 1u);
+            mma_ss_one(d, desc(fq + fq_low), desc(fk), kF, 1u);
+            mma_ss_one(d, desc(fq), desc(fk + fk_low), kF, 1u);
+            fq += kk == 3 ? (128 * 128 >> 4) - 6 : 2, fk += kk == 3 ? (kTileKeys * 128 >> 4) - 6 : 2;
           }
         }
         tc_commit(&c.s_full[t]);
-        if (p.split || n1 == 0 || t == 1) tc_commit(&c.k_empty[slot]);
+        if (alone || t == 1) {
+          tc_commit(&c.k_empty[slot]);
+          ++ktile;
+        }
       };
-      auto product = [&](int t, int i, bool final) {
-        const unsigned tile = done + unsigned(p.split ? 2 * i + t : i);
-        const int slot = p.vs == 2 ? int(tile & 1u) : 0;
-        wait_for(&c.v_full[slot], (p.vs == 2 ? tile >> 1 : tile) & 1u, abort);
-        wait_for(&c.p_full[t], pphase[t] & 1u, abort);
-        ++pphase[t];
+      auto product = [&](uint32_t t, bool first, bool final) {
+        const uint32_t slot = vs2 ? vtile & 1u : 0u;
+        if (t == 0 || split) wait_for(&c.v_full[slot], (vs2 ? vtile >> 1 : vtile) & 1u, abort);
+        wait_for(&c.p_full[t], (pphase >> t) & 1u, abort);
+        pphase ^= 1u << t;
         tc_fence_after();
-        const uint32_t d = (tm + 256u + 128u * t), pt = (tm + 128u * t);
-        const uint32_t v = ((base + p.v + slot * kTile) >> 4), more = (i > 0 ? 1u : 0u);
-#pragma unroll 1
-        for (int kk = 0; kk < kTileKeys / 16; ++kk)
-          mma_ts_one(d, pt + uint32_t(kk * 8), desc_v(v + step_v(kk)), kPV, kk > 0 ? 1u : more);
-        if (p.split || n1 == 0 || t == 1) tc_commit(&c.v_empty[slot]);
+        const uint32_t d = tmem + 256u + 128u * t, pt = tmem + 128u * t, v = v0 + slot * (kTile >> 4);
+        mma_ts_one(d, pt, desc(v), kPV, first ? 0u : 1u);
+#pragma unroll
+        for (int kk = 1; kk < kTileKeys / 16; ++kk) mma_ts_one(d, pt + uint32_t(kk * 8), desc(v + step_v(kk)), kPV, 1u);
+        if (alone || t == 1) {
+          tc_commit(&c.v_empty[slot]);
+          ++vtile;
+        }
         if (final) tc_commit(&c.o_final[t]);
       };
-      // S_0(0), S_1(0), PV_0(0), S_0(1), PV_1(0), S_1(1), PV_0(1), ...: one place in the code for each
+      // S_0(0), S_1(0), PV_0(0), S_0(1), PV_1(0), S_1(1), PV_0(1), ...
 #pragma unroll 1
       for (int half = 0; half <= 2 * n0; ++half) {
-        const int t = half & 1, i = half >> 1, pt = 1 - t, pi = t ? i : i - 1;
-        if (i < (t ? n1 : n0)) score(t, i);
-        const int pn = pt ? n1 : n0;
-        if (pi >= 0 && pi < pn) product(pt, pi, pi == pn - 1);
+        const uint32_t t = half & 1;
+        const int i = half >> 1, pi = t ? i : i - 1, pn = t ? n0 : n1;
+        if (i < (t ? n1 : n0)) score(t);
+        if (pi >= 0 && pi < pn) product(1 - t, pi == 0, pi == pn - 1);
       }
-      done += n;
     }
     if (lane == 0) {
       tc_commit(&c.drain);
@@ -778,22 +766,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const __gr
 TilePlan make_plan(int d, int R, int rows) {
   const int DP = d <= 64 ? 64 : 128;
   const int RP = (R + 15) / 16 * 16;
-  const uint32_t tile = kTileKeys * DP * 2;
+  const uint32_t tile = kTileKeys * DP * 2, qtile = 128 * DP * 2;
   TilePlan best{};
-  // One or two row tiles, then K, V and factor slots. One K slot costs less than one V slot: K is stored ready-made.
-  static const int kOptions[8][4] = {{2, 2, 2, 2}, {2, 1, 2, 2}, {2, 1, 1, 2}, {2, 1, 1, 1},
-                                     {1, 2, 2, 2}, {1, 1, 2, 2}, {1, 1, 2, 1}, {1, 1, 1, 1}};
+  // One or two row tiles, then slots of K and of V.
+  static const int kOptions[8][3] = {{2, 2, 2}, {2, 1, 2}, {2, 2, 1}, {2, 1, 1}, {1, 2, 2}, {1, 1, 2}, {1, 2, 1}, {1, 1, 1}};
   for (const auto &o : kOptions) {
     TilePlan p{};
-    p.tiles = o[0], p.ks = o[1], p.vs = o[2], p.fs = o[3];
+    p.tiles = o[0], p.ks = o[1], p.vs = o[2];
     if (p.tiles == 2 && rows <= 128) continue;
     p.rpb = R <= kCacheBiasExact ? 0 : (RP <= 32 ? 32 : (RP <= 64 ? 64 : 128));
     const uint32_t f = kTileKeys * 4 * p.rpb;
     p.q = 0;
-    p.fq = p.q + p.tiles * tile;
-    p.k = p.fq + p.tiles * f;
+    p.fq = p.q + p.tiles * qtile;
+    p.k = p.fq + p.tiles * 128 * 4 * p.rpb;
     p.fk = p.k + p.ks * tile;
-    p.v = p.fk + p.fs * f;
+    p.v = p.fk + p.ks * f;
     p.planes = p.v + p.vs * tile;
     p.ctrl = p.planes + (R > 0 && R <= kCacheBiasExact ? 4 * 4 * kTileKeys * 4 : 0);
     p.smem = p.ctrl + uint32_t(sizeof(Ctrl)) + 1024;
