@@ -368,64 +368,45 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const __gr
       const bool whole = g.k0 == 0 && g.k1 == g.blocks;
       float *mine = a.part + (2ll * blockIdx.x + (g.k0 == 0)) * kSlot;
       if (!busy) nat = -INFINITY, l = 0.f;
-      // stream 1 of a split: its part to rows 128 .. 255 of the slot; stream 0 joins it
-      if (p.split && t == 1) {
-        const int at = 128 + row;
-        mine[DP * 256 + at] = nat, mine[(DP + 1) * 256 + at] = l;
-        if (steps > 0 && busy) {
+      // A row tile whose keys are all here leaves straight away. Else each stream puts its part (O, maximum, sum) into
+      // this CTA's slot, rows 128 and up for stream 1 of a split, and the item's last CTA joins the parts in order.
+      const bool direct = whole && !p.split;
+      bool any_odd = odd;
+      if (p.split) {  // stream 0 adds what left the products of either
+        if (odd) c.seg_odd[seg & 1] = seg + 1;
+        named_bar_sync(1, 256);
+        any_odd = t == 0 && c.seg_odd[seg & 1] == seg + 1;
+      }
+      if (t < nstreams) {
+        const bool none = tok < 0 || nat == -INFINITY;
+        const int at = p.split ? t * 128 + row : r;
+        if (!direct)
+          mine[DP * 256 + at] = nat, mine[(DP + 1) * 256 + at] = l;
+        else if (have)
+          a.LSE[qrow] = none ? -INFINITY : nat + logf(l);
+        const float inv = none ? 0.f : 1.f / l;
+        const int odd0 = max(g.k0 * kTileKeys, s.prefix / kTileKeys * kTileKeys), odd1 = min(s.len, g.k1 * kTileKeys);
+        const bool real = steps > 0 && busy;  // uniform over the warp; other parts have a maximum of -inf and no O
+        if (real || direct) {
 #pragma unroll 1
           for (int q = 0; q < DP / 32; ++q) {
             uint32_t x[32];
-            tmem_ld32(o_tm + 32u * q, x);
-            tmem_ld_wait32(x);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) mine[(32 * q + k) * 256 + at] = __uint_as_float(x[k]);
-          }
-        }
-      }
-      if (odd) c.seg_odd[seg & 1] = seg + 1;
-      named_bar_sync(1, 256);
-      if (t < p.tiles) {
-        float f0 = 1.f, f1 = 0.f;
-        if (p.split) {
-          const float m1 = mine[DP * 256 + 128 + row], l1 = mine[(DP + 1) * 256 + 128 + row];
-          const float top = fmaxf(nat, m1);
-          f0 = nat == -INFINITY ? 0.f : ex2_approx((nat - top) * kCacheLog2e);
-          f1 = m1 == -INFINITY ? 0.f : ex2_approx((m1 - top) * kCacheLog2e);
-          l = l * f0 + l1 * f1;
-          nat = top;
-        }
-        const bool none = tok < 0 || nat == -INFINITY;
-        if (have && whole) a.LSE[qrow] = none ? -INFINITY : nat + logf(l);
-        if (!whole) mine[DP * 256 + r] = nat, mine[(DP + 1) * 256 + r] = l;
-        const bool any_odd = c.seg_odd[seg & 1] == seg + 1;
-        const float inv = none ? 0.f : 1.f / l;
-        const int odd0 = max(g.k0 * kTileKeys, s.prefix / kTileKeys * kTileKeys), odd1 = min(s.len, g.k1 * kTileKeys);
-#pragma unroll 1
-        for (int q = 0; q < DP / 32; ++q) {
-          uint32_t x[32];
-#pragma unroll
-          for (int k = 0; k < 32; ++k) x[k] = 0u;
-          if (steps > 0 && busy) {  // uniform over the warp
-            tmem_ld32(o_tm + 32u * q, x);
-            tmem_ld_wait32(x);
-          }
-          if (p.split) {
-#pragma unroll
-            for (int k = 0; k < 32; ++k) {
-              float v = f0 == 0.f ? 0.f : __uint_as_float(x[k]) * f0;
-              if (f1 != 0.f) v = fmaf(mine[(32 * q + k) * 256 + 128 + row], f1, v);
-              x[k] = __float_as_uint(v);
+            for (int k = 0; k < 32; ++k) x[k] = 0u;
+            if (real) {
+              tmem_ld32(o_tm + 32u * q, x);
+              tmem_ld_wait32(x);
             }
-          }
-          if (any_odd && tok >= 0) {
+            if (__builtin_expect(any_odd && tok >= 0, 0)) {
 #pragma unroll
-            for (int k = 0; k < 32; ++k)
-              if (32 * q + k < a.d)
-                x[k] = __float_as_uint(__uint_as_float(x[k]) + odd_sum_of<E4M3>(a, s, g.b, h, tok, 32 * q + k, odd0, odd1));
-          }
-          if (whole) {
-            if (have) {
+              for (int k = 0; k < 32; ++k)
+                if (32 * q + k < a.d)
+                  x[k] = __float_as_uint(__uint_as_float(x[k]) + odd_sum_of<E4M3>(a, s, g.b, h, tok, 32 * q + k, odd0, odd1));
+            }
+            if (!direct) {
+#pragma unroll
+              for (int k = 0; k < 32; ++k) mine[(32 * q + k) * 256 + at] = __uint_as_float(x[k]);
+            } else if (have) {
               uint4 *o = reinterpret_cast<uint4 *>(a.O + qrow * a.d + 32 * q);
 #pragma unroll
               for (int k = 0; k < 32; k += 8) {
@@ -437,45 +418,57 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const __gr
                                         pack_bf16x2(y[6], y[7]));
               }
             }
-          } else {
-#pragma unroll
-            for (int k = 0; k < 32; ++k) mine[(32 * q + k) * 256 + r] = __uint_as_float(x[k]);
           }
         }
       }
-      if (!whole) {
-        const int c0 = walk.owner(g.start), c1 = walk.owner(g.start + g.blocks - 1);
+      if (!direct) {
         __threadfence();
         named_bar_sync(1, 256);
-        if (threadIdx.x == kSoftmaxWarp * 32) c.last = atomicAdd(a.counters + c0, 1u) == unsigned(c1 - c0);
-        named_bar_sync(1, 256);
-        if (c.last && t < p.tiles && have) {
-          __threadfence();
-          float top = -INFINITY;
-          for (int cc = c0; cc <= c1; ++cc) top = fmaxf(top, __ldcg(a.part + (2ll * cc + (cc == c0)) * kSlot + DP * 256 + r));
-          const bool none = tok < 0 || top == -INFINITY;
-          float sum = 0.f;
-          for (int cc = c0; cc <= c1; ++cc) {
-            const float *part = a.part + (2ll * cc + (cc == c0)) * kSlot;
-            const float mc = __ldcg(part + DP * 256 + r);
-            if (mc != -INFINITY) sum += __ldcg(part + (DP + 1) * 256 + r) * ex2_approx((mc - top) * kCacheLog2e);
+        int c0 = blockIdx.x, c1 = blockIdx.x;
+        bool last = true;
+        if (!whole) {
+          c0 = walk.owner(g.start), c1 = walk.owner(g.start + g.blocks - 1);
+          if (threadIdx.x == kSoftmaxWarp * 32) {
+            c.last = atomicAdd(a.counters + c0, 1u) == unsigned(c1 - c0);
+            if (c.last) a.counters[c0] = 0u;  // for the next call
           }
-          a.LSE[qrow] = none ? -INFINITY : top + logf(sum);
+          named_bar_sync(1, 256);
+          last = c.last;
+          if (last) __threadfence();
+        }
+        if (last && have && (p.split || t < p.tiles)) {
+          // part i: CTA c0 + i / halves, half i % halves; in a split the streams' warps take half of the columns each
+          const int halves = p.split ? 2 : 1, parts = (c1 - c0 + 1) * halves;
+          auto part = [&](int i) {
+            const int cc = c0 + (p.split ? i >> 1 : i);
+            return a.part + (2ll * cc + (cc == c0)) * kSlot + (p.split ? (i & 1) * 128 + row : r);
+          };
+          float top = -INFINITY, sum = 0.f;
+#pragma unroll 4
+          for (int i = 0; i < parts; ++i) {  // running maximum and sum
+            const float mc = __ldcg(part(i) + DP * 256), lc = __ldcg(part(i) + (DP + 1) * 256);
+            const float mn = fmaxf(top, mc), z = mn == -INFINITY ? 0.f : mn;
+            sum = sum * ex2_approx((top - z) * kCacheLog2e) + (mc == -INFINITY ? 0.f : lc * ex2_approx((mc - z) * kCacheLog2e));
+            top = mn;
+          }
+          const bool none = tok < 0 || top == -INFINITY;
+          if (!p.split || t == 0) a.LSE[qrow] = none ? -INFINITY : top + logf(sum);
           const float inv = none ? 0.f : 1.f / sum;
+          const int k0 = p.split ? t * (DP / 2) : 0, k1 = p.split ? k0 + DP / 2 : DP;
 #pragma unroll 1
-          for (int k = 0; k < a.d; k += 32) {  // 32 loads in flight; the columns past a head dim of 16 n exist in the slot
+          for (int k = k0; k < k1; k += 32) {  // 32 loads in flight
             float y[32];
 #pragma unroll
             for (int e = 0; e < 32; ++e) y[e] = 0.f;
             if (!none)
 #pragma unroll 1
-              for (int cc = c0; cc <= c1; ++cc) {
-                const float *part = a.part + (2ll * cc + (cc == c0)) * kSlot;
-                const float mc = __ldcg(part + DP * 256 + r);
+              for (int i = 0; i < parts; ++i) {
+                const float *x = part(i);
+                const float mc = __ldcg(x + DP * 256);
+                if (mc == -INFINITY) continue;  // its O was not written
                 float v[32];
 #pragma unroll
-                for (int e = 0; e < 32; ++e) v[e] = __ldcg(part + (k + e) * 256 + r);
-                if (mc == -INFINITY) continue;
+                for (int e = 0; e < 32; ++e) v[e] = __ldcg(x + (k + e) * 256);
                 const float f = ex2_approx((mc - top) * kCacheLog2e) * inv;
 #pragma unroll
                 for (int e = 0; e < 32; ++e) y[e] = fmaf(v[e], f, y[e]);
@@ -488,10 +481,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const __gr
                                       pack_bf16x2(y[e + 4], y[e + 5]), pack_bf16x2(y[e + 6], y[e + 7]));
           }
         }
-        named_bar_sync(1, 256);
-        if (threadIdx.x == kSoftmaxWarp * 32 && c.last) a.counters[c0] = 0u;  // for the next call
+        if (p.split) named_bar_sync(1, 256);  // the slot's parts have been read
       }
-      if (p.split) named_bar_sync(1, 256);  // stream 1's part has been read
     }
   } else if (warp != kIssuer) {
     // ------------------------------------------------------------- loaders
@@ -515,6 +506,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const __gr
       const int h = g.item / a.chunks;
       pages.now = pages.fetch(a, g.b, g.k0 * kTileKeys, s.len, lane);
       pages.next = pages.fetch(a, g.b, (g.k0 + 1) * kTileKeys, s.len, lane);
+      uint4 raw[CPR];
+      uint32_t sc[E4M3 ? CPR : 1];
+      auto load = [&](int i, int pg, int j) {  // rows behind the last key read what lies there and are cleared below
+        const long long pr = pool_row(a, pg, h, j, row0 + i * stride);
+        raw[i] = __ldg(reinterpret_cast<const uint4 *>(pool + pr * rb + at));
+        if (E4M3) sc[E4M3 ? i : 0] = __ldg(scales + pr);
+      };
+#pragma unroll
+      for (int i = 0; i < CPR; ++i)
+        if (i < mine) load(i, pages.now, g.k0 * kTileKeys);
       if (!is_v) {
         // ---- the query tiles, a thread per row, and their factors; their last readers are the S of all tiles so far
         for (unsigned n = 1; n <= unsigned(slots) && n <= tile; ++n)
@@ -579,16 +580,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const __gr
         fence_proxy_async_smem();
         mbar_arrive(&c.q_full);
       }
-      uint4 raw[CPR];
-      uint32_t sc[E4M3 ? CPR : 1];
-      auto load = [&](int i, int pg, int j) {  // rows behind the last key read what lies there and are cleared below
-        const long long pr = pool_row(a, pg, h, j, row0 + i * stride);
-        raw[i] = __ldg(reinterpret_cast<const uint4 *>(pool + pr * rb + at));
-        if (E4M3) sc[E4M3 ? i : 0] = __ldg(scales + pr);
-      };
-#pragma unroll
-      for (int i = 0; i < CPR; ++i)
-        if (i < mine) load(i, pages.now, g.k0 * kTileKeys);
       for (int kt = g.k0; kt < g.k1; ++kt, ++tile) {
         const int j0 = kt * kTileKeys, left = s.len - j0;
         const bool tail = j0 + kTileKeys > s.prefix;
@@ -623,18 +614,30 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const __gr
               const uint32_t ft = base + p.fk + slot * fk_tile;
               const int groups = a.RP / 4, total = kTileKeys * groups;
               const uint4 *fbase = static_cast<const uint4 *>(a.fk) + (long long)hk * a.P * groups;
+              // lo columns: four chunks on in the same 64 columns, or in the blocks behind the hi ones
+              const uint32_t lo_flip = p.rpb == 32 ? 64u : 0u, lo_skip = (p.rpb >> 6) * (kTileKeys * 128);
+              auto copy = [&](const uint4 *src, int row, int q) {
+                const uint32_t hi = ft + tile_at<kTileKeys>(row, q >> 1) + (q & 1) * 8;
+                copy_whole<2>(hi, src);
+                copy_whole<2>((hi ^ lo_flip) + lo_skip, reinterpret_cast<const uint2 *>(src) + 1);
+              };
               int row = l / groups, q = l - row * groups;
               const int rstep = 128 / groups, qstep = 128 - rstep * groups;
+              if (plain) {
+                const uint4 *src = fbase + (long long)j0 * groups + l;
 #pragma unroll 1
-              for (int e = l; e < total; e += 128) {
-                const uint4 *src = fbase + (long long)position(row) * groups + q;
-                const uint32_t hi = tile_at<kTileKeys>(row, q >> 1) + (q & 1) * 8;
-                // lo columns: four chunks on in the same 64 columns, or in the blocks behind the hi ones
-                const uint32_t lo = p.rpb == 32 ? hi ^ 64u : hi + (p.rpb >> 6) * (kTileKeys * 128);
-                copy_whole<2>(ft + hi, src);
-                copy_whole<2>(ft + lo, reinterpret_cast<const uint2 *>(src) + 1);
-                row += rstep, q += qstep;
-                if (q >= groups) q -= groups, ++row;
+                for (int e = l; e < total; e += 128) {
+                  copy(src, row, q);
+                  src += 128, row += rstep, q += qstep;
+                  if (q >= groups) q -= groups, ++row;
+                }
+              } else {
+#pragma unroll 1
+                for (int e = l; e < total; e += 128) {
+                  copy(fbase + (long long)position(row) * groups + q, row, q);
+                  row += rstep, q += qstep;
+                  if (q >= groups) q -= groups, ++row;
+                }
               }
             }
           }
