@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kWarps * 32, cta_per_sm(NB)) attn_cache_kernel
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
         // top = 1.m 2^(f - 127), 448 = 1.75 2^8
         const uint32_t bits = __float_as_uint(top);
-        const int e = int(bits >> 23) - 135 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
+        const int e = max(int(bits >> 23) - 135 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0), -126);
         const float down = pow2i(-e), up = pow2i(e);
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
@@ -684,7 +684,7 @@ __global__ void __launch_bounds__(kWarps * 32, cta_per_sm(NB)) attn_cache_kernel
       float sum = 0.f, val = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        if (join.m[w][row] == -INFINITY) continue;
+        if (saw_none(join.m[w][row], join.l[w][row])) continue;
         const float y = (join.m[w][row] - top) * kCacheLog2e;
         sum += join.l[w][row] * ex2_approx(y);
         val += join.o[w][row][dd] * ex2_approx(y + join.e[w][row]);
@@ -711,8 +711,8 @@ __global__ void __launch_bounds__(kWarps * 32, cta_per_sm(NB)) attn_cache_kernel
           for (int c = c0; c <= c1; ++c) {
             const float *p = a.part + (2ll * c + (c == c0)) * kSlot + row * (D + 2);
             const float mc = __ldcg(p + D);
-            if (mc == -INFINITY) continue;
             const float sc = __ldcg(p + D + 1), vc = __ldcg(p + dd);
+            if (saw_none(mc, sc)) continue;
             const float mn = fmaxf(top, mc);
             const float f0 = ex2_approx((top - mn) * kCacheLog2e), f1 = ex2_approx((mc - mn) * kCacheLog2e);
             sum = sum * f0 + sc * f1;

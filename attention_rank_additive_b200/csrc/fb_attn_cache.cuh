@@ -23,6 +23,7 @@ __device__ __forceinline__ void copy_whole(uint32_t dst, const void *src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(4 * N) : "memory");
 }
 __device__ __forceinline__ void copies_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 struct Seq {
   int prefix, count, len;
 };
@@ -96,14 +97,16 @@ __device__ __forceinline__ float odd_sum(const CacheAttnArgs &a, const Seq &s, i
   return sum;
 }
 
+// Whether a part of a row has seen no key. A maximum of -inf alone does not say so: it passes over NaN, which the sum keeps.
+__device__ __forceinline__ bool saw_none(float top, float sum) { return top == -INFINITY && sum == 0.f; }
+
 // Value dd of one output row, from the sums relative to exp(top); row t of a sequence that brings fewer tokens is 0.
 __device__ __forceinline__ void write_row(const CacheAttnArgs &a, const Seq &s, long long row, int t, int dd, float top,
                                           float sum, float val) {
-  const bool none = t >= s.count || top == -INFINITY;
+  const bool none = t >= s.count || saw_none(top, sum);
   if (dd < a.d) a.O[row * a.d + dd] = __float2bfloat16_rn(none ? 0.f : val / sum);
   if (dd == 0) a.LSE[row] = none ? -INFINITY : top + logf(sum);
 }
-
 
 // One CTA's part of an item (a sequence's rows of one key/value head): blocks k0 .. k1 - 1 of its `blocks`.
 struct Segment {

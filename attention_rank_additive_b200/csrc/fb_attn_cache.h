@@ -1,5 +1,5 @@
 // fb_attn_cache.h -- arguments of the attention over a paged cache, shared by
-// its kernels (fb_attn_cache*.cu) and the entry points (fb_cache_api.cu).
+// its kernels (fb_attn_cache*.cu) and the entry points (fb_cache_bias.cu).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -38,8 +38,7 @@ struct CacheAttnArgs {
 size_t cache_attn_part_floats(int d, int T, int G, int sms);
 cudaError_t launch_attn_cache(CacheAttnArgs a, int e4m3, int sms, cudaStream_t st);
 
-// The kernel for many: whether its tiles fit, and the same.
-bool cache_tile_fits(int d, int R, int rows);
+// The kernel for many: the same.
 size_t cache_tile_part_floats(int d, int sms);
 cudaError_t launch_attn_cache_tile(CacheAttnArgs a, int e4m3, int sms, cudaStream_t st);
 

@@ -46,7 +46,7 @@ constexpr float kRaise = 8.f;  // log2 units: O is rescaled when the maximum gro
 struct TilePlan {
   int tiles;  // row tiles of an item's chunk: 1 or 2
   int split;  // one row tile, its key tiles dealt to two streams
-  int ks, vs;  // slots of K and its factors, and of V
+  int ks;     // slots of K and its factors: 1 or 2 (V has two)
   int rpb;    // bias: columns reserved for the hi and for the lo parts (32, 64, 128), or 0
   uint32_t q, fq, k, fk, v, planes, ctrl;  // shared memory offsets from the 1024-byte aligned base
   uint32_t smem;
@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const __gr
         any_odd = t == 0 && c.seg_odd[seg & 1] == seg + 1;
       }
       if (t < nstreams) {
-        const bool none = tok < 0 || nat == -INFINITY;
+        const bool none = tok < 0 || saw_none(nat, l);
         const int at = p.split ? t * 128 + row : r;
         if (!direct)
           mine[DP * 256 + at] = nat, mine[(DP + 1) * 256 + at] = l;
@@ -448,10 +448,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const __gr
           for (int i = 0; i < parts; ++i) {  // running maximum and sum
             const float mc = __ldcg(part(i) + DP * 256), lc = __ldcg(part(i) + (DP + 1) * 256);
             const float mn = fmaxf(top, mc), z = mn == -INFINITY ? 0.f : mn;
-            sum = sum * ex2_approx((top - z) * kCacheLog2e) + (mc == -INFINITY ? 0.f : lc * ex2_approx((mc - z) * kCacheLog2e));
+            sum = sum * ex2_approx((top - z) * kCacheLog2e) + (saw_none(mc, lc) ? 0.f : lc * ex2_approx((mc - z) * kCacheLog2e));
             top = mn;
           }
-          const bool none = tok < 0 || top == -INFINITY;
+          const bool none = tok < 0 || saw_none(top, sum);
           if (!p.split || t == 0) a.LSE[qrow] = none ? -INFINITY : top + logf(sum);
           const float inv = none ? 0.f : 1.f / sum;
           const int k0 = p.split ? t * (DP / 2) : 0, k1 = p.split ? k0 + DP / 2 : DP;
@@ -465,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const __gr
               for (int i = 0; i < parts; ++i) {
                 const float *x = part(i);
                 const float mc = __ldcg(x + DP * 256);
-                if (mc == -INFINITY) continue;  // its O was not written
+                if (saw_none(mc, __ldcg(x + (DP + 1) * 256))) continue;  // its O was not written
                 float v[32];
 #pragma unroll
                 for (int e = 0; e < 32; ++e) v[e] = __ldcg(x + (k + e) * 256);
@@ -489,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const __gr
     const bool is_v = warp < kKWarp;
     const int l = is_v ? threadIdx.x - kVWarp * 32 : threadIdx.x - kKWarp * 32, threads = is_v ? kVThreads : 128;
     const uint8_t *pool = static_cast<const uint8_t *>(is_v ? a.vp : a.kp), *scales = is_v ? a.vs : a.ks;
-    const int slots = is_v ? p.vs : p.ks;
+    const int slots = is_v ? 2 : p.ks;
     const uint32_t dst0 = base + (is_v ? p.v : p.k);
     uint64_t *full = is_v ? c.v_full : c.k_full, *empty = is_v ? c.v_empty : c.k_empty;
     // This thread's chunks, 16 bytes of a pool row each, which become one (bf16) or two (e4m3) of the tile's: at ch of
@@ -684,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const __gr
     const uint32_t q0 = low_k(base + p.q), fq0 = low_k(base + p.fq), k0 = low_k(base + p.k), fk0 = low_k(base + p.fk);
     const uint32_t v0 = low_v(base + p.v);
     const uint32_t fq_low = BIAS == 2 ? step_k<128>(p.rpb / 16) : 0u, fk_low = BIAS == 2 ? step_k<kTileKeys>(p.rpb / 16) : 0u;
-    const bool split = p.split, ks2 = p.ks == 2, vs2 = p.vs == 2;
+    const bool split = p.split, ks2 = p.ks == 2;
     const int factor_steps = BIAS == 2 ? a.RP / 16 : 0;
     unsigned ktile = 0, vtile = 0;  // tiles whose K and V the products to come read
     uint32_t qphase = 0, pphase = 0;  // bit t of pphase: stream t's
@@ -725,8 +725,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const __gr
         }
       };
       auto product = [&](uint32_t t, bool first, bool final) {
-        const uint32_t slot = vs2 ? vtile & 1u : 0u;
-        if (t == 0 || split) wait_for(&c.v_full[slot], (vs2 ? vtile >> 1 : vtile) & 1u, abort);
+        const uint32_t slot = vtile & 1u;
+        if (t == 0 || split) wait_for(&c.v_full[slot], (vtile >> 1) & 1u, abort);
         wait_for(&c.p_full[t], (pphase >> t) & 1u, abort);
         pphase ^= 1u << t;
         tc_fence_after();
@@ -771,11 +771,12 @@ TilePlan make_plan(int d, int R, int rows) {
   const int RP = (R + 15) / 16 * 16;
   const uint32_t tile = kTileKeys * DP * 2, qtile = 128 * DP * 2;
   TilePlan best{};
-  // One or two row tiles, then slots of K and of V.
-  static const int kOptions[8][3] = {{2, 2, 2}, {2, 1, 2}, {2, 2, 1}, {2, 1, 1}, {1, 2, 2}, {1, 1, 2}, {1, 2, 1}, {1, 1, 1}};
+  // One or two row tiles, then slots of K. One of these fits at every head dim and rank: two row tiles up to rank 64
+  // (with one slot of K at head dim 128 and rank 64), and beyond it one, with one slot of K at head dim 128.
+  static const int kOptions[4][2] = {{2, 2}, {2, 1}, {1, 2}, {1, 1}};
   for (const auto &o : kOptions) {
     TilePlan p{};
-    p.tiles = o[0], p.ks = o[1], p.vs = o[2];
+    p.tiles = o[0], p.ks = o[1];
     if (p.tiles == 2 && rows <= 128) continue;
     p.rpb = R <= kCacheBiasExact ? 0 : (RP <= 32 ? 32 : (RP <= 64 ? 64 : 128));
     const uint32_t f = kTileKeys * 4 * p.rpb;
@@ -784,10 +785,10 @@ TilePlan make_plan(int d, int R, int rows) {
     p.k = p.fq + p.tiles * 128 * 4 * p.rpb;
     p.fk = p.k + p.ks * tile;
     p.v = p.fk + p.ks * f;
-    p.planes = p.v + p.vs * tile;
+    p.planes = p.v + 2 * tile;
     p.ctrl = p.planes + (R > 0 && R <= kCacheBiasExact ? 4 * 4 * kTileKeys * 4 : 0);
     p.smem = p.ctrl + uint32_t(sizeof(Ctrl)) + 1024;
-    p.split = p.tiles == 1 && p.ks == 2 && p.vs == 2;
+    p.split = p.tiles == 1 && p.ks == 2;
     if (p.smem <= 227u * 1024u) {
       best = p;
       break;
@@ -814,8 +815,6 @@ cudaError_t launch_tile(const CacheAttnArgs &a, const TilePlan &p, int grid, cud
 }
 
 }  // namespace
-
-bool cache_tile_fits(int d, int R, int rows) { return make_plan(d, R, rows).smem != 0; }
 
 size_t cache_tile_part_floats(int d, int sms) { return size_t(2) * sms * 256 * ((d <= 64 ? 64 : 128) + 2); }
 

@@ -219,9 +219,8 @@ int fb_attn_cache_fwd(int cache_dt, int B, int Hq, int H, int T, int d, const vo
     a.fk = base + size_t(phi_q_heads) * P * row;
   }
   a.flags = flags;
-  const bool tiles = a.rows > kTileRows && cache_tile_fits(d, R, a.rows);
-  const cudaError_t e = (tiles ? launch_attn_cache_tile : launch_attn_cache)(a, cache_dt == FB_E4M3, sm_count(),
-                                                                            static_cast<cudaStream_t>(stream));
+  const cudaError_t e = (a.rows > kTileRows ? launch_attn_cache_tile : launch_attn_cache)(
+      a, cache_dt == FB_E4M3, sm_count(), static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? FB_OK : FB_ERR_CUDA;
 }
 

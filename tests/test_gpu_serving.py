@@ -520,3 +520,101 @@ def test_decode_steps_agree_with_full_attention():
                 a, b, c = a[:, :, 0].double(), b[:, :, i].double(), c[:, :, N + i].double()
                 # all three round probabilities (2^-8 of weights that add up to 1, on values below 5) and O
                 assert (a - b).abs().max() <= 2.0 ** -6 and (a - c).abs().max() <= 2e-2
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("T,context", [(1, 0), (1, 5000), (6, 40), (40, 0), (40, 3000), (150, 90)])
+def test_nan_is_not_taken_for_a_row_without_keys(kind, T, context):
+    """A query with a NaN, and a context key with one, make their rows NaN (O and LSE), also where no other score of a
+    part of the row is finite; the other rows keep their results."""
+    c = _case(kind, 64, 2, 2, T, 16, [context, context], None, "none", False, seed=7)
+    clean = _call(c)
+    c["q"][0, 1, T - 1, 9] = math.nan
+    o, lse = _call(c)
+    assert o[0, 1, T - 1].isnan().all() and lse[0, 1, T - 1].isnan()
+    hit = torch.zeros(2, 2, T, dtype=torch.bool, device="cuda")
+    hit[0, 1, T - 1] = True
+    assert torch.equal(o[~hit], clean[0][~hit]) and torch.equal(lse[~hit], clean[1][~hit])
+    # new token 0's key in head 0 of sequence 1: all rows of that head see it
+    pool = c["cache"].k
+    at = int(c["table"][1, context // 16]), 0, context % 16, 3
+    if kind == "bf16":
+        pool[at] = math.nan
+    else:
+        pool.view(torch.uint8)[at] = 0x7F
+    o, lse = _call(c)
+    hit[1, 0] = True
+    assert o[hit].isnan().all() and lse[hit].isnan().all()
+    assert torch.equal(o[~hit], clean[0][~hit]) and torch.equal(lse[~hit], clean[1][~hit])
+    assert _status() == fb.FB_OK
+
+
+def test_smallest_queries_against_the_largest_scales():
+    """Queries near the least normal number with 8-bit keys whose scale is the largest: the products are ordinary."""
+    c = _case("e4m3", 64, 1, 1, 1, 16, [40], None, "none", False, seed=9)
+    c["q"] = (c["q"].float() * 2.0 ** -124).to(torch.bfloat16)
+    c["cache"].k_scale.view(torch.uint8).fill_(127 + 116)
+    _compare(_call(c), _want(c))
+
+
+def test_refusals():
+    c = _case("bf16", 64, 4, 2, 2, 16, [20], None, "low8", True)
+    cache, table, prefix, q = c["cache"], c["table"].cuda(), c["prefix"].cuda(), c["q"].cuda()
+    e4 = _cache(3, 2, 16, 64, "e4m3", 1)
+    ok = dict(tree_mask=c["mask"].cuda(), depths=c["depth"].cuda())
+    k = torch.zeros(1, 2, 3, 64, device="cuda", dtype=torch.bfloat16)
+    r = fb.Rope.scaled(64)
+    refused = [
+        lambda: fb.attn_cache(q.float(), cache, table, prefix, **ok),
+        lambda: fb.attn_cache(q.cpu(), cache, table, prefix, **ok),
+        lambda: fb.attn_cache(q[..., :32], cache, table, prefix, **ok),
+        lambda: fb.attn_cache(q.transpose(1, 2).contiguous().transpose(1, 2), cache, table, prefix, **ok),
+        lambda: fb.attn_cache(q, cache, table.long(), prefix, **ok),
+        lambda: fb.attn_cache(q, cache, table.expand(2, -1), prefix, **ok),
+        lambda: fb.attn_cache(q, cache, table, prefix.expand(2), **ok),
+        lambda: fb.attn_cache(q, cache, table, prefix.cpu(), **ok),
+        lambda: fb.attn_cache(q, cache, table, prefix, tree_mask=ok["tree_mask"][:, :1]),
+        lambda: fb.attn_cache(q, cache, table, prefix, tree_mask=ok["tree_mask"].float()),
+        lambda: fb.attn_cache(q, cache, table, prefix, depths=ok["depths"].cpu()),
+        lambda: fb.attn_cache(q, cache, table, prefix, out=torch.empty_like(q).float()),
+        lambda: fb.attn_cache(q, cache, table, prefix, lse=torch.empty(1, 4, 2, device="cuda", dtype=torch.bfloat16)),
+        lambda: fb.attn_cache(q, cache, table, prefix, workspace=torch.zeros(64, device="cuda")),
+        lambda: fb.cache_write(cache, k[:, :1], k[:, :1], table, prefix),
+        lambda: fb.cache_write(cache, k, k[:, :, :2], table, prefix),
+        lambda: fb.cache_write(cache, k, k.float(), table, prefix),
+        lambda: fb.cache_write(cache, k.half(), k.half(), table, prefix),
+        lambda: fb.cache_write(cache, k, k, table, None),
+        lambda: fb.cache_read(cache, table, None, None, 4, dtype=torch.float16),
+        lambda: fb.cache_read(cache, table, None, None, 4, out=(k, k)),
+        lambda: fb.PagedCache(cache.k, cache.v.transpose(2, 3)),
+        lambda: fb.PagedCache(cache.k, cache.v, torch.zeros(1, device="cuda"), torch.zeros(1, device="cuda")),
+        lambda: fb.PagedCache(e4.k, e4.v),
+        lambda: fb.PagedCache(e4.k, e4.v, e4.k_scale[:, :1], e4.v_scale),
+        lambda: fb.CacheBias(torch.zeros(1, 4, 8, device="cuda"), torch.zeros(1, 5, 8, device="cuda")),
+        lambda: fb.CacheBias(torch.zeros(1, 4, 8), torch.zeros(1, 4, 8)),
+        lambda: fb.rope(q.half(), None, r), lambda: fb.rope(q.cpu(), None, r), lambda: fb.rope(q, k, r),
+        lambda: fb.rope(q, None, r, positions=torch.zeros(3, dtype=torch.int32, device="cuda")),
+        lambda: fb.rope(q, None, r, positions=torch.zeros(2, device="cuda")),
+        lambda: fb.rope(q, None, r, out=(torch.empty_like(q)[..., :1].expand_as(q), None)),
+        lambda: fb.rope(q.transpose(2, 3), None, r),
+        lambda: fb.Rope([]), lambda: fb.Rope([1.0], factor=math.inf), lambda: fb.Rope.scaled(64, scaling="other"),
+        lambda: fb.cache_workspace(1, 3, 2, 1, 64),
+    ]
+    for i, call in enumerate(refused):
+        with pytest.raises(ValueError):
+            call()
+            pytest.fail(f"call {i} was not refused")
+    for call, status in (
+            (lambda: fb.attn_cache(q, cache, table, prefix, scale=0.0), fb.FB_ERR_INVALID_ARG),
+            (lambda: fb.attn_cache(q, cache, table, prefix, workspace=torch.zeros(256, device="cuda", dtype=torch.uint8)),
+             fb.FB_ERR_WORKSPACE),
+            (lambda: fb.cache_write(cache, torch.zeros(1, 2, 3, 65, device="cuda")[..., :64],
+                                    torch.zeros(1, 2, 3, 65, device="cuda")[..., :64], table, prefix),
+             fb.FB_ERR_UNSUPPORTED),
+            (lambda: fb.rope(q[:, :, :0], None, r), fb.FB_ERR_INVALID_ARG),
+            (lambda: fb.Rope([math.nan]), fb.FB_ERR_INVALID_ARG)):
+        with pytest.raises(fb.FlashBiasError) as e:
+            call()
+        assert e.value.status == status
+    torch.cuda.synchronize()
+    assert _status() == fb.FB_OK
