@@ -32,6 +32,7 @@
 #include <cuda_fp8.h>
 
 #include <algorithm>
+#include <climits>
 #include <cmath>
 #include <cstring>
 
@@ -44,11 +45,13 @@ namespace {
 constexpr int kWarps = 4;
 
 // 16-key groups that a warp takes in one step: two where rows are short, which gives its chains of dependent
-// instructions something to overlap with (one group a step: ALiBi decode step 130 us).
+// instructions something to overlap with.
 constexpr int groups_per_step(int D, bool E4M3, int NB) { return NB == 1 && D * (E4M3 ? 1 : 2) <= 128 ? 2 : 1; }
 
 // CTAs of 128 threads on an SM at most, by blocks of 8 query rows: the registers of O and Q allow no more.
-constexpr int cta_per_sm(int NB) { return NB == 1 ? 4 : (NB == 2 ? 3 : 2); }
+constexpr int cta_per_sm(int NB) { return NB == 1 ? 4 : 3; }
+// And what their rings leave room for (head dim 128 in 8 bits with two groups a step: three).
+constexpr int most_ctas(int D, bool E4M3, int NB) { return std::min(cta_per_sm(NB), D == 128 ? (E4M3 ? 3 : 2) : 4); }
 
 __device__ __forceinline__ void mma_bf16(float *c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
@@ -60,13 +63,6 @@ __device__ __forceinline__ void mma_bf16(float *c, uint32_t a0, uint32_t a1, uin
 __device__ __forceinline__ void mma_f16(float *c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-               "{%0,%1,%2,%3};"
-               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void mma_e4m3(float *c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
                "{%0,%1,%2,%3};"
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -105,11 +101,6 @@ __device__ __forceinline__ void read_words(const uint8_t *src, uint32_t *w) {
   }
 }
 
-__device__ __forceinline__ uint32_t e4m3_codes(const float *x) {
-  return __nv_cvt_float2_to_fp8x2(make_float2(x[0], x[1]), __NV_SATFINITE, __NV_E4M3) |
-         uint32_t(__nv_cvt_float2_to_fp8x2(make_float2(x[2], x[3]), __NV_SATFINITE, __NV_E4M3)) << 16;
-}
-
 // How a lane's share of a row lies, for head dims padded to D (32, 64, 96, 128).
 template <int D, bool E4M3>
 struct Lay {
@@ -146,27 +137,28 @@ struct Smem {
   int pad;
 };
 
-// A group in the ring: 16 rows of K, of V, 16 scale bytes of each (e4m3), 16 rows of factors; 16-byte multiples.
+// What a group takes in the ring: 16 rows of K, of V, 16 scale bytes of each (e4m3), 16 rows of factors. A slot holds a
+// step's groups, all of their K first, then V, the scales and the factors; 16-byte multiples.
 __host__ __device__ __forceinline__ int stage_bytes(int d, bool e4m3, int bias, int RP) {
   return 32 * d * (e4m3 ? 1 : 2) + (e4m3 ? 32 : 0) + (bias == 1 ? 256 : (bias == 2 ? 64 * RP : 0));
 }
 
 template <int D, bool E4M3, int NB, int BIAS>
-__global__ void __launch_bounds__(kWarps * 32, cta_per_sm(NB)) attn_cache_kernel(const __grid_constant__ CacheAttnArgs a, const int stages) {
+__global__ void __launch_bounds__(kWarps * 32, most_ctas(D, E4M3, NB)) attn_cache_kernel(const __grid_constant__ CacheAttnArgs a, const int stages) {
   using L = Lay<D, E4M3>;
   constexpr int KS = D / 16, ROWS = 8 * NB, KM = groups_per_step(D, E4M3, NB);
   constexpr int BK = 16 * KM * kWarps;  // a block of keys: a step of each warp
   extern __shared__ __align__(16) uint8_t smem_raw[];
   auto &sm = *reinterpret_cast<Smem<NB, BIAS> *>(smem_raw);
   auto &join = *reinterpret_cast<Join<D, NB> *>(smem_raw + sizeof(sm));
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
   griddep_wait();
 
   // ---- this CTA's run of blocks of all items
   Walk walk(a, BK, lane);
   if (blockIdx.x >= walk.ctas) return;
   if (threadIdx.x == 0) sm.abort = 0;
-  if (lane < stages) mbar_init(&sm.full[warp][lane], KM);
+  if (lane < stages) mbar_init(&sm.full[warp][lane], 1);
   fence_mbar_init();
   int slot = 0;         // of the next group to use
   uint32_t parity = 0;  // of its barrier
@@ -177,63 +169,44 @@ __global__ void __launch_bounds__(kWarps * 32, cta_per_sm(NB)) attn_cache_kernel
     const int h = seg.item / a.chunks, r0 = (seg.item - h * a.chunks) * ROWS;
     const long long qrow0 = ((long long)b * a.Hq + (long long)h * a.G) * a.T;  // row r of the item is output row qrow0 + r
 
-    // ---- queries as the matrix operand: lane (g, t4) holds row g's values at the d that its key loads have. For an
-    // 8-bit cache each row is a power of two times two e4m3 parts, hi + lo / 16: with the row's largest value in
-    // (224, 448] hi holds four bits of every value and lo the four that are left of a bf16, so the sum is exact, or
-    // off by 2^-23 of the largest value where lo is subnormal. The keys' codes then are operands as they are.
-    uint32_t qf[NB][KS][2];  // bf16 pairs; e4m3: [32 d][hi words], then [32 d][lo words]
+    // ---- queries as the matrix operand: lane (g, t4) holds row g's values at the d that its key loads have. 8-bit keys
+    // become fp16, exactly, and the queries too: a power of two is taken out of a row so that its largest value lies in
+    // [2^14, 2^15). Values from 2^-28 of that on are exact, smaller ones off by 2^-40 of it at most.
+    uint32_t qf[NB][KS][2];  // bf16 or fp16 pairs
     float mult[NB][2];       // scale, and the power of two taken out of a query row
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
       const int r = r0 + n * 8 + g;
       const bool in = r < a.rows;
       const __nv_bfloat16 *q = a.Q + (qrow0 + (in ? r : 0)) * a.d;
-      uint32_t u[KS][2];
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
         constexpr int per = L::KL * 4 / L::ES;  // values per load and lane
         const int d0 = (k * 4 / per) * (4 * per) + t4 * per + (k * 4) % per;
         uint2 v = make_uint2(0u, 0u);
         if (in && d0 < a.d) v = __ldg(reinterpret_cast<const uint2 *>(q + d0));
-        u[k][0] = v.x, u[k][1] = v.y;
+        qf[n][k][0] = v.x, qf[n][k][1] = v.y;
       }
       mult[n][0] = mult[n][1] = a.scale;
-      if constexpr (!E4M3) {
-#pragma unroll
-        for (int k = 0; k < KS; ++k) qf[n][k][0] = u[k][0], qf[n][k][1] = u[k][1];
-      } else {
+      if constexpr (E4M3) {
         float top = 0.f;
 #pragma unroll
         for (int k = 0; k < KS; ++k)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float x0 = fabsf(__uint_as_float(u[k][i] << 16)), x1 = fabsf(__uint_as_float(u[k][i] & 0xffff0000u));
+            const float x0 = fabsf(__uint_as_float(qf[n][k][i] << 16)), x1 = fabsf(__uint_as_float(qf[n][k][i] & 0xffff0000u));
             top = fmaxf(top, fmaxf(x0 < INFINITY ? x0 : 0.f, x1 < INFINITY ? x1 : 0.f));
           }
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // top = 1.m 2^(f - 127), 448 = 1.75 2^8
-        const uint32_t bits = __float_as_uint(top);
-        const int e = max(int(bits >> 23) - 135 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0), -126);
+        const int e = max(int(__float_as_uint(top) >> 23) - 141, -126);  // top = 1.m 2^(e + 14)
         const float down = pow2i(-e), up = pow2i(e);
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          float x[4] = {__uint_as_float(u[k][0] << 16), __uint_as_float(u[k][0] & 0xffff0000u),
-                        __uint_as_float(u[k][1] << 16), __uint_as_float(u[k][1] & 0xffff0000u)};
-          float lo[4];
+        for (int k = 0; k < KS; ++k)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            x[i] *= down;
-            if (!(fabsf(x[i]) < INFINITY)) x[i] = __uint_as_float(0x7fffffffu);
-          }
-          const uint32_t h = e4m3_codes(x);
-          const uint32_t l0 = e4m3_lo(h), l1 = e4m3_hi(h);
-          const float2 f0 = __half22float2(*reinterpret_cast<const __half2 *>(&l0));
-          const float2 f1 = __half22float2(*reinterpret_cast<const __half2 *>(&l1));
-          lo[0] = (x[0] - f0.x) * 16.f, lo[1] = (x[1] - f0.y) * 16.f, lo[2] = (x[2] - f1.x) * 16.f, lo[3] = (x[3] - f1.y) * 16.f;
-          qf[n][k / 2][k & 1] = h;
-          qf[n][KS / 2 + k / 2][k & 1] = e4m3_codes(lo);
-        }
+          for (int i = 0; i < 2; ++i)
+            qf[n][k][i] = pack_f16x2(__uint_as_float(qf[n][k][i] << 16) * down,
+                                     __uint_as_float(qf[n][k][i] & 0xffff0000u) * down);
         mult[n][0] *= __shfl_sync(0xffffffffu, up, t4 * 8);
         mult[n][1] *= __shfl_sync(0xffffffffu, up, t4 * 8 + 4);
       }
@@ -293,37 +266,53 @@ __global__ void __launch_bounds__(kWarps * 32, cta_per_sm(NB)) attn_cache_kernel
     const int jend = min(s.len, k1 * BK), jstart = k0 * BK + warp * 16 * KM;
     const int hk = BIAS ? (a.fk_heads > 1 ? h : 0) : 0;
     const int rb = a.d * L::ES;  // bytes of a row
-    const int group = stage_bytes(a.d, E4M3, BIAS, a.RP);  // of the ring: a group, of which a slot has KM
+    const int slot_bytes = KM * stage_bytes(a.d, E4M3, BIAS, a.RP);
+    const int v_at = KM * 16 * rb, ks_at = 2 * v_at, vs_at = ks_at + KM * 16, f_at = ks_at + (E4M3 ? KM * 32 : 0);
     const int fk_row = BIAS == 1 ? 16 : 4 * a.RP;
     const uint8_t *fk_head = static_cast<const uint8_t *>(a.fk) + (BIAS ? (long long)hk * a.P * fk_row : 0ll);
-    uint8_t *ring = smem_raw + sizeof(sm) + warp * stages * KM * group;
-    // the page of lane i's group (i < KM) of the step at j
+    uint8_t *ring = smem_raw + sizeof(sm) + warp * stages * slot_bytes;
+    // The page of lane i's group (i < KM) of the step at j, and one that is not there.
     auto page_of = [&](int j) {
       j += 16 * lane;
       return lane < KM && j < jend ? __ldg(table + (j >> a.page_shift)) : -1;
     };
     auto page_ok = [&](int page) { return page >= 0 && page < a.num_pages; };
-    // Fetch the step at j into ring slot `to`: lane i its group i.
+    // Fetch the step at j into ring slot `to`. What the copies take is the same in all lanes, found by reductions, which
+    // leave it in uniform registers: a copy by a lane with values of its own costs a loop over the lanes.
     auto fetch = [&](int j, int page, int to) {
-      if (j >= jend || lane >= KM) return;
-      uint64_t *bar = &sm.full[warp][to];
-      uint8_t *dst = ring + (to * KM + lane) * group;
-      j += 16 * lane;
-      if (!page_ok(page)) {
-        if (j < jend) atomicOr(a.flags, kFlagRange);
-        mbar_arrive(bar);
-        return;
+      if (j >= jend) return;
+      int pages[KM];
+      bool ok[KM];
+      int there = 0;
+#pragma unroll
+      for (int i = 0; i < KM; ++i) {
+        pages[i] = __reduce_max_sync(0xffffffffu, lane == i ? page : INT_MIN);
+        ok[i] = page_ok(pages[i]);
+        there += ok[i];
+        if (!ok[i] && j + 16 * i < jend && lane == 0) atomicOr(a.flags, kFlagRange);
       }
-      const long long prow = (((long long)page * a.H + h) << a.page_shift) + (j & ((1 << a.page_shift) - 1));
-      const bool factors = BIAS != 0 && j + 16 <= min(s.prefix, a.P);  // else read where they are used
-      mbar_arrive_expect_tx(bar, 32 * rb + (E4M3 ? 32 : 0) + (factors ? 16 * fk_row : 0));
-      bulk_load(dst, static_cast<const uint8_t *>(a.kp) + prow * rb, 16 * rb, bar);
-      bulk_load(dst + 16 * rb, static_cast<const uint8_t *>(a.vp) + prow * rb, 16 * rb, bar);
-      if constexpr (E4M3) {
-        bulk_load(dst + 32 * rb, a.ks + prow, 16, bar);
-        bulk_load(dst + 32 * rb + 16, a.vs + prow, 16, bar);
+      // the step's factors, where all are of the context; else they are read where they are used
+      const bool factors = BIAS != 0 && j + 16 * KM <= min(s.prefix, a.P);
+      const bool one = KM == 1 || (a.page_shift > 4 && there == KM);  // its groups are neighbours in one page
+      if (elect_one()) {
+        uint64_t *bar = &sm.full[warp][to];
+        uint8_t *dst = ring + to * slot_bytes;
+        mbar_arrive_expect_tx(bar, there * (32 * rb + (E4M3 ? 32 : 0)) + (factors ? KM * 16 * fk_row : 0));
+#pragma unroll
+        for (int i = 0; i < KM; ++i) {
+          if (!ok[i] || (one && i > 0)) continue;
+          const long long prow = (((long long)pages[i] * a.H + h) << a.page_shift) + ((j + 16 * i) & ((1 << a.page_shift) - 1));
+          const int rows = one ? 16 * KM : 16;
+          bulk_load(dst + 16 * i * rb, static_cast<const uint8_t *>(a.kp) + prow * rb, rows * rb, bar);
+          bulk_load(dst + v_at + 16 * i * rb, static_cast<const uint8_t *>(a.vp) + prow * rb, rows * rb, bar);
+          if constexpr (E4M3) {
+            bulk_load(dst + ks_at + 16 * i, a.ks + prow, rows, bar);
+            bulk_load(dst + vs_at + 16 * i, a.vs + prow, rows, bar);
+          }
+        }
+        if (factors) bulk_load(dst + f_at, fk_head + (long long)j * fk_row, KM * 16 * fk_row, bar);
       }
-      if (factors) bulk_load(dst + 32 * rb + (E4M3 ? 32 : 0), fk_head + (long long)j * fk_row, 16 * fk_row, bar);
+      __syncwarp();
     };
     // Lanes whose d lies past the row read its first bytes instead: the queries are 0 there, and O is not written.
     int kat[L::KW / L::KL], vat[L::VW / L::VL0 + (D == 96 ? 1 : 0)];
@@ -335,7 +324,7 @@ __global__ void __launch_bounds__(kWarps * 32, cta_per_sm(NB)) attn_cache_kernel
 #pragma unroll
     for (int c = 0; c < L::VW / L::VL0 + (D == 96 ? 1 : 0); ++c) {
       const int at = D == 96 && c == 1 ? 64 * L::ES + g * (L::VL0 * 2) : (c * 8 + g) * (L::VL0 * 4);
-      vat[c] = (16 + 2 * t4) * rb + (at < rb ? at : 0);
+      vat[c] = v_at + 2 * t4 * rb + (at < rb ? at : 0);
     }
     // page numbers one step ahead of their fetch
     int fill = slot;
@@ -351,44 +340,42 @@ __global__ void __launch_bounds__(kWarps * 32, cta_per_sm(NB)) attn_cache_kernel
       page_fill = page_of(j0 + stages * BK);
       const unsigned alive = __ballot_sync(0xffffffffu, page_ok(page_use));  // bit mb: group mb has a page
       page_use = page_of(j0 + BK);
-      mbar_wait_long(&sm.full[warp][slot], parity, &sm.abort);
-      const uint8_t *src = ring + slot * KM * group;
+      mbar_wait(&sm.full[warp][slot], parity, &sm.abort);
+      const uint8_t *src = ring + slot * slot_bytes;
       const bool tail = j0 + 16 * KM > s.prefix || alive != (1u << KM) - 1u;  // new tokens, rows past the end, or no page
 
       // ---- scores: S^T = K Q^T (16 keys x 8 rows per block)
       float x[KM][NB][4];
 #pragma unroll
       for (int mb = 0; mb < KM; ++mb) {
-        float xl[NB][4];
 #pragma unroll
         for (int n = 0; n < NB; ++n)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) x[mb][n][i] = xl[n][i] = 0.f;
+          for (int i = 0; i < 4; ++i) x[mb][n][i] = 0.f;
 #pragma unroll
         for (int c = 0; c < L::KW / L::KL; ++c) {
           uint32_t kr[2][L::KL];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) read_words<L::KL>(src + mb * group + 8 * i * rb + kat[c], kr[i]);
+          for (int i = 0; i < 2; ++i) read_words<L::KL>(src + (mb * 16 + 8 * i) * rb + kat[c], kr[i]);
+          // a product takes four values of each row: two words of bf16, or one word of codes
+          constexpr int products = E4M3 ? L::KL : L::KL / 2;
 #pragma unroll
-          for (int kk = 0; kk < L::KL / 2; ++kk) {
-            const int k = c * (L::KL / 2) + kk;
-            const uint32_t a0 = kr[0][2 * kk], a1 = kr[1][2 * kk], a2 = kr[0][2 * kk + 1], a3 = kr[1][2 * kk + 1];
+          for (int kk = 0; kk < products; ++kk) {
+            const int k = c * products + kk;
+            uint32_t a0, a1, a2, a3;
+            if constexpr (E4M3) {
+              a0 = e4m3_lo(kr[0][kk]), a1 = e4m3_lo(kr[1][kk]), a2 = e4m3_hi(kr[0][kk]), a3 = e4m3_hi(kr[1][kk]);
+            } else {
+              a0 = kr[0][2 * kk], a1 = kr[1][2 * kk], a2 = kr[0][2 * kk + 1], a3 = kr[1][2 * kk + 1];
+            }
 #pragma unroll
             for (int n = 0; n < NB; ++n) {
-              if constexpr (E4M3) {
-                mma_e4m3(x[mb][n], a0, a1, a2, a3, qf[n][k][0], qf[n][k][1]);
-                mma_e4m3(xl[n], a0, a1, a2, a3, qf[n][KS / 2 + k][0], qf[n][KS / 2 + k][1]);
-              } else {
+              if constexpr (E4M3)
+                mma_f16(x[mb][n], a0, a1, a2, a3, qf[n][k][0], qf[n][k][1]);
+              else
                 mma_bf16(x[mb][n], a0, a1, a2, a3, qf[n][k][0], qf[n][k][1]);
-              }
             }
           }
-        }
-        if constexpr (E4M3) {
-#pragma unroll
-          for (int n = 0; n < NB; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[mb][n][i] = fmaf(xl[n][i], 0.0625f, x[mb][n][i]);
         }
       }
       // ---- scale and bias
@@ -396,8 +383,8 @@ __global__ void __launch_bounds__(kWarps * 32, cta_per_sm(NB)) attn_cache_kernel
 #pragma unroll
       for (int mb = 0; mb < KM; ++mb) {
         const int j1 = j0 + 16 * mb;
-        const bool in_ring = BIAS != 0 && j1 + 16 <= min(s.prefix, a.P);
-        const uint8_t *fsrc = src + mb * group + 32 * rb + (E4M3 ? 32 : 0);
+        const bool in_ring = BIAS != 0 && j0 + 16 * KM <= min(s.prefix, a.P);
+        const uint8_t *fsrc = src + f_at + mb * 16 * fk_row;
         int kpos[2] = {0, 0};
         if (BIAS != 0 && !in_ring) {
 #pragma unroll
@@ -455,7 +442,7 @@ __global__ void __launch_bounds__(kWarps * 32, cta_per_sm(NB)) attn_cache_kernel
           skf[i] = svf[mb][i] = 0.f;
           if constexpr (E4M3) {
             // 2^(byte - 127); byte 255 is NaN, byte 0 (2^-127, which cache_write does not make) counts as 0
-            const uint32_t k8 = src[mb * group + 32 * rb + g + 8 * i], v8 = src[mb * group + 32 * rb + 16 + g + 8 * i];
+            const uint32_t k8 = src[ks_at + mb * 16 + g + 8 * i], v8 = src[vs_at + mb * 16 + g + 8 * i];
             skf[i] = __uint_as_float(k8 == 255u ? 0x7fffffffu : k8 << 23);
             svf[mb][i] = v8 == 255u ? __uint_as_float(0x7fffffffu) : float(int(v8) - 127);
           }
@@ -604,7 +591,7 @@ __global__ void __launch_bounds__(kWarps * 32, cta_per_sm(NB)) attn_cache_kernel
           uint32_t vr[4][VP];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const uint8_t *p = src + mb * group + ((i & 1) + 8 * (i >> 1)) * rb + vat[c];
+            const uint8_t *p = src + (mb * 16 + (i & 1) + 8 * (i >> 1)) * rb + vat[c];
             if (!last)
               read_words<VP>(p, vr[i]);
             else
@@ -737,7 +724,7 @@ cudaError_t launch_bias(const CacheAttnArgs &a, int sms, cudaStream_t st) {
   // CTAs on an SM: as many as leave each a ring of four groups a warp (three, of one group a step) in the 227 KB (1 KB
   // a CTA is the system's); every CTA of the grid is resident, so the equal runs of keys also end together
   constexpr int least = groups_per_step(D, E4M3, NB) == 2 ? 2 : 3;
-  int ctas = cta_per_sm(NB) + 1, stages = 0;
+  int ctas = most_ctas(D, E4M3, NB) + 1, stages = 0;
   while (stages < least && ctas > 1) {
     --ctas;
     stages = std::min(kMaxStages, (227 * 1024 / ctas - 1024 - fixed) / stage);

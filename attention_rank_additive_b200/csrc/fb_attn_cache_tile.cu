@@ -167,7 +167,7 @@ __device__ __noinline__ Chunks clear_odd(Chunks c, int *odd, int stamp) {
 }
 
 __device__ __noinline__ void wait_long(uint64_t *bar, uint32_t parity, volatile int *abort) {
-  mbar_wait_long(bar, parity, abort);
+  mbar_wait(bar, parity, abort);
 }
 __device__ __forceinline__ void wait_for(uint64_t *bar, uint32_t parity, volatile int *abort) {
   if (!mbar_try_wait(bar, parity)) wait_long(bar, parity, abort);
