@@ -688,7 +688,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const __gr
     const int factor_steps = BIAS == 2 ? a.RP / 16 : 0;
     unsigned ktile = 0, vtile = 0;  // tiles whose K and V the products to come read
     uint32_t qphase = 0, pphase = 0;  // bit t of pphase: stream t's
-    while (lane == 0 && walk.next(a, g)) {
+    if (elect_one()) {
+    while (walk.next(a, g)) {
       const int n = g.k1 - g.k0, h = g.item / a.chunks;
       const int rows = min(p.tiles * 128, a.rows - (g.item - h * a.chunks) * p.tiles * 128);
       const int n0 = steps_of(0, n, rows), n1 = nstreams == 2 ? steps_of(1, n, rows) : 0;
@@ -749,7 +750,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const __gr
         if (pi >= 0 && pi < pn) product(1 - t, pi == 0, pi == pn - 1);
       }
     }
-    if (lane == 0) {
       tc_commit(&c.drain);
       if (!mbar_wait_for(&c.drain, 0, 1000000000ull)) c.abort = 1;
     }
