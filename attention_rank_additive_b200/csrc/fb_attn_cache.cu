@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(kWarps * 32, most_ctas(D, E4M3, NB)) attn_cach
   griddep_wait();
 
   // ---- this CTA's run of blocks of all items
-  Walk walk(a, BK, lane);
+  Walk walk(a, BK, 0, lane);
   if (blockIdx.x >= walk.ctas) return;
   if (threadIdx.x == 0) sm.abort = 0;
   if (lane < stages) mbar_init(&sm.full[warp][lane], 1);

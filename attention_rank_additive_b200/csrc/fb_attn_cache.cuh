@@ -112,24 +112,26 @@ __device__ __forceinline__ void write_row(const CacheAttnArgs &a, const Seq &s, 
 struct Segment {
   Seq s;
   int b, item, blocks, k0, k1;
-  long long start;  // the item's first block among all
+  long long start;  // the number of the item's first block
 };
 
 // All blocks of keys of all items, numbered sequence by sequence and item by item, are dealt out in equal runs: CTA c
-// of `ctas` takes first(c) .. first(c + 1) - 1. Built and walked by whole warps.
+// of `ctas` takes first(c) .. first(c + 1) - 1. Built and walked by whole warps. Before an item's blocks `extra` numbers
+// stand for what an item costs beside them, so that CTAs with more items get fewer blocks.
 struct Walk {
   long long total, ctas, pos, hi, bstart;
-  int b, keys, per_seq;
+  int b, keys, extra, per_seq;
 
   __device__ __forceinline__ int blocks_of(const Seq &s) const { return max(1, int(((long long)s.len + keys - 1) / keys)); }
+  __device__ __forceinline__ int numbers_of(const Seq &s) const { return blocks_of(s) + extra; }
   __device__ __forceinline__ long long first(long long c) const { return c * total / ctas; }
 
-  __device__ __forceinline__ Walk(const CacheAttnArgs &a, int block_keys, int lane) {
-    keys = block_keys;
+  __device__ __forceinline__ Walk(const CacheAttnArgs &a, int block_keys, int item_extra, int lane) {
+    keys = block_keys, extra = item_extra;
     per_seq = a.H * a.chunks;
     total = 0;
     for (int b0 = 0; b0 < a.B; b0 += 32)
-      total += __reduce_add_sync(0xffffffffu, b0 + lane < a.B ? blocks_of(sequence(a, b0 + lane, false)) : 0);
+      total += __reduce_add_sync(0xffffffffu, b0 + lane < a.B ? numbers_of(sequence(a, b0 + lane, false)) : 0);
     total *= per_seq;
     ctas = min((long long)gridDim.x, total);
     pos = hi = 0;
@@ -138,7 +140,7 @@ struct Walk {
     if (blockIdx.x >= ctas) return;
     pos = first(blockIdx.x), hi = first(blockIdx.x + 1);
     for (int b0 = 0; b0 < a.B; b0 += 32) {  // the sequence that block `pos` is in
-      const int mine = b0 + lane < a.B ? blocks_of(sequence(a, b0 + lane, false)) : 0;
+      const int mine = b0 + lane < a.B ? numbers_of(sequence(a, b0 + lane, false)) : 0;
       int incl = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -159,19 +161,22 @@ struct Walk {
   __device__ __forceinline__ bool next(const CacheAttnArgs &a, Segment &g) {
     while (pos < hi && b < a.B) {
       g.s = sequence(a, b, true);
-      const int nb = blocks_of(g.s);
-      if (pos >= bstart + (long long)nb * per_seq) {
-        bstart += (long long)nb * per_seq;
+      const int n = numbers_of(g.s);
+      if (pos >= bstart + (long long)n * per_seq) {
+        bstart += (long long)n * per_seq;
         ++b;
         continue;
       }
       g.b = b;
-      g.blocks = nb;
-      g.item = int((pos - bstart) / nb);
-      g.start = bstart + (long long)g.item * nb;
-      g.k0 = int(pos - g.start);
-      g.k1 = int(min((long long)nb, g.k0 + (hi - pos)));
-      pos += g.k1 - g.k0;
+      g.blocks = n - extra;
+      g.item = int((pos - bstart) / n);
+      const long long start = bstart + (long long)g.item * n;
+      const int n0 = int(pos - start), n1 = int(min((long long)n, n0 + (hi - pos)));
+      pos += n1 - n0;
+      if (n1 <= extra) continue;  // the item's blocks begin in the next run
+      g.start = start + extra;
+      g.k0 = max(n0 - extra, 0);
+      g.k1 = n1 - extra;
       return true;
     }
     return false;

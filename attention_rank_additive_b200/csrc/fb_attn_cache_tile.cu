@@ -41,6 +41,7 @@ constexpr int kThreads = 16 * 32;  // four warps a scheduler: 128 registers a th
 constexpr int kVThreads = 96;
 constexpr int kIssuer = 0, kVWarp = 1, kKWarp = 4, kSoftmaxWarp = 8;
 constexpr int kTileKeys = 96, kGroups = kTileKeys / 16;
+constexpr int kItemExtra = 3;  // what the queries' loads and the parts' joins of an item cost, in tiles
 constexpr float kRaise = 8.f;  // log2 units: O is rescaled when the maximum grows by more
 
 struct TilePlan {
@@ -61,7 +62,7 @@ struct Ctrl {
   int odd[8];                     // [tile & 7]: tile number + 1 where a non-finite value left the products
   int seg_odd[2];                 // [segment & 1]: segment number + 1 where one of its tiles was odd
   uint32_t tmem;
-  int abort, last;
+  int abort, last[2][2];
 };
 
 // 16-byte chunk `ch` of row `row` in a tile of 128-byte rows, swizzled; columns past 64 go to the next block of ROWS rows.
@@ -210,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const __gr
 
   // A wait that runs out marks the CTA: every role then runs on through its loops without waiting (all addresses stay
   // in bounds, the result is garbage) and the call is flagged.
-  Walk walk(a, kTileKeys, lane);
+  Walk walk(a, kTileKeys, kItemExtra, lane);
   Segment g;
   const int nstreams = p.split || p.tiles == 2 ? 2 : 1;
   // what a segment's streams do: stream t takes steps of key tiles first + t, first + t + 2, ... (split) or all
@@ -368,120 +369,163 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const __gr
       const bool whole = g.k0 == 0 && g.k1 == g.blocks;
       float *mine = a.part + (2ll * blockIdx.x + (g.k0 == 0)) * kSlot;
       if (!busy) nat = -INFINITY, l = 0.f;
-      // A row tile whose keys are all here leaves straight away. Else each stream puts its part (O, maximum, sum) into
-      // this CTA's slot, rows 128 and up for stream 1 of a split, and the item's last CTA joins the parts in order.
-      const bool direct = whole && !p.split;
+      // Parts (O, maximum, sum) of an item that crosses CTAs, and of the two streams of a split (rows 128 and up for
+      // stream 1), go to this CTA's slots; the item's last CTA joins them in order.
       bool any_odd = odd;
       if (p.split) {  // stream 0 adds what left the products of either
         if (odd) c.seg_odd[seg & 1] = seg + 1;
         named_bar_sync(1, 256);
         any_odd = t == 0 && c.seg_odd[seg & 1] == seg + 1;
       }
-      if (t < nstreams) {
-        const bool none = tok < 0 || saw_none(nat, l);
-        const int at = p.split ? t * 128 + row : r;
-        if (!direct)
-          mine[DP * 256 + at] = nat, mine[(DP + 1) * 256 + at] = l;
-        else if (have)
-          a.LSE[qrow] = none ? -INFINITY : nat + logf(l);
-        const float inv = none ? 0.f : 1.f / l;
-        const int odd0 = max(g.k0 * kTileKeys, s.prefix / kTileKeys * kTileKeys), odd1 = min(s.len, g.k1 * kTileKeys);
-        const bool real = steps > 0 && busy;  // uniform over the warp; other parts have a maximum of -inf and no O
-        if (real || direct) {
+      const int at = p.split ? t * 128 + row : r;
+      const int odd0 = max(g.k0 * kTileKeys, s.prefix / kTileKeys * kTileKeys), odd1 = min(s.len, g.k1 * kTileKeys);
+      const bool real = steps > 0 && busy;  // uniform over the warp; other parts have a maximum of -inf and no O
+      // columns 16 q .. 16 q + 15 of this row's O
+      auto own = [&](int q, float *x) {
+        uint32_t w[16];
+        tmem_ld16(o_tm + 16u * q, w);
+        tmem_ld_wait16(w);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) x[k] = __uint_as_float(w[k]);
+        if (__builtin_expect(any_odd && tok >= 0, 0)) {
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+            if (16 * q + k < a.d) x[k] += odd_sum_of<E4M3>(a, s, g.b, h, tok, 16 * q + k, odd0, odd1);
+        }
+      };
+      auto write_part = [&]() {
+        mine[DP * 256 + at] = nat, mine[(DP + 1) * 256 + at] = l;
+        if (!real) return;
 #pragma unroll 1
-          for (int q = 0; q < DP / 32; ++q) {
-            uint32_t x[32];
+        for (int q = 0; q < DP / 16; ++q) {
+          float x[16];
+          own(q, x);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) x[k] = 0u;
-            if (real) {
-              tmem_ld32(o_tm + 32u * q, x);
-              tmem_ld_wait32(x);
-            }
-            if (__builtin_expect(any_odd && tok >= 0, 0)) {
-#pragma unroll
-              for (int k = 0; k < 32; ++k)
-                if (32 * q + k < a.d)
-                  x[k] = __float_as_uint(__uint_as_float(x[k]) + odd_sum_of<E4M3>(a, s, g.b, h, tok, 32 * q + k, odd0, odd1));
-            }
-            if (!direct) {
-#pragma unroll
-              for (int k = 0; k < 32; ++k) mine[(32 * q + k) * 256 + at] = __uint_as_float(x[k]);
-            } else if (have) {
-              uint4 *o = reinterpret_cast<uint4 *>(a.O + qrow * a.d + 32 * q);
-#pragma unroll
-              for (int k = 0; k < 32; k += 8) {
-                float y[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = none ? 0.f : __uint_as_float(x[k + e]) * inv;
-                if (32 * q + k < a.d)
-                  o[k / 8] = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
-                                        pack_bf16x2(y[6], y[7]));
-              }
-            }
-          }
+          for (int k = 0; k < 16; ++k) mine[(16 * q + k) * 256 + at] = x[k];
         }
-      }
-      if (!direct) {
-        __threadfence();
-        named_bar_sync(1, 256);
-        int c0 = blockIdx.x, c1 = blockIdx.x;
-        bool last = true;
+      };
+      // 16 columns of an output row
+      auto store = [&](long long out_row, int k, const float *y) {
+        uint4 *o = reinterpret_cast<uint4 *>(a.O + out_row * a.d + k);
+#pragma unroll
+        for (int e = 0; e < 16; e += 8)
+          if (k + e < a.d)
+            o[e / 8] = make_uint4(pack_bf16x2(y[e], y[e + 1]), pack_bf16x2(y[e + 2], y[e + 3]),
+                                  pack_bf16x2(y[e + 4], y[e + 5]), pack_bf16x2(y[e + 6], y[e + 7]));
+      };
+      int c0 = blockIdx.x, c1 = blockIdx.x;
+      bool last = true;
+      if (!whole) c0 = walk.owner(g.start), c1 = walk.owner(g.start + g.blocks - 1);
+      if (!p.split) {
+        // Row tiles: a thread joins its row, with this CTA's part out of TMEM. A CTA that finds all others done does not
+        // write its part at all: CTAs end together, and writing and reading all parts then took 15 us of 200.
         if (!whole) {
-          c0 = walk.owner(g.start), c1 = walk.owner(g.start + g.blocks - 1);
-          if (threadIdx.x == kSoftmaxWarp * 32) {
-            c.last = atomicAdd(a.counters + c0, 1u) == unsigned(c1 - c0);
-            if (c.last) a.counters[c0] = 0u;  // for the next call
-          }
+          const bool leader = threadIdx.x == kSoftmaxWarp * 32;
+          int *flag = c.last[seg & 1];
+          if (leader) flag[0] = atomicAdd(a.counters + c0, 0u) == unsigned(c1 - c0);
           named_bar_sync(1, 256);
-          last = c.last;
-          if (last) __threadfence();
+          last = flag[0];
+          if (!last) {
+            write_part();
+            __threadfence();
+            named_bar_sync(1, 256);
+            if (leader) flag[1] = atomicAdd(a.counters + c0, 1u) == unsigned(c1 - c0);
+            named_bar_sync(1, 256);
+            last = flag[1];
+          }
+          if (last) {
+            __threadfence();
+            if (leader) a.counters[c0] = 0u;  // for the next call
+          }
         }
-        if (last && have && (p.split || t < p.tiles)) {
-          // part i: CTA c0 + i / halves, half i % halves; in a split the streams' warps take half of the columns each
-          const int halves = p.split ? 2 : 1, parts = (c1 - c0 + 1) * halves;
-          auto part = [&](int i) {
-            const int cc = c0 + (p.split ? i >> 1 : i);
-            return a.part + (2ll * cc + (cc == c0)) * kSlot + (p.split ? (i & 1) * 128 + row : r);
-          };
+        if (last) {
+          auto part = [&](int cc) { return a.part + (2ll * cc + (cc == c0)) * kSlot + r; };
           float top = -INFINITY, sum = 0.f;
 #pragma unroll 4
-          for (int i = 0; i < parts; ++i) {  // running maximum and sum
-            const float mc = __ldcg(part(i) + DP * 256), lc = __ldcg(part(i) + (DP + 1) * 256);
+          for (int cc = c0; cc <= c1; ++cc) {
+            const bool here = cc == int(blockIdx.x);
+            const float mc = here ? nat : __ldcg(part(cc) + DP * 256), lc = here ? l : __ldcg(part(cc) + (DP + 1) * 256);
             const float mn = fmaxf(top, mc), z = mn == -INFINITY ? 0.f : mn;
-            sum = sum * ex2_approx((top - z) * kCacheLog2e) + (saw_none(mc, lc) ? 0.f : lc * ex2_approx((mc - z) * kCacheLog2e));
+            sum = sum * ex2_approx((top - z) * kCacheLog2e) + lc * ex2_approx((mc - z) * kCacheLog2e);
             top = mn;
           }
           const bool none = tok < 0 || saw_none(top, sum);
-          if (!p.split || t == 0) a.LSE[qrow] = none ? -INFINITY : top + logf(sum);
-          const float inv = none ? 0.f : 1.f / sum;
-          const int k0 = p.split ? t * (DP / 2) : 0, k1 = p.split ? k0 + DP / 2 : DP;
+          const float inv = none ? 0.f : 1.f / sum, z = top == -INFINITY ? 0.f : top;
+          if (have) a.LSE[qrow] = none ? -INFINITY : top + logf(sum);
 #pragma unroll 1
-          for (int k = k0; k < k1; k += 32) {  // 32 loads in flight
-            float y[32];
+          for (int q = 0; q < DP / 16; ++q) {
+            float x[16], y[16];
 #pragma unroll
-            for (int e = 0; e < 32; ++e) y[e] = 0.f;
-            if (!none)
-#pragma unroll 1
-              for (int i = 0; i < parts; ++i) {
-                const float *x = part(i);
-                const float mc = __ldcg(x + DP * 256);
-                if (saw_none(mc, __ldcg(x + (DP + 1) * 256))) continue;  // its O was not written
-                float v[32];
+            for (int e = 0; e < 16; ++e) x[e] = y[e] = 0.f;
+            if (real) own(q, x);
+            if (!none) {
+#pragma unroll 2
+              for (int cc = c0; cc <= c1; ++cc) {
+                const bool here = cc == int(blockIdx.x);
+                const float *from = part(cc);
+                float v[16];
 #pragma unroll
-                for (int e = 0; e < 32; ++e) v[e] = __ldcg(x + (k + e) * 256);
-                const float f = ex2_approx((mc - top) * kCacheLog2e) * inv;
+                for (int e = 0; e < 16; ++e) v[e] = here ? x[e] : __ldcg(from + (16 * q + e) * 256);
+                const float mc = here ? nat : __ldcg(from + DP * 256), lc = here ? l : __ldcg(from + (DP + 1) * 256);
+                const bool seen = !saw_none(mc, lc);  // else its O was not written
+                const float f = ex2_approx((mc - z) * kCacheLog2e) * inv;
 #pragma unroll
-                for (int e = 0; e < 32; ++e) y[e] = fmaf(v[e], f, y[e]);
+                for (int e = 0; e < 16; ++e) y[e] = seen ? fmaf(v[e], f, y[e]) : y[e];
               }
-            uint4 *o = reinterpret_cast<uint4 *>(a.O + qrow * a.d + k);
-#pragma unroll
-            for (int e = 0; e < 32; e += 8)
-              if (k + e < a.d)
-                o[e / 8] = make_uint4(pack_bf16x2(y[e], y[e + 1]), pack_bf16x2(y[e + 2], y[e + 3]),
-                                      pack_bf16x2(y[e + 4], y[e + 5]), pack_bf16x2(y[e + 6], y[e + 7]));
+            }
+            if (have) store(qrow, 16 * q, y);
           }
         }
-        if (p.split) named_bar_sync(1, 256);  // the slot's parts have been read
+      } else {
+        write_part();
+        __threadfence();
+        named_bar_sync(1, 256);
+        if (!whole) {
+          if (threadIdx.x == kSoftmaxWarp * 32) {
+            c.last[0][0] = atomicAdd(a.counters + c0, 1u) == unsigned(c1 - c0);
+            if (c.last[0][0]) a.counters[c0] = 0u;  // for the next call
+          }
+          named_bar_sync(1, 256);
+          last = c.last[0][0];
+          if (last) __threadfence();
+        }
+        if (last) {
+          // Part i: CTA c0 + i / 2, stream i % 2. A warp takes 32 rows by 16 columns at a time: with few rows all warps have
+          // some.
+          const int parts = (c1 - c0 + 1) * 2, row_blocks = (rows + 31) >> 5;
+          const long long row0 = ((long long)g.b * a.Hq + (long long)h * a.G) * a.T + chunk0;
+#pragma unroll 1
+          for (int task = warp - kSoftmaxWarp; task < row_blocks * (DP / 16); task += 8) {
+            const int k = task / row_blocks * 16, rr = task % row_blocks * 32 + lane;
+            if (rr >= rows) continue;
+            float top = -INFINITY, sum = 0.f, y[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) y[e] = 0.f;
+#pragma unroll 2
+            for (int i = 0; i < parts; ++i) {
+              const int cc = c0 + (i >> 1);
+              const float *x = a.part + (2ll * cc + (cc == c0)) * kSlot + (i & 1) * 128 + rr;
+              const float mc = __ldcg(x + DP * 256), lc = __ldcg(x + (DP + 1) * 256);
+              float v[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) v[e] = __ldcg(x + (k + e) * 256);
+              const bool seen = !saw_none(mc, lc);
+              const float mn = fmaxf(top, mc), z = mn == -INFINITY ? 0.f : mn;
+              const float f0 = ex2_approx((top - z) * kCacheLog2e), f1 = ex2_approx((mc - z) * kCacheLog2e);
+              sum = sum * f0 + lc * f1;
+#pragma unroll
+              for (int e = 0; e < 16; ++e) y[e] = fmaf(seen ? v[e] : 0.f, f1, y[e] * f0);
+              top = mn;
+            }
+            const bool none = (chunk0 + rr) % a.T >= s.count || saw_none(top, sum);
+            if (k == 0) a.LSE[row0 + rr] = none ? -INFINITY : top + logf(sum);
+            const float inv = none ? 0.f : 1.f / sum;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) y[e] = none ? 0.f : y[e] * inv;
+            store(row0 + rr, k, y);
+          }
+        }
+        named_bar_sync(1, 256);  // the slot's parts have been read
       }
     }
   } else if (warp != kIssuer) {
@@ -529,16 +573,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const __gr
           const uint32_t qt = base + p.q + t * kQTile;
           const uint4 *q = reinterpret_cast<const uint4 *>(
               a.Q + (((long long)g.b * a.Hq + (long long)h * a.G) * a.T + chunk0 + (have ? r : 0)) * a.d);
+          constexpr int kLoads = DP == 128 && !E4M3 ? 8 : DP / 8;  // in flight, beside the registers of the first rows of K
 #pragma unroll 1
-          for (int c0 = 0; c0 < DP / 8; c0 += 8) {
-            uint4 v[8];
+          for (int c0 = 0; c0 < DP / 8; c0 += kLoads) {
+            uint4 v[kLoads];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < kLoads; ++i) {
               v[i] = make_uint4(0u, 0u, 0u, 0u);
               if (have && (c0 + i) * 8 < a.d) v[i] = __ldg(q + c0 + i);
             }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sts16(qt + tile_at<128>(l, c0 + i), v[i].x, v[i].y, v[i].z, v[i].w);
+            for (int i = 0; i < kLoads; ++i) sts16(qt + tile_at<128>(l, c0 + i), v[i].x, v[i].y, v[i].z, v[i].w);
           }
           if constexpr (BIAS == 2) {
             const uint32_t ft = base + p.fq + t * fq_tile;
