@@ -5,7 +5,7 @@
 
 #include "fb_attn_cache.h"
 #include "fb_internal.h"
-#include "fb_ptx.cuh"
+#include "fb_ptx_cache.cuh"
 
 namespace fb {
 
