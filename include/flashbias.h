@@ -571,7 +571,8 @@ int fb_cache_bias_prepare(int Hq, int H, int P, int R, const float *phi_q, const
  * Values in cache rows that a query row does not see (infinities and NaN too)
  * do not reach it. Cache rows that the table does not lead to are not seen and
  * flag FB_ERR_RANGE.
- * Arithmetic: products of bf16 queries with bf16 or e4m3 keys are exact, sums
+ * Arithmetic: products of bf16 queries with bf16 or e4m3 keys are exact (few
+ * rows of an e4m3 cache: to 2^-39 of the query row's largest value), sums
  * and the softmax are fp32; the probabilities are rounded once for the product
  * with V, to bf16, or to fp16 where an e4m3 cache meets at most 16 query rows of
  * a key/value head (T Hq / H; more rows go through 128-row tiles, where a bias of

@@ -618,3 +618,63 @@ def test_refusals():
         assert e.value.status == status
     torch.cuda.synchronize()
     assert _status() == fb.FB_OK
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("context", [0, 70, 9000])
+def test_non_finite_values_in_two_row_tiles(kind, context):
+    """150 rows, so two row tiles, whose keys one CTA or many have: a non-finite value of a new token reaches the rows
+    that see it, in its channel, and nothing else, to the bit."""
+    T, hot = 150, 100
+    c = _case(kind, 64, 2, 2, T, 16, [context, 33], None, "low8", False, seed=11)
+    clean = _call(c)
+    at = int(c["table"][0, (context + hot) // 16]), 1, (context + hot) % 16, 5
+    if kind == "bf16":
+        c["cache"].v[at] = -math.inf
+    else:
+        c["cache"].v.view(torch.uint8)[at] = 0x7F
+    o, lse = _call(c)
+    assert torch.equal(lse, clean[1])
+    hit = torch.zeros_like(o, dtype=torch.bool)
+    hit[0, 1, hot:, 5] = True
+    assert torch.equal(o[~hit], clean[0][~hit])
+    assert (o[hit] == -math.inf).all() if kind == "bf16" else o[hit].isnan().all()
+    assert _status() == fb.FB_OK
+
+
+@pytest.mark.parametrize("kind,d,Hq,H,T,page,prefix,counts,bias,tree", [
+    ("bf16", 128, 16, 1, 17, 16, [40000], None, "none", False),  # one item over all CTAs, two row tiles
+    ("e4m3", 128, 4, 1, 70, 64, [0, 1, 95, 96, 97], [70, 1, 0, 70, 69], "low64", True),
+    ("e4m3", 128, 8, 2, 40, 16, [700, 20000], None, "low100", True),  # one row tile, one slot of keys
+    ("bf16", 64, 2, 1, 300, 32, [1234], None, "sandwich128", False),
+    ("e4m3", 32, 40, 2, 20, 256, [5000] * 3, [20, 0, 7], "alibi", True),  # chunks of 256 rows
+    ("bf16", 96, 1, 1, 24, 16, [30000], None, "alibi", True),  # one split row tile over all CTAs
+])
+def test_tiles_at_their_borders(kind, d, Hq, H, T, page, prefix, counts, bias, tree):
+    c = _case(kind, d, Hq, H, T, page, prefix, counts, bias, tree, seed=21)
+    ws = fb.cache_workspace(len(prefix), Hq, H, T, d)
+    want, got = _want(c), _call(c, workspace=ws)
+    assert _status() == fb.FB_OK
+    _compare(got, want)
+    for _ in range(3):
+        again = _call(c, workspace=ws)
+        assert all(torch.equal(a, b) for a, b in zip(got, again))
+
+
+def test_two_streams_with_workspaces_of_their_own():
+    """Calls that overlap: the same cache read by two streams at once gives each what it gets alone."""
+    cases = [_case("e4m3", 128, 8, 2, T, 64, [6000, 900], None, "none", False, seed=30 + T) for T in (1, 40)]
+    alone = [_call(c) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    spaces = [fb.cache_workspace(2, 8, 2, c["q"].shape[2], 128) for c in cases]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        out = []
+        for c, s, w in zip(cases, streams, spaces):
+            with torch.cuda.stream(s):
+                out.append(_call(c, workspace=w))
+        torch.cuda.synchronize()
+        for a, b in zip(out, alone):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+    assert _status() == fb.FB_OK
