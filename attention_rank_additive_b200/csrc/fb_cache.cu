@@ -61,7 +61,7 @@ __device__ __forceinline__ long long pool_row(const CacheArgs &a, int b, int h, 
 }
 
 // Which rows this thread's group of lanes works on: n, n + step, ...
-constexpr int kSteps = 4;
+constexpr int kSteps = 2;
 struct Row {
   int b, h, n, step, lane;
 };
@@ -101,11 +101,12 @@ struct Eight {
   }
 };
 
-// STEPS runs of rows at a time: all of their loads are issued before the first row's maximum is taken, so that a block
-// costs one memory latency (one row after the other: 20 us for 8 prompts of up to 2048 tokens of 12 heads).
+// All loads of a block's rows are issued before the first row's maximum is taken, so that a block costs one memory
+// latency (one row after the other: 20 us for 8 prompts of up to 2048 tokens of 12 heads of 64 into pages of 16). Two
+// rows a thread: with four the registers left fewer threads on an SM and the last wave was longer (18 us, and 133 us in
+// place of 127 for the read of 4 x 32768 tokens, 8 heads of 128, whose kernel is laid out alike); now 15.5 us, 3.9 TB/s.
 template <typename T, bool E4M3>
 __global__ void __launch_bounds__(256) cache_write_kernel(const CacheArgs a) {
-  constexpr int STEPS = sizeof(T) == 4 ? 2 : 4;
   const Row r = row_of(a);
   griddep_wait();
   const int count = r.h < a.H ? min(a.counts ? a.counts[r.b] : a.N, a.N) : 0;
@@ -113,55 +114,52 @@ __global__ void __launch_bounds__(256) cache_write_kernel(const CacheArgs a) {
   const bool lane_in = r.lane * 8 < a.d;
   const T *src[2] = {static_cast<const T *>(a.src[0]) + r.b * a.xb + r.h * a.xh + r.lane * 8,
                      static_cast<const T *>(a.src[1]) + r.b * a.yb + r.h * a.yh + r.lane * 8};
-#pragma unroll 1
-  for (int i0 = 0; i0 < kSteps; i0 += STEPS) {
-    Eight<T> in[STEPS][2];
-    long long row[STEPS];
+  Eight<T> in[kSteps][2];
+  long long row[kSteps];
 #pragma unroll
-    for (int i = 0; i < STEPS; ++i) {
-      const int n = r.n + (i0 + i) * r.step;
-      const bool have = n < count && lane_in;
+  for (int i = 0; i < kSteps; ++i) {
+    const int n = r.n + i * r.step;
+    const bool have = n < count && lane_in;
 #pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        in[i][w].clear();
-        if (have) in[i][w].load(src[w] + n * (w ? a.yn : a.xn));
-      }
-      row[i] = -1;
-      if (n < count) row[i] = pool_row(a, r.b, r.h, start + n);
+    for (int w = 0; w < 2; ++w) {
+      in[i][w].clear();
+      if (have) in[i][w].load(src[w] + n * (w ? a.yn : a.xn));
     }
+    row[i] = -1;
+    if (n < count) row[i] = pool_row(a, r.b, r.h, start + n);
+  }
 #pragma unroll
-    for (int i = 0; i < STEPS; ++i) {
-      const bool live = row[i] >= 0 && lane_in;
+  for (int i = 0; i < kSteps; ++i) {
+    const bool live = row[i] >= 0 && lane_in;
 #pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        float x[8];
-        in[i][w].get(x);
-        if constexpr (!E4M3) {
-          if (live) store8(static_cast<__nv_bfloat16 *>(a.dst[w]) + row[i] * a.d + r.lane * 8, x);
-        } else {
-          // the row's largest finite magnitude; infinities, which are rare, are left out in a second look
-          float top = 0.f;
+    for (int w = 0; w < 2; ++w) {
+      float x[8];
+      in[i][w].get(x);
+      if constexpr (!E4M3) {
+        if (live) store8(static_cast<__nv_bfloat16 *>(a.dst[w]) + row[i] * a.d + r.lane * 8, x);
+      } else {
+        // the row's largest finite magnitude; infinities, which are rare, are left out in a second look
+        float top = 0.f;
 #pragma unroll
-          for (int k = 0; k < 8; k += 2) top = fmax3(top, fabsf(x[k]), fabsf(x[k + 1]));
-          if (__any_sync(0xffffffffu, top == INFINITY)) {
-            top = 0.f;
+        for (int k = 0; k < 8; k += 2) top = fmax3(top, fabsf(x[k]), fabsf(x[k + 1]));
+        if (__any_sync(0xffffffffu, top == INFINITY)) {
+          top = 0.f;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(x[k]) < INFINITY ? fabsf(x[k]) : 0.f);
-          }
+          for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(x[k]) < INFINITY ? fabsf(x[k]) : 0.f);
+        }
 #pragma unroll
-          for (int o = 8; o > 0; o >>= 1)
-            if (o < a.lanes) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-          // top = 1.m 2^(f - 127); the scale's exponent is f - 127 - 8, one more where 1.m > 1.75 (448 = 1.75 2^8)
-          const uint32_t bits = __float_as_uint(top);
-          int e = int(bits >> 23) - 135 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
-          e = max(e, -126);
-          const float inv = __uint_as_float(uint32_t(127 - e) << 23);
-          if (live) {
-            const uint32_t lo = e4m3x2(x[0] * inv, x[1] * inv) | (e4m3x2(x[2] * inv, x[3] * inv) << 16);
-            const uint32_t hi = e4m3x2(x[4] * inv, x[5] * inv) | (e4m3x2(x[6] * inv, x[7] * inv) << 16);
-            *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(a.dst[w]) + row[i] * a.d + r.lane * 8) = make_uint2(lo, hi);
-            if (r.lane == 0) a.scale[w][row[i]] = uint8_t(e + 127);
-          }
+        for (int o = 8; o > 0; o >>= 1)
+          if (o < a.lanes) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        // top = 1.m 2^(f - 127); the scale's exponent is f - 127 - 8, one more where 1.m > 1.75 (448 = 1.75 2^8)
+        const uint32_t bits = __float_as_uint(top);
+        int e = int(bits >> 23) - 135 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
+        e = max(e, -126);
+        const float inv = __uint_as_float(uint32_t(127 - e) << 23);
+        if (live) {
+          const uint32_t lo = e4m3x2(x[0] * inv, x[1] * inv) | (e4m3x2(x[2] * inv, x[3] * inv) << 16);
+          const uint32_t hi = e4m3x2(x[4] * inv, x[5] * inv) | (e4m3x2(x[6] * inv, x[7] * inv) << 16);
+          *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(a.dst[w]) + row[i] * a.d + r.lane * 8) = make_uint2(lo, hi);
+          if (r.lane == 0) a.scale[w][row[i]] = uint8_t(e + 127);
         }
       }
     }

@@ -496,6 +496,7 @@ int fb_rope_frequencies_host(int rot, double base, int scaling, double factor,
  *
  *  cache_dt    FB_BF16 or FB_E4M3 (scales may be NULL for FB_BF16).
  *  d           16 to 128, a multiple of 16. page_size 16, 32, 64, 128 or 256.
+ *  T, N        up to 2^21 - 32 rows of a sequence in one write or read.
  *  pools       16-byte aligned, their scales too.
  *  block_table [B, max_pages] int32 device.
  *  starts      [B] int32 device; counts [B] int32 device or NULL (all).
