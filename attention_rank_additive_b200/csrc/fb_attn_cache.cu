@@ -653,6 +653,7 @@ __global__ void __launch_bounds__(kWarps * 32, most_ctas(D, E4M3, NB)) attn_cach
     }
 
     __syncthreads();  // the ring becomes the join's memory
+    const bool odd = sm.odd;  // read by all before the next barrier, behind which thread 0 may clear it for the next segment
     // ---- the warps' parts of the segment
 #pragma unroll
     for (int n = 0; n < NB; ++n)
@@ -684,7 +685,7 @@ __global__ void __launch_bounds__(kWarps * 32, most_ctas(D, E4M3, NB)) attn_cach
         sum += join.l[w][row] * ex2_approx(y);
         val += join.o[w][row][dd] * ex2_approx(y + join.e[w][row]);
       }
-      if (sm.odd && dd < a.d) val += odd_sum<E4M3>(a, s, b, h, (r0 + row) % a.T, dd, max(k0 * BK, s.prefix / (16 * KM) * (16 * KM)), jend);
+      if (odd && dd < a.d) val += odd_sum<E4M3>(a, s, b, h, (r0 + row) % a.T, dd, max(k0 * BK, s.prefix / (16 * KM) * (16 * KM)), jend);
       if (whole) {
         write_row(a, s, qrow0 + r0 + row, (r0 + row) % a.T, dd, top, sum, val);
       } else {

@@ -678,3 +678,35 @@ def test_two_streams_with_workspaces_of_their_own():
         for a, b in zip(out, alone):
             assert all(torch.equal(x, y) for x, y in zip(a, b))
     assert _status() == fb.FB_OK
+
+
+def _plant(c, kind, b, head, token, channel, what=math.inf):
+    """`what` (NaN in an 8-bit cache) at one value of cache token `token` of sequence b."""
+    page = c["cache"].page
+    at = int(c["table"][b, token // page]), head, token % page, channel
+    if kind == "bf16":
+        c["cache"].v[at] = what
+    else:
+        c["cache"].v.view(torch.uint8)[at] = 0x7F
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("bias", ["none", "alibi", "low8"])
+def test_non_finite_values_in_many_short_items(kind, bias):
+    """Many items whose keys one CTA has, one after the other: a non-finite value of a new token, in every third
+    sequence, reaches all rows that see it and nothing of the next item."""
+    B, H, T, d = 160, 16, 4, 32
+    c = _case(kind, d, H, H, T, 16, [(7 * b) % 40 for b in range(B)], None, bias, True, seed=41)
+    clean = _call(c)
+    hit = torch.zeros(B, H, T, d, dtype=torch.bool)
+    for b in range(0, B, 3):
+        h, u = b % H, b % T
+        _plant(c, kind, b, h, int(c["prefix"][b]) + u, 9)
+        hit[b, h, :, 9] = ((c["mask"][b, :, 0] >> u) & 1).bool()
+    hit = hit.cuda()
+    ws = fb.cache_workspace(B, H, H, T, d)
+    for _ in range(5):
+        o, lse = _call(c, workspace=ws)
+        assert torch.equal(lse, clean[1]) and torch.equal(o[~hit], clean[0][~hit])
+        assert (o[hit] == math.inf).all() if kind == "bf16" else o[hit].isnan().all()
+    assert _status() == fb.FB_OK
