@@ -247,6 +247,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const __gr
       const int tok_all = have ? (chunk0 + r) % a.T : 0;
       const int tok = have && tok_all < s.count ? tok_all : -1;
       const int steps = t < nstreams ? steps_of(t, n, rows) : 0;
+      // A stream without steps would let the other one run any number of tiles ahead of a warp that has yet to read the
+      // last segment's marks (odd, last).
+      if (!p.split && steps_of(1, n, rows) == 0) named_bar_sync(1, 256);
       float fq[4] = {0.f, 0.f, 0.f, 0.f};
       if (BIAS == 1 && tok >= 0) {
         const int hq = a.fq_heads > 1 ? h * a.G + (chunk0 + r) / a.T : 0;

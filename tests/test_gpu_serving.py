@@ -710,3 +710,17 @@ def test_non_finite_values_in_many_short_items(kind, bias):
         assert torch.equal(lse, clean[1]) and torch.equal(o[~hit], clean[0][~hit])
         assert (o[hit] == math.inf).all() if kind == "bf16" else o[hit].isnan().all()
     assert _status() == fb.FB_OK
+
+
+@pytest.mark.parametrize("B,H,T,context", [(20, 8, 300, 0), (12, 6, 260, 90), (50, 3, 140, 5)])
+def test_many_short_items_of_two_row_tiles(B, H, T, context):
+    """Items of one to four key tiles, most of which one CTA has, between items that cross CTAs: chunks of both row
+    tiles and of one in turn."""
+    c = _case("bf16", 32, H, H, T, 16, [context + b % 7 for b in range(B)], None, "none", False, seed=61)
+    ws = fb.cache_workspace(B, H, H, T, 32)
+    got = _call(c, workspace=ws)
+    _compare(got, _want(c))
+    for _ in range(5):
+        again = _call(c, workspace=ws)
+        assert all(torch.equal(a, b) for a, b in zip(got, again))
+    assert _status() == fb.FB_OK
