@@ -65,7 +65,6 @@ struct Ctrl {
   uint64_t drain;
   unsigned alive[4];              // [tile & 3]: bit i: 16-key group i has a page
   int odd[8];                     // [tile & 7]: tile number + 1 where a non-finite value left the products
-  int seg_odd[2];                 // [segment & 1]: segment number + 1 where one of its tiles was odd
   uint32_t tmem;
   int abort, last[2][2];
 };
@@ -108,9 +107,15 @@ __device__ __noinline__ uint32_t sees(const CacheAttnArgs &a, int prefix, int co
   return __funnelshift_r(word(u0 >> 5), u0 & 31 ? word((u0 >> 5) + 1) : 0u, u0 & 31);
 }
 
+// The non-finite values at d = dd that left the products of the key tiles k, k + stride, ... below k1 (those that reach
+// past the context), of the keys that token t sees.
 template <bool E4M3>
-__device__ __noinline__ float odd_sum_of(const CacheAttnArgs &a, Seq s, int b, int h, int t, int dd, int j0, int j1) {
-  return odd_sum<E4M3>(a, s, b, h, t, dd, j0, j1);
+__device__ __noinline__ float odd_sum_of(const CacheAttnArgs &a, Seq s, int b, int h, int t, int dd, int k, int k1, int stride) {
+  const int first = s.prefix / kTileKeys;
+  if (k < first) k += (first - k + stride - 1) / stride * stride;
+  float sum = 0.f;
+  for (; k < k1; k += stride) sum += odd_sum<E4M3>(a, s, b, h, t, dd, k * kTileKeys, min(s.len, (k + 1) * kTileKeys));
+  return sum;
 }
 
 // Two e4m3 codes (half `hi` of w) times a scale, as bf16; NaN codes stay NaN.
@@ -202,7 +207,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const __gr
     }
     mbar_init(&c.drain, 1);
     for (int i = 0; i < 8; ++i) c.odd[i] = 0;
-    c.seg_odd[0] = c.seg_odd[1] = 0;
     c.abort = 0;
     fence_mbar_init();
   }
@@ -378,15 +382,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const __gr
       float *mine = a.part + (2ll * blockIdx.x + (g.k0 == 0)) * kSlot;
       if (!busy) nat = -INFINITY, l = 0.f;
       // Parts (O, maximum, sum) of an item that crosses CTAs, and of the two streams of a split (rows 128 and up for
-      // stream 1), go to this CTA's slots; the item's last CTA joins them in order.
-      bool any_odd = odd;
-      if (p.split) {  // stream 0 adds what left the products of either
-        if (odd) c.seg_odd[seg & 1] = seg + 1;
-        named_bar_sync(1, 256);
-        any_odd = t == 0 && c.seg_odd[seg & 1] == seg + 1;
-      }
+      // stream 1), go to this CTA's slots; the item's last CTA joins them in order. Non-finite values that left a stream's
+      // products come back into its own part: another may have seen no key of the row, or weigh nothing beside it.
       const int at = p.split ? t * 128 + row : r;
-      const int odd0 = max(g.k0 * kTileKeys, s.prefix / kTileKeys * kTileKeys), odd1 = min(s.len, g.k1 * kTileKeys);
       const bool real = steps > 0 && busy;  // uniform over the warp; other parts have a maximum of -inf and no O
       // columns 16 q .. 16 q + 15 of this row's O
       auto own = [&](int q, float *x) {
@@ -395,10 +393,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const __gr
         tmem_ld_wait16(w);
 #pragma unroll
         for (int k = 0; k < 16; ++k) x[k] = __uint_as_float(w[k]);
-        if (__builtin_expect(any_odd && tok >= 0, 0)) {
+        if (__builtin_expect(odd && tok >= 0, 0)) {
 #pragma unroll
           for (int k = 0; k < 16; ++k)
-            if (16 * q + k < a.d) x[k] += odd_sum_of<E4M3>(a, s, g.b, h, tok, 16 * q + k, odd0, odd1);
+            if (16 * q + k < a.d) x[k] += odd_sum_of<E4M3>(a, s, g.b, h, tok, 16 * q + k, g.k0 + (p.split ? t : 0), g.k1,
+                                                           p.split ? 2 : 1);
         }
       };
       auto write_part = [&]() {

@@ -724,3 +724,32 @@ def test_many_short_items_of_two_row_tiles(B, H, T, context):
         again = _call(c, workspace=ws)
         assert all(torch.equal(a, b) for a, b in zip(got, again))
     assert _status() == fb.FB_OK
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("T", [99, 100, 128])
+@pytest.mark.parametrize("context", [0, 200, 9000])
+@pytest.mark.parametrize("late", [False, True])
+def test_non_finite_values_in_a_split_row_tile(kind, T, context, late):
+    """One row tile, whose key tiles two streams take in turn, and one CTA or many. A row may see nothing but its own key,
+    which the second stream has, or keys of the first whose weight is nothing beside those of the second: the value
+    reaches the rows that see it, in its channel, as it is."""
+    c = _case(kind, 64, 2, 2, T, 16, [context, 3], None, "none", False, seed=43)
+    see = torch.ones(T, T, dtype=torch.bool).tril()
+    if late:
+        P = context + T + 16
+        fk = torch.zeros(1, P, 1)
+        fk[0, context + 96:] = 200.0  # e^200 times the weight of the keys before
+        c["fq"], c["fk"] = torch.ones(1, P, 1), fk
+    else:
+        see[T - 3:] = torch.eye(T, dtype=torch.bool)[T - 3:]
+    c["mask"] = _words(see[None].expand(2, T, T))
+    clean = _call(c)
+    hit = torch.zeros_like(clean[0], dtype=torch.bool)
+    for u, channel in ((T - 3, 5), (T - 1, 63)):
+        _plant(c, kind, 0, 1, context + u, channel)
+        hit[0, 1, see[:, u].nonzero()[:, 0].cuda(), channel] = True
+    o, lse = _call(c)
+    assert torch.equal(lse, clean[1]) and torch.equal(o[~hit], clean[0][~hit])
+    assert (o[hit] == math.inf).all() if kind == "bf16" else o[hit].isnan().all()
+    assert _status() == fb.FB_OK
