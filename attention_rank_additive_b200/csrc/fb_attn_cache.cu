@@ -685,7 +685,7 @@ __global__ void __launch_bounds__(kWarps * 32, most_ctas(D, E4M3, NB)) attn_cach
         sum += join.l[w][row] * ex2_approx(y);
         val += join.o[w][row][dd] * ex2_approx(y + join.e[w][row]);
       }
-      if (odd && dd < a.d) val += odd_sum<E4M3>(a, s, b, h, (r0 + row) % a.T, dd, max(k0 * BK, s.prefix / (16 * KM) * (16 * KM)), jend);
+      if (odd && dd < a.d) val += odd_sum<E4M3, false>(a, s, b, h, (r0 + row) % a.T, dd, max(k0 * BK, s.prefix / (16 * KM) * (16 * KM)), jend);
       if (whole) {
         write_row(a, s, qrow0 + r0 + row, (r0 + row) % a.T, dd, top, sum, val);
       } else {

@@ -3,6 +3,8 @@
 // output row.
 #pragma once
 
+#include <cuda_fp8.h>
+
 #include "fb_attn_cache.h"
 #include "fb_internal.h"
 #include "fb_ptx_cache.cuh"
@@ -60,7 +62,7 @@ __device__ __forceinline__ int new_position(const CacheAttnArgs &a, int b, const
   return int(p);
 }
 
-// Non-finite values in a word of value codes, the word without them, and one such value (0 for a finite one).
+// A word of value codes without its non-finite values.
 template <bool E4M3>
 __device__ __forceinline__ uint32_t even_word(uint32_t w) {
   if constexpr (E4M3) {
@@ -73,9 +75,15 @@ __device__ __forceinline__ uint32_t even_word(uint32_t w) {
   }
   return w;
 }
-template <bool E4M3>
-__device__ __forceinline__ float odd_value(const uint8_t *row, int at) {
-  if constexpr (E4M3) {
+// One of them, or 0: value `at` of a row. AS_BF16: an 8-bit value left the products as bf16, times its row's scale, and may
+// lie beyond that type's range.
+template <bool E4M3, bool AS_BF16>
+__device__ __forceinline__ float odd_value(const uint8_t *row, int at, uint32_t scale) {
+  if constexpr (E4M3 && AS_BF16) {
+    const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2(row[at], __NV_E4M3);
+    const float v = __bfloat162float(__float2bfloat16_rn(__low2float(__half2(r)) * __uint_as_float(scale << 23)));
+    return fabsf(v) < INFINITY ? 0.f : v;
+  } else if constexpr (E4M3) {
     return (row[at] & 0x7fu) == 0x7fu ? __uint_as_float(0x7fffffffu) : 0.f;
   } else {
     const uint32_t v = reinterpret_cast<const uint16_t *>(row)[at];
@@ -84,15 +92,16 @@ __device__ __forceinline__ float odd_value(const uint8_t *row, int at) {
 }
 
 // The non-finite values at d = dd of the keys j0 .. j1 - 1 that token t sees.
-template <bool E4M3>
+template <bool E4M3, bool AS_BF16>
 __device__ __forceinline__ float odd_sum(const CacheAttnArgs &a, const Seq &s, int b, int h, int t, int dd, int j0, int j1) {
   float sum = 0.f;
   for (int j = j0; j < j1; ++j) {
     const int page = a.table[(long long)b * a.max_pages + (j >> a.page_shift)], u = j - s.prefix;
     if (page < 0 || page >= a.num_pages || !(u < 0 || drafted_visible(a, b, t, u))) continue;
     const long long row = (((long long)page * a.H + h) << a.page_shift) + (j & ((1 << a.page_shift) - 1));
-    if (E4M3 && a.vs[row] == 255) return __uint_as_float(0x7fffffffu);
-    sum += odd_value<E4M3>(static_cast<const uint8_t *>(a.vp) + row * a.d * (E4M3 ? 1 : 2), dd);
+    const uint32_t scale = E4M3 ? a.vs[row] : 0u;
+    if (E4M3 && scale == 255u) return __uint_as_float(0x7fffffffu);
+    sum += odd_value<E4M3, AS_BF16>(static_cast<const uint8_t *>(a.vp) + row * a.d * (E4M3 ? 1 : 2), dd, scale);
   }
   return sum;
 }

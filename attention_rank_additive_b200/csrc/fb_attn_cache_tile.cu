@@ -114,7 +114,8 @@ __device__ __noinline__ float odd_sum_of(const CacheAttnArgs &a, Seq s, int b, i
   const int first = s.prefix / kTileKeys;
   if (k < first) k += (first - k + stride - 1) / stride * stride;
   float sum = 0.f;
-  for (; k < k1; k += stride) sum += odd_sum<E4M3>(a, s, b, h, t, dd, k * kTileKeys, min(s.len, (k + 1) * kTileKeys));
+  for (; k < k1; k += stride)
+    sum += odd_sum<E4M3, true>(a, s, b, h, t, dd, k * kTileKeys, min(s.len, (k + 1) * kTileKeys));
   return sum;
 }
 

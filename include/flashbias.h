@@ -578,7 +578,8 @@ int fb_cache_bias_prepare(int Hq, int H, int P, int R, const float *phi_q, const
  * with V, to bf16, or to fp16 where an e4m3 cache meets at most 16 query rows of
  * a key/value head (T Hq / H; more rows go through 128-row tiles, where a bias of
  * rank 5 and up also passes fp16 as phi_q / scale and may flag FB_ERR_RANGE from
- * 2^26 on). Bitwise reproducible.
+ * 2^26 on, and where e4m3 keys and values are bf16: exact from 2^-126 on, infinite
+ * beyond that type's range). Bitwise reproducible.
  */
 size_t fb_attn_cache_workspace_bytes(int B, int Hq, int H, int T, int d);
 

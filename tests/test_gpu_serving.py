@@ -753,3 +753,25 @@ def test_non_finite_values_in_a_split_row_tile(kind, T, context, late):
     assert torch.equal(lse, clean[1]) and torch.equal(o[~hit], clean[0][~hit])
     assert (o[hit] == math.inf).all() if kind == "bf16" else o[hit].isnan().all()
     assert _status() == fb.FB_OK
+
+
+@pytest.mark.parametrize("T,context", [(24, 0), (24, 500), (100, 10), (150, 90)])
+def test_values_beyond_bf16_in_the_tiles(T, context):
+    """A finite value that its code and scale carry past bf16's range (3.4e38 is written as 2^128) is infinite in the
+    128-row tiles, for a new token as for one of the context: the rows that see it get it, the others nothing."""
+    c = _case("e4m3", 64, 2, 2, T, 16, [context, 3], None, "none", False, seed=45)
+    clean = _call(c)
+    hot = T - 2
+    row = torch.zeros(2, 2, 1, 64)
+    row[:, :, 0, 11], row[:, :, 0, 12] = 3.4e38, -3.4e38
+    at = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    pool, scale = c["cache"].k.clone(), c["cache"].k_scale.clone()
+    fb.cache_write(c["cache"], row.cuda(), row.cuda(), c["table"].cuda(), at([context + hot, 3 + hot]), at([1, 0]))
+    c["cache"].k.copy_(pool)
+    c["cache"].k_scale.copy_(scale)
+    o, lse = _call(c)
+    assert torch.equal(lse, clean[1])
+    assert (o[0, :, hot:, 11] == math.inf).all() and (o[0, :, hot:, 12] == -math.inf).all()
+    assert torch.equal(o[0, :, :hot], clean[0][0, :, :hot]) and torch.equal(o[1], clean[0][1])
+    assert torch.isfinite(o[0, :, hot:, :11]).all() and torch.isfinite(o[0, :, hot:, 13:]).all()
+    assert _status() == fb.FB_OK
