@@ -322,7 +322,10 @@ __global__ void __launch_bounds__(kWarps * 32, most_ctas(D, E4M3, NB)) attn_cach
       }
       __syncwarp();
     };
-    // Lanes whose d lies past the row read its first bytes instead: the queries are 0 there, and O is not written.
+    // Lanes whose d lies past the row (two of a key row's four, in its last piece) read its first bytes instead: the
+    // queries are 0 there, and O is not written. Key values of 16 bits, which may be infinite, become 0 too; an 8-bit one
+    // is finite or NaN, and NaN is the score in any case.
+    const bool past = !E4M3 && a.d < D && t4 >= 2;
     int kat[L::KW / L::KL], vat[L::VW / L::VL0 + (D == 96 ? 1 : 0)];
 #pragma unroll
     for (int c = 0; c < L::KW / L::KL; ++c) {
@@ -365,6 +368,10 @@ __global__ void __launch_bounds__(kWarps * 32, most_ctas(D, E4M3, NB)) attn_cach
           uint32_t kr[2][L::KL];
 #pragma unroll
           for (int i = 0; i < 2; ++i) read_words<L::KL>(src + (mb * 16 + 8 * i) * rb + kat[c], kr[i]);
+          if (!E4M3 && c == L::KW / L::KL - 1 && past) {
+#pragma unroll
+            for (int w = 0; w < L::KL; ++w) kr[0][w] = kr[1][w] = 0u;
+          }
           // a product takes four values of each row: two words of bf16, or one word of codes
           constexpr int products = E4M3 ? L::KL : L::KL / 2;
 #pragma unroll

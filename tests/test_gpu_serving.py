@@ -775,3 +775,21 @@ def test_values_beyond_bf16_in_the_tiles(T, context):
     assert torch.equal(o[0, :, :hot], clean[0][0, :, :hot]) and torch.equal(o[1], clean[0][1])
     assert torch.isfinite(o[0, :, hot:, :11]).all() and torch.isfinite(o[0, :, hot:, 13:]).all()
     assert _status() == fb.FB_OK
+
+
+@pytest.mark.parametrize("d", [16, 32, 48, 64, 80, 96, 112, 128])
+@pytest.mark.parametrize("T", [1, 5, 24])
+@pytest.mark.parametrize("channel", [0, 3, 7, 12])
+def test_infinite_keys(d, T, channel):
+    """A key whose score is -inf has no weight, whatever the head dim: the result is, to the bit, that of a key whose
+    score is so low that its weight is 0."""
+    c = _case("bf16", d, 2, 2, T, 16, [40], None, "none", False, seed=47)
+    c["q"][..., channel] = c["q"][..., channel].abs() + 0.5
+    at = int(c["table"][0, 1]), slice(None), 5, channel  # context token 21
+    c["cache"].k[at] = -1e38
+    low = _call(c)
+    c["cache"].k[at] = -math.inf
+    got = _call(c)
+    assert torch.isfinite(low[0]).all()
+    assert torch.equal(got[0], low[0]) and torch.equal(got[1], low[1])
+    assert _status() == fb.FB_OK
