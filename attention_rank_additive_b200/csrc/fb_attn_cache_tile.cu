@@ -616,7 +616,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const __gr
                   const float2 l2 = __half22float2(*reinterpret_cast<const __half2 *>(&lw[w]));
                   float x0 = (h2.x + l2.x) * inv, x1 = (h2.y + l2.y) * inv;
                   over |= !(fabsf(x0) <= 65504.f) || !(fabsf(x1) <= 65504.f);
-                  x0 = fminf(fmaxf(x0, -65504.f), 65504.f), x1 = fminf(fmaxf(x1, -65504.f), 65504.f);
+                  if (fabsf(x0) > 65504.f) x0 = copysignf(65504.f, x0);  // NaN stays
+                  if (fabsf(x1) > 65504.f) x1 = copysignf(65504.f, x1);
                   const __half2 hh = __floats2half2_rn(x0, x1);
                   const float2 hf = __half22float2(hh);
                   const __half2 ll = __floats2half2_rn(x0 - hf.x, x1 - hf.y);

@@ -793,3 +793,22 @@ def test_infinite_keys(d, T, channel):
     assert torch.isfinite(low[0]).all()
     assert torch.equal(got[0], low[0]) and torch.equal(got[1], low[1])
     assert _status() == fb.FB_OK
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("T", [1, 16, 17, 40, 150])
+@pytest.mark.parametrize("R", [3, 8, 40])
+def test_nan_factors_reach_their_rows(kind, T, R):
+    """A NaN in a query position's factors makes the rows of that position NaN, whatever kernel their number takes; the
+    other rows keep their results."""
+    c = _case(kind, 64, 2, 2, T, 16, [50], None, f"low{R}", False, seed=49)
+    c["fq"][0, 0, R - 1] = 2 * c["fq"].abs().max()  # the column's size stays when another value becomes NaN
+    clean = _call(c)
+    assert _status() == fb.FB_OK
+    c["fq"][1, 50 + T - 1, R - 1] = math.nan
+    o, lse = _call(c)
+    assert _status() == (fb.FB_OK if R <= 4 else fb.FB_ERR_RANGE)
+    hit = torch.zeros(1, 2, T, dtype=torch.bool, device="cuda")
+    hit[0, 1, T - 1] = True
+    assert o[hit].isnan().all() and lse[hit].isnan().all()
+    assert torch.equal(o[~hit], clean[0][~hit]) and torch.equal(lse[~hit], clean[1][~hit])
