@@ -456,9 +456,8 @@ __global__ void __launch_bounds__(kWarps * 32, most_ctas(D, E4M3, NB)) attn_cach
           }
           skf[i] = svf[mb][i] = 0.f;
           if constexpr (E4M3) {
-            // 2^(byte - 127); byte 255 is NaN, byte 0 (2^-127, which cache_write does not make) counts as 0
             const uint32_t k8 = src[ks_at + mb * 16 + g + 8 * i], v8 = src[vs_at + mb * 16 + g + 8 * i];
-            skf[i] = __uint_as_float(k8 == 255u ? 0x7fffffffu : k8 << 23);
+            skf[i] = scale_value(k8);
             svf[mb][i] = v8 == 255u ? __uint_as_float(0x7fffffffu) : float(int(v8) - 127);
           }
         }

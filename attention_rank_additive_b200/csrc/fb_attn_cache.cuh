@@ -81,7 +81,7 @@ template <bool E4M3, bool AS_BF16>
 __device__ __forceinline__ float odd_value(const uint8_t *row, int at, uint32_t scale) {
   if constexpr (E4M3 && AS_BF16) {
     const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2(row[at], __NV_E4M3);
-    const float v = __bfloat162float(__float2bfloat16_rn(__low2float(__half2(r)) * __uint_as_float(scale << 23)));
+    const float v = __bfloat162float(__float2bfloat16_rn(__low2float(__half2(r)) * scale_value(scale)));
     return fabsf(v) < INFINITY ? 0.f : v;
   } else if constexpr (E4M3) {
     return (row[at] & 0x7fu) == 0x7fu ? __uint_as_float(0x7fffffffu) : 0.f;

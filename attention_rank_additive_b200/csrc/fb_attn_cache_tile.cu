@@ -705,9 +705,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const __gr
           Chunks out;
           out.x = out.y = was;
           if constexpr (E4M3) {
-            // 2^(byte - 127); byte 255 is NaN, byte 0 (2^-127, which cache_write does not make) counts as 0
-            const uint32_t byte = sc[E4M3 ? i : 0];
-            const float f = __uint_as_float(byte == 255u ? 0x7fffffffu : byte << 23);
+            const float f = scale_value(sc[E4M3 ? i : 0]);
             out.x = make_uint4(e4m3_to_bf16(was.x, false, f), e4m3_to_bf16(was.x, true, f),
                                e4m3_to_bf16(was.y, false, f), e4m3_to_bf16(was.y, true, f));
             out.y = make_uint4(e4m3_to_bf16(was.z, false, f), e4m3_to_bf16(was.z, true, f),

@@ -16,7 +16,7 @@
 #include <cuda_fp8.h>
 
 #include "fb_internal.h"
-#include "fb_ptx.cuh"
+#include "fb_ptx_cache.cuh"
 
 namespace fb {
 namespace {
@@ -185,8 +185,7 @@ __device__ __forceinline__ Piece<E4M3> fetch(const void *pool, const uint8_t *sc
 template <bool E4M3>
 __device__ __forceinline__ void expand(const Piece<E4M3> &p, float *x) {
   if constexpr (E4M3) {
-    // 2^(s - 127); s = 0 is 2^-127, a subnormal
-    const float scale = __uint_as_float(p.v.z ? p.v.z << 23 : 0x400000u);
+    const float scale = scale_value(p.v.z);
     const uint32_t v[2] = {p.v.x, p.v.y};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {

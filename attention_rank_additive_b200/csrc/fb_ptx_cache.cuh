@@ -1,10 +1,15 @@
 // fb_ptx_cache.cuh -- PTX wrappers of the cache kernels, beside those of
-// fb_ptx.cuh.
+// fb_ptx.cuh, and the value of a row's scale byte, which all of them share.
 #pragma once
 
 #include "fb_ptx.cuh"
 
 namespace fb {
+
+// 2^(byte - 127): byte 0 is the subnormal 2^-127, byte 255 NaN.
+__device__ __forceinline__ float scale_value(uint32_t byte) {
+  return __uint_as_float(byte == 255u ? 0x7fffffffu : max(byte << 23, 0x400000u));
+}
 
 // True in one lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {

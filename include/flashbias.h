@@ -491,7 +491,8 @@ int fb_rope_frequencies_host(int rot, double base, int scaling, double factor,
  * The paged key/value cache. (No counterpart in the FlashBias paper: the
  * serving form of its language-model case.) Two pools of pages,
  * [num_pages, H, page_size, d] contiguous, bf16 or e4m3; an e4m3 row has a
- * power-of-two scale in one byte (E8M0: 2^(byte - 127)) in [num_pages, H, page_size].
+ * power-of-two scale in one byte (E8M0: 2^(byte - 127), 255 is NaN) in
+ * [num_pages, H, page_size].
  * Token i of sequence b is row i % page_size of page block_table[b][i / page_size].
  *
  *  cache_dt    FB_BF16 or FB_E4M3 (scales may be NULL for FB_BF16).

@@ -812,3 +812,49 @@ def test_nan_factors_reach_their_rows(kind, T, R):
     hit[0, 1, T - 1] = True
     assert o[hit].isnan().all() and lse[hit].isnan().all()
     assert torch.equal(o[~hit], clean[0][~hit]) and torch.equal(lse[~hit], clean[1][~hit])
+
+
+def test_reserved_and_least_scale_bytes_read_back():
+    """Byte 255 is NaN and byte 0 is 2^-127, as the type of the scales says."""
+    cache = _cache(1, 2, 16, 32, "e4m3", 51)
+    cache.k_scale.view(torch.uint8)[0, :, 3] = 255
+    cache.v_scale.view(torch.uint8)[0, :, 4] = 0
+    cache.v_scale.view(torch.uint8)[0, :, 5] = 255
+    cache.v.view(torch.uint8)[0, :, 5] = 0
+    tab = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+    for dtype in (torch.float32, torch.bfloat16):
+        k, v = fb.cache_read(cache, tab, None, None, 16, dtype=dtype)
+        assert k[0, :, 3].isnan().all() and v[0, :, 5].isnan().all()
+        least = ref.e4m3_values(cache.v.view(torch.uint8)[0, :, 4].cpu()) * 2.0 ** -127
+        assert torch.equal(v[0, :, 4].cpu().to(F64), least.to(dtype).to(F64))
+        assert torch.isfinite(k[0, :, [i for i in range(16) if i != 3]]).all()
+        assert torch.isfinite(v[0, :, [i for i in range(16) if i != 5]]).all()
+    assert _status() == fb.FB_OK
+
+
+@pytest.mark.parametrize("T", [1, 6, 24])
+def test_least_scales_of_keys(T):
+    """Keys with the scale 2^-127 against queries near the largest: ordinary scores, in both kernels."""
+    c = _case("e4m3", 64, 2, 2, T, 16, [60], None, "none", False, seed=53)
+    c["q"] = (c["q"].float() * 2.0 ** 121).to(torch.bfloat16)
+    c["cache"].k_scale.view(torch.uint8).zero_()
+    o, lse, to, tl = _want(c)
+    assert float(lse.max()) - math.log(61) > 0.05  # the scores matter
+    # the tiles hold keys as bf16, whose step below 2^-126 is 2^-133: half of it for each value of a key
+    off = 2.0 ** -134 * c["q"].to(F64).abs().sum(-1) / 8 if T > 16 else torch.zeros(1, 2, T, dtype=F64)
+    weight = ref.rows(ref.pool_values(c["cache"].v.cpu(), c["cache"].v_scale.cpu()), c["table"][0], 0, 60 + T).abs().amax()
+    _compare(_call(c), (o, lse, to + 2 * off[..., None] * weight, tl + off))
+
+
+@pytest.mark.parametrize("T", [1, 6, 24])
+def test_scale_byte_of_nan(T):
+    """A key row whose scale is NaN makes the rows that see it NaN."""
+    c = _case("e4m3", 64, 2, 2, T, 16, [20], None, "none", False, seed=55)
+    clean = _call(c)
+    c["cache"].k_scale.view(torch.uint8)[int(c["table"][0, (20 + T - 1) // 16]), 1, (20 + T - 1) % 16] = 255
+    o, lse = _call(c)
+    hit = torch.zeros(1, 2, T, dtype=torch.bool, device="cuda")
+    hit[0, 1, T - 1] = True
+    assert o[hit].isnan().all() and lse[hit].isnan().all()
+    assert torch.equal(o[~hit], clean[0][~hit]) and torch.equal(lse[~hit], clean[1][~hit])
+    assert _status() == fb.FB_OK
