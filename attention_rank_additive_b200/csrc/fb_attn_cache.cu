@@ -612,9 +612,11 @@ __global__ void __launch_bounds__(kWarps * 32, most_ctas(D, E4M3, NB)) attn_cach
               read_words<(VP + 1) / 2>(p, vr[i]);
           }
           // an infinite or NaN value must not reach the rows that do not see its key (0 * inf): where new tokens are
-          // among the keys it leaves the product, and the rows that see it get it back when the segment is joined;
-          // rows behind the last token, and those of no page, are nothing at all
+          // among the step's keys it leaves the product, and the rows that see it get it back when the segment is joined
+          // (a step wholly of the context keeps it: all rows see it); rows behind the last token, and those of no page,
+          // are nothing at all
           if (tail) {
+            const bool fresh = j0 + 16 * KM > s.prefix;
             bool odd = false;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -622,7 +624,7 @@ __global__ void __launch_bounds__(kWarps * 32, most_ctas(D, E4M3, NB)) attn_cach
 #pragma unroll
               for (int w = 0; w < VP; ++w) {
                 if (last && w >= VP / 2) continue;
-                const uint32_t was = real ? vr[i][w] : 0u, even = even_word<E4M3>(was);
+                const uint32_t was = real ? vr[i][w] : 0u, even = fresh ? even_word<E4M3>(was) : was;
                 odd |= even != was;
                 vr[i][w] = even;
               }

@@ -858,3 +858,21 @@ def test_scale_byte_of_nan(T):
     assert o[hit].isnan().all() and lse[hit].isnan().all()
     assert torch.equal(o[~hit], clean[0][~hit]) and torch.equal(lse[~hit], clean[1][~hit])
     assert _status() == fb.FB_OK
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("T", [1, 3, 24])
+def test_values_beside_a_page_that_is_not_there(kind, T):
+    """A page of the context that the table does not lead to is not seen; a non-finite value in the page beside it, which
+    every row sees, stays."""
+    c = _case(kind, 64, 2, 2, T, 16, [60], None, "none", False, seed=57)
+    c["table"][0, 1] = -1
+    clean = _call(c)
+    assert _status() == fb.FB_ERR_RANGE and torch.isfinite(clean[0]).all()
+    _plant(c, kind, 0, 1, 3, 7)
+    o, lse = _call(c)
+    assert _status() == fb.FB_ERR_RANGE
+    hit = torch.zeros_like(o, dtype=torch.bool)
+    hit[0, 1, :, 7] = True
+    assert torch.equal(lse, clean[1]) and torch.equal(o[~hit], clean[0][~hit])
+    assert (o[hit] == math.inf).all() if kind == "bf16" else o[hit].isnan().all()
