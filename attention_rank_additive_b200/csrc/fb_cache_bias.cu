@@ -69,7 +69,8 @@ __global__ void __launch_bounds__(256) bias_split_kernel(int R, int RP, long lon
     const int r = r0 + j;
     if (r >= R) break;
     const unsigned tq = top[r], tk = top[kMaxRank + r];
-    int c = tq && tk ? (exponent(tq) - exponent(tk)) / 2 : 0;
+    // a column that is zero on one side adds nothing: the other side is brought to 1, so that it does not overflow
+    int c = tq && tk ? (exponent(tq) - exponent(tk)) / 2 : (tq ? exponent(tq) : (tk ? -exponent(tk) : 0));
     c = side ? c : -c;
     float v = ldexpf(x[r], c);
     if (!(fabsf(v) <= 65504.f)) {

@@ -876,3 +876,17 @@ def test_values_beside_a_page_that_is_not_there(kind, T):
     hit[0, 1, :, 7] = True
     assert torch.equal(lse, clean[1]) and torch.equal(o[~hit], clean[0][~hit])
     assert (o[hit] == math.inf).all() if kind == "bf16" else o[hit].isnan().all()
+
+
+@pytest.mark.parametrize("T", [1, 24])
+@pytest.mark.parametrize("side", ["fq", "fk"])
+def test_factor_columns_of_zeros(T, side):
+    """A column that is zero on one side adds nothing, however large the other side is, and is no error."""
+    c = _case("bf16", 64, 2, 2, T, 16, [40], None, "low8", False, seed=59)
+    other = "fk" if side == "fq" else "fq"
+    c[side][..., 2] = 0.0
+    want = _want(c)
+    c[other][..., 2] = _randn(c[other].shape[:2], 60) * 1e9
+    got = _call(c)
+    assert _status() == fb.FB_OK
+    _compare(got, want)
