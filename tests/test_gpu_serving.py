@@ -890,3 +890,27 @@ def test_factor_columns_of_zeros(T, side):
     got = _call(c)
     assert _status() == fb.FB_OK
     _compare(got, want)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("first", [0, 123456, 2 ** 24])
+def test_rope_of_pairs_of_very_different_size(dtype, inter, first):
+    """Each pair is turned to its own size: the bound is of its two values (angle, sine, cosine and products within
+    2^-21 of them, one rounding), not of the head's largest."""
+    B, H, N, d, rot = 1, 3, 130, 64, 48
+    r = fb.Rope.scaled(rot, interleaved=inter, factor=1.5)
+    p = torch.arange(rot // 2)
+    ia, ib = (2 * p, 2 * p + 1) if inter else (p, p + rot // 2)
+    size = torch.ones(d)
+    size[ia] = size[ib] = torch.exp2(-40.0 * p / p[-1])
+    x = (_randn((B, H, N, d), 63) * size).to(dtype)
+    pos = (torch.arange(N) + first).to(torch.int32)
+    for call, sign in ((fb.rope, 1.0), (fb.rope_bwd, -1.0)):
+        y, _ = call(x.cuda(), None, r, pos.cuda())
+        want = ref.rope(x, r.frequencies, pos[None], rot, inter, r.factor, sign)
+        big = torch.zeros_like(want)
+        big[..., ia] = big[..., ib] = torch.maximum(x[..., ia].abs(), x[..., ib].abs()).to(F64) * r.factor
+        err = (y.cpu().to(F64) - want).abs()
+        assert (err <= torch.finfo(dtype).eps / 2 * want.abs() + 2.0 ** -21 * 2 * big).all()
+    assert _status() == fb.FB_OK

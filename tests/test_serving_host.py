@@ -210,3 +210,26 @@ def test_turns():
     assert fb.fb_rope_turns_host(len(freq), ctypes.addressof(f), ctypes.addressof(t)) == INVALID
     assert fb.fb_rope_turns_host(0, ctypes.addressof(f), ctypes.addressof(t)) == INVALID
     assert fb.fb_rope_turns_host(2, 0, ctypes.addressof(t)) == INVALID
+
+
+@pytest.mark.parametrize("rot", [8, 64, 128])
+@pytest.mark.parametrize("base", [10000.0, 500000.0])
+@pytest.mark.parametrize("by,trained,fast,slow", [(8.0, 4096.0, 32.0, 1.0), (16.0, 8192.0, 32.0, 1.0), (2.0, 300.0, 5.0, 0.25)])
+def test_yarn_ramp(rot, base, by, trained, fast, slow):
+    """Pair p keeps its frequency as far as it makes `fast` turns over the trained length, is divided by `by` from `slow`
+    turns down, and in between the share kept falls linearly with p, from the whole pair number below the first border to
+    the one above the second (within 0 and rot - 1)."""
+    status, got, _ = _frequencies(rot, base, 3, by, trained, fast, slow)
+    assert status == fb.FB_OK
+
+    def border(turns):  # base^(-2 p / rot) trained / 2 pi = turns
+        return rot / 2 * math.log(trained / (2 * math.pi * turns)) / math.log(base)
+
+    first, last = max(math.floor(border(fast)), 0), min(math.ceil(border(slow)), rot - 1)
+    ramped = 0
+    for p in range(rot // 2):
+        w = base ** (-2.0 * p / rot)
+        share = 1.0 if p <= first else (0.0 if p >= last else (last - p) / (last - first))
+        assert math.isclose(got[p], w * share + w / by * (1.0 - share), rel_tol=2.0 ** -40)
+        ramped += 0.0 < share < 1.0
+    assert first < last and (ramped > 0 or rot == 8)
