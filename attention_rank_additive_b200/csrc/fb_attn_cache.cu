@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(kWarps * 32, most_ctas(D, E4M3, NB)) attn_cach
 
     // ---- queries as the matrix operand: lane (g, t4) holds row g's values at the d that its key loads have. 8-bit keys
     // become fp16, exactly, and the queries too: a power of two is taken out of a row so that its largest value lies in
-    // [2^14, 2^15). Values from 2^-28 of that on are exact, smaller ones off by 2^-40 of it at most.
+    // [2^14, 2^15). Values from 2^-28 of that on are exact, smaller ones off by 2^-39 of it at most.
     uint32_t qf[NB][KS][2];  // bf16 or fp16 pairs
     float mult[NB][2];       // scale, and the power of two taken out of a query row
 #pragma unroll

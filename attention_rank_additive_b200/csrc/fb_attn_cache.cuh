@@ -16,13 +16,9 @@ constexpr float kCacheLog2e = 1.4426950408889634f;
 // 2^e for an integer e, clamped to the normal range.
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float(uint32_t(min(max(e, -126), 127) + 127) << 23); }
 
-// Asynchronous copy of N words (2 or 4) to shared memory.
-template <int N>
-__device__ __forceinline__ void copy_whole(uint32_t dst, const void *src) {
-  if constexpr (N == 4)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(4 * N) : "memory");
+// Asynchronous copy of 8 bytes to shared memory.
+__device__ __forceinline__ void copy8(uint32_t dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copies_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 

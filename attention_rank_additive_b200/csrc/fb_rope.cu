@@ -7,18 +7,23 @@
 // past the first `rot` of a head are copied. The gradient is the same turn by
 // the opposite angle (the transpose of a rotation), times f.
 //
-// Angles: w_p is kept as 64-bit fixed-point turns, t_p = round(2^64 w_p / 2 pi).
-// The low 64 bits of n t_p are then the fraction of a turn that the angle has
-// passed, exact to n 2^-65 turns at any 32-bit position, and its upper 32 bits
-// go through sincospi in fp32: one integer multiply in place of a product and
-// a range reduction in fp64, with an angle good to 2^-24 turns.
+// Angles: w_p is kept as 64-bit fixed-point turns, t_p = 2^64 w_p / 2 pi from a
+// product of doubles, off by 2^-52 of w_p at most. The low 64 bits of n t_p are
+// then the fraction of a turn that the angle has passed, off by n w_p 2^-52 radians
+// (2^-21 at position 2^31 for w = 1), and its upper 32 bits go through sincospi in
+// fp32, which rounds them to 2^-25 turns: one integer multiply in place of a
+// product and a range reduction in fp64.
 //
 // What bounds it: each value is read and written once (HBM) and costs about
 // three operations, while a sine and cosine cost about 40 instructions. So a
 // thread computes the V sine/cosine pairs of one token and walks over several
 // heads with them; V pairs are two 16-byte loads and two 16-byte stores. The two
 // lie half the rotated part apart in either layout (interleaved: V / 2 pairs
-// each), so that neighbouring lanes read neighbouring 16 bytes.
+// each), so that neighbouring lanes read neighbouring 16 bytes. Measured: prompts of
+// 8 x 2048 tokens, 12 + 12 heads of 64, bf16, 21.8 us, 4.6 TB/s. Its 48 registers a
+// thread leave 5 blocks on an SM, so 768 blocks are 1.04 waves: 32 warps an SM, which
+// wait for their loads most of the time (9 of 15 stall cycles an instruction), not
+// HBM's rate, and the last blocks alone.
 #include <cmath>
 
 #include "fb_internal.h"

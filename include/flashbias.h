@@ -436,7 +436,8 @@ int fb_svd_factors_host(const double *bias_host, int N, int R, int oversample,
  * gradients of x from those of y: the turn by the opposite angle, times f.
  *
  *  dt          FB_BF16 or FB_F32 (of q, k and the outputs). Angles, sines and
- *              products are fp32 or better; one rounding at the end.
+ *              products are fp32 or better (the angle at position n is off by
+ *              n w_p 2^-52 beside that); one rounding at the end.
  *  d, rot      head dim (1 to 4096) and rotated part, rot even, 2 <= rot <= d.
  *  turns       [rot / 2] device: fb_rope_turns_host's form of the w_p.
  *  factor      f, finite and not 0.
@@ -468,7 +469,7 @@ int fb_rope_bwd(int dt, int B, int N, int d, int rot, int interleaved,
                 void *stream);
 
 /* turns_host[p] = the fraction of a turn that pair p passes per position, in
- * units of 2^-64 turns (w_p modulo a turn; exact to 2^-53 of w_p). */
+ * units of 2^-64 turns (w_p modulo a turn; off by 2^-52 of w_p at most). */
 int fb_rope_turns_host(int pairs, const double *freq_host, uint64_t *turns_host);
 
 /*
@@ -533,9 +534,9 @@ int fb_cache_read(int dt, int cache_dt, int B, int H, int N, int d,
  * [H, P, R] fp32 device contiguous, over positions 0 .. P - 1 (Hq or H 1: shared
  * by all heads). R <= 4: kept in fp32. 5 <= R <= 128: two fp16 parts (22 bits),
  * each column balanced between q and k by a power of two; a column whose bias
- * passes 2^30 saturates and flags FB_ERR_RANGE. `prepared`: at least
- * fb_cache_bias_bytes(...) bytes, 256-byte aligned, written on `stream`; the
- * factors may be freed or changed once that work has run.
+ * passes 2^30 saturates and flags FB_ERR_RANGE; a NaN stays one and flags it too.
+ * `prepared`: at least fb_cache_bias_bytes(...) bytes, 256-byte aligned, written
+ * on `stream`; the factors may be freed or changed once that work has run.
  */
 size_t fb_cache_bias_bytes(int Hq, int H, int P, int R);
 
@@ -560,6 +561,7 @@ int fb_cache_bias_prepare(int Hq, int H, int P, int R, const float *phi_q, const
  *  cache       as above; d 16 to 128, a multiple of 16.
  *  prefix      [B] int32 device; counts [B] int32 device or NULL (T each).
  *  tree_mask   [B, T, mask_words] device, 32 mask_words >= T, or NULL.
+ *  scale       finite and > 0.
  *  depths      [B, T] int32 device, or NULL.
  *  R, P, heads, prepared_bias   as given to fb_cache_bias_prepare, whose output
  *              this is (the heads 1 or Hq, 1 or H); R = 0: no bias. A position
@@ -578,9 +580,12 @@ int fb_cache_bias_prepare(int Hq, int H, int P, int R, const float *phi_q, const
  * and the softmax are fp32; the probabilities are rounded once for the product
  * with V, to bf16, or to fp16 where an e4m3 cache meets at most 16 query rows of
  * a key/value head (T Hq / H; more rows go through 128-row tiles, where a bias of
- * rank 5 and up also passes fp16 as phi_q / scale and may flag FB_ERR_RANGE from
- * 2^26 on, and where e4m3 keys and values are bf16: exact from 2^-126 on, infinite
- * beyond that type's range). Bitwise reproducible.
+ * rank 5 and up also passes fp16 as phi_q / scale and may saturate and flag
+ * FB_ERR_RANGE from about (65504 scale)^2 on, 2^26 at head dim 64, and where e4m3
+ * keys and values are bf16: exact from 2^-126 on, infinite beyond that type's
+ * range). The fp16 probabilities carry the power of two of their value row; one
+ * below 2^-22 of the query row's largest loses bits, 2^-33 of that largest at most.
+ * Bitwise reproducible.
  */
 size_t fb_attn_cache_workspace_bytes(int B, int Hq, int H, int T, int d);
 
