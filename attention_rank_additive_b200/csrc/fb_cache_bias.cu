@@ -111,7 +111,7 @@ bool sizes_ok(int B, int Hq, int H, int T, int d) {
 }
 
 // Query rows of an item (heads of a group times tokens) above which the 128-row tiles are used: the other kernel holds two
-// blocks of 8 in its registers. With three it took 62 us for 8 trees of 24 rows on contexts up to 2024, 12 heads of 64,
+// blocks of 8 in its registers. With four it took 62 us for 8 trees of 24 rows on contexts up to 2024, 12 heads of 64,
 // rank 64, and the tiles 47.
 constexpr int kTileRows = 16;
 

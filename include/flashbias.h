@@ -573,8 +573,10 @@ int fb_cache_bias_prepare(int Hq, int H, int P, int R, const float *phi_q, const
  *              run at the same time need one each.
  * A row that sees no key, and rows t >= counts[b], give O = 0 and LSE = -inf.
  * Values in cache rows that a query row does not see (infinities and NaN too)
- * do not reach it. Cache rows that the table does not lead to are not seen and
- * flag FB_ERR_RANGE.
+ * do not reach it. One that it sees reaches its channel of O; where its key has
+ * no weight (a score of -inf, or far below the others) that channel is not
+ * specified, the others are as ever. Cache rows that the table does not lead to
+ * are not seen and flag FB_ERR_RANGE.
  * Arithmetic: products of bf16 queries with bf16 or e4m3 keys are exact (few
  * rows of an e4m3 cache: to 2^-39 of the query row's largest value), sums
  * and the softmax are fp32; the probabilities are rounded once for the product

@@ -914,3 +914,29 @@ def test_rope_of_pairs_of_very_different_size(dtype, inter, first):
         err = (y.cpu().to(F64) - want).abs()
         assert (err <= torch.finfo(dtype).eps / 2 * want.abs() + 2.0 ** -21 * 2 * big).all()
     assert _status() == fb.FB_OK
+
+
+@pytest.mark.parametrize("T", [3, 24, 150])
+@pytest.mark.parametrize("by", ["key", "bias"])
+def test_non_finite_values_of_keys_without_weight(T, by):
+    """Infinite values of a context token and a new one whose score is -inf, or shut out by the bias: what 0 times
+    infinity makes of their channels is open, the other channels and the rows that do not see them keep their results."""
+    c = _case("bf16", 64, 1, 1, T, 16, [40], None, "none", False, seed=65)
+    page = lambda i: (int(c["table"][0, i // 16]), 0, i % 16)  # noqa: E731
+    if by == "key":
+        c["q"][..., 2] = c["q"][..., 2].abs() + 0.5
+        for i in (7, 41):
+            c["cache"].k[page(i) + (2,)] = -math.inf
+    else:
+        fk = torch.zeros(1, 48 + T, 1)
+        fk[0, 7] = fk[0, 41] = 1.0
+        c["fq"], c["fk"] = torch.full((1, 48 + T, 1), -1e38), fk
+    clean = _call(c)
+    c["cache"].v[page(7) + (10,)] = math.inf
+    c["cache"].v[page(41) + (20,)] = -math.inf
+    o, lse = _call(c)
+    open_ = torch.zeros_like(o, dtype=torch.bool)
+    open_[..., 10] = True
+    open_[0, 0, 1:, 20] = True
+    assert torch.isfinite(clean[0]).all() and torch.equal(lse, clean[1]) and torch.equal(o[~open_], clean[0][~open_])
+    assert _status() == fb.FB_OK
