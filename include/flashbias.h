@@ -561,11 +561,11 @@ int fb_cache_bias_prepare(int Hq, int H, int P, int R, const float *phi_q, const
  *  cache       as above; d 16 to 128, a multiple of 16.
  *  prefix      [B] int32 device; counts [B] int32 device or NULL (T each).
  *  tree_mask   [B, T, mask_words] device, 32 mask_words >= T, or NULL.
- *  scale       finite and > 0.
  *  depths      [B, T] int32 device, or NULL.
  *  R, P, heads, prepared_bias   as given to fb_cache_bias_prepare, whose output
  *              this is (the heads 1 or Hq, 1 or H); R = 0: no bias. A position
  *              outside 0 .. P - 1 is moved to its end and flags FB_ERR_RANGE.
+ *  scale       finite and > 0.
  *  LSE         [B, Hq, T] fp32 device.
  *  workspace   fb_attn_cache_workspace_bytes(...) bytes, 256-byte aligned, zero
  *              before its first use (every call leaves the counters in it at
